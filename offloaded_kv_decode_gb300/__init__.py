@@ -768,3 +768,11 @@ def clo_hybrid_decode_attn_noalloc(q: torch.Tensor, cbK: Optional[torch.Tensor],
         pq, pcbk, pcbv, pidx, k, C, ppk, ppv, ppid, Np, T, B, Hq, Hkv, d, float(scale),
         pout, plse, perr, ctypes.byref(opts) if opts is not None else None, _stream(stream)),
         "clo_hybrid_decode_attn_noalloc")
+
+
+# ---------------------------------------------------------------- paged KV cache in 4 bits
+
+from .kv4 import (FLAG_NO_ROOM, KV4_BLOCK_SIZE, KV4_GROUPS, clo_kv4_append,  # noqa: E402,F401
+                  clo_kv4_block_bytes, clo_kv4_gather, clo_kv4_paged_decode_attn,
+                  clo_kv4_paged_workspace_size, clo_paged_plan, prepare_kv4_append,
+                  prepare_kv4_gather, prepare_kv4_paged_decode_attn, prepare_paged_plan)
