@@ -14,28 +14,29 @@
 //   * The queries are scaled by a power of two a row so that their largest
 //     element is near 2^13: exact, for bf16 too, but for elements some 2^-27 of
 //     the largest.
-//   * Online softmax with one reference a query row, the running maximum of
-//     x_t + log2(largest V scale of t), x the score in log2 units.  The weights
-//     p_t s_tg that are rounded to fp16 for the second product are then at most
-//     1 and never all small, whatever the V scales are; l = sum p_t stays in
-//     fp32 (p_t < 2^25 as an fp16 scale is at least 2^-24).
+//   * Online softmax with one reference m a query row, p_t = 2^(x_t - m), x the
+//     score in log2 units.  m follows the maximum of x_t + log2(largest V scale
+//     of t), and only when a unit passes it by more than 2^8: the weights
+//     p_t s_tg that are rounded to fp16 for the second product are then below
+//     2^9 and never all small, whatever the V scales are, most units need no
+//     reduction over lanes, and the sums are hardly ever rescaled.  l = sum p_t
+//     stays in fp32 (p_t < 2^33 as an fp16 scale is at least 2^-24).
 //
 // Shape.  mma.sync m16n8k16 with 16 tokens on M and 8 query rows (of the
 // G * n_q of a KV head) on N for the scores, then channels on M for the second
 // product; the operands come out of registers because they are made there (a
 // tcgen05 operand would have to be written back to shared memory in 16 bits,
-// 4 times the bytes that were read).  The kernel is bound by HBM: at 24 bytes a
-// clock and SM the codes need 0.19 of these instructions a clock and n8 tile.
+// 4 times the bytes that were read).
 //
-// Work split.  A tile is the record of one block and KV head (2176 to 2560
-// bytes, K, V and parameters together): one bulk copy.  All tiles of the call
-// form one stream, ordered by request, head and position, cut into equal
-// ranges, one a warp; each warp keeps a ring of records in flight.  A (request,
-// KV head) that lies in one warp's range is finished by that warp alone.  What
-// crosses ranges is merged once a CTA at its end, in shared memory, and what
-// crosses CTAs leaves one fp32 partial a CTA, merged by a second kernel.  The
-// split depends on the lengths alone, so the bits of a result do not depend on
-// timing.
+// Work split.  A unit is 32 tokens of one KV head: the records of two blocks
+// (2176 to 2560 bytes each, K, V and parameters together), a bulk copy each.
+// All units of the call form one stream, ordered by request, head and
+// position, cut into equal ranges, one a warp; each warp keeps a ring of units
+// in flight.  A (request, KV head) that lies in one warp's range is finished by
+// that warp alone.  What crosses ranges is merged once a CTA at its end, and
+// what crosses CTAs leaves one fp32 partial a CTA, merged by a second kernel.
+// The split depends on the lengths alone, so the bits of a result do not
+// depend on timing.
 #include <math.h>
 
 #include <algorithm>
@@ -46,15 +47,19 @@ namespace clo {
 
 constexpr int KV4_WARPS = 4;
 constexpr int KV4_THREADS = KV4_WARPS * 32;
-constexpr int KV4_STAGES = 4;      // records a warp has room for
+constexpr int KV4_UNIT = 2 * KV4_BLOCK;  // tokens of a unit
 constexpr int KV4_MAX_ROWS = 32;   // query rows of a KV head: G * n_q
 constexpr int KV4_PIECE_ROW = KV4_D + 4;  // floats of a row of a piece; the four behind: m, l
 constexpr int KV4_SMEM_PER_SM = 228 * 1024;  // 1 KB of it reserved for each CTA
 constexpr long long KV4_WAIT_CLOCKS = 1ll << 32;  // about 2 s
+constexpr float KV4_SLACK = 8.f;  // how far x + log2(V scale) may pass the reference, log2
 constexpr uint32_t LOW_CODES = 0x000f000fu, HIGH_CODES = 0x00f000f0u;
 
 // CTAs an SM for NT tiles of 8 query rows (registers: 128, 168, 255 a thread).
 __host__ __device__ constexpr int kv4_ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+
+// Units a warp's ring has room for: what fits beside the others' at 4 CTAs an SM.
+__host__ __device__ constexpr int kv4_stages(int ng) { return ng == 4 ? 2 : 3; }
 
 struct Kv4Args {
     const void* q;
@@ -65,6 +70,7 @@ struct Kv4Args {
     const int32_t* ctx_len;
     int32_t* err_flag;
     float* ws_o;    // [2 * CTAs][rows][128] partial sums, head piece and tail piece of each CTA
+    float* ws_first;  // [warps][rows][KV4_PIECE_ROW] piece of the set that ends in a warp but began before it
     float2* ws_ml;  // [2 * CTAs][rows] their (reference, denominator); denominator -1: bad data
     int2* ws_tail;  // [CTAs] (token set, CTAs it covers) of the set that starts in this CTA and goes on, or covers 0
     float scale_log2;
@@ -107,14 +113,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-// Tiles of request r of one KV head; 0 if it is empty or its length is bad.
-__device__ __forceinline__ int kv4_tiles(const Kv4Args& a, int r, bool& bad) {
+// Units of request r of one KV head; 0 if it is empty or its length is bad.
+__device__ __forceinline__ int kv4_units(const Kv4Args& a, int r, bool& bad) {
     const int n = a.ctx_len[r];
     bad = n < 0 || n > a.max_blocks * KV4_BLOCK;
-    return bad ? 0 : (n + KV4_BLOCK - 1) / KV4_BLOCK;
+    return bad ? 0 : (n + KV4_UNIT - 1) / KV4_UNIT;
 }
 
-// prefix[r] = tiles of the requests before r (all heads), r <= B.
+// prefix[r] = units of the requests before r (all heads), r <= B.
 __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* wsum) {
     const int per = (a.B + KV4_THREADS - 1) / KV4_THREADS;
     const int r0 = min(a.B, static_cast<int>(threadIdx.x) * per), r1 = min(a.B, r0 + per);
@@ -122,7 +128,7 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     bool bad, any_bad = false;
     int mine = 0;
     for (int r = r0; r < r1; ++r) {
-        mine += kv4_tiles(a, r, bad) * a.Hkv;
+        mine += kv4_units(a, r, bad) * a.Hkv;
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
@@ -138,13 +144,13 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     for (int w = 0; w < warp; ++w) run += wsum[w];
     if (threadIdx.x == 0) prefix[0] = 0;
     for (int r = r0; r < r1; ++r) {
-        run += kv4_tiles(a, r, bad) * a.Hkv;
+        run += kv4_units(a, r, bad) * a.Hkv;
         prefix[r + 1] = run;
     }
     __syncthreads();
 }
 
-// A position in the stream of tiles: tile j of nt of request r's head h.
+// A position in the stream: unit j of nt of request r's head h.
 struct Place {
     int r, h, j, nt;
 };
@@ -163,7 +169,7 @@ __device__ __forceinline__ Place kv4_place(const int* prefix, int B, int Hkv, in
     return p;
 }
 
-// The next tile's place (one past the last tile: r == B, nt == 0).
+// The next unit's place (one past the last: r == B, nt == 0).
 __device__ __forceinline__ void kv4_next(const int* prefix, int B, int Hkv, Place& p) {
     if (++p.j < p.nt) return;
     p.j = 0;
@@ -175,19 +181,39 @@ __device__ __forceinline__ void kv4_next(const int* prefix, int B, int Hkv, Plac
     p.nt = p.r < B ? (prefix[p.r + 1] - prefix[p.r]) / Hkv : 0;
 }
 
-// The queries of one KV head in the layout of the first product's B operand,
-// and what their scores need in fp32.
+// The queries of one KV head: the B operand of the first product, and what
+// the scores need in fp32.  One n8 tile is kept in registers, more in the
+// warp's shared memory.
 template <int NT, int NG>
 struct Queries {
-    uint32_t b[NT][4][2][2];  // [n8 tile][word j][low, high codes][register]
-    float unit[NT][2];        // fp32 factor of the code sums, columns 2c and 2c + 1
-    float sum[NT][2][NG];     // sum of the group's elements (log2 units)
-    int limit[NT][2];         // tokens behind the last one that the column does not see
+    static constexpr bool kShared = NT > 1;
+    // Shared: [NT][4][32] operands, then [NT * 8] units and [NG][NT * 8] sums.
+    static constexpr int kBytes = kShared ? NT * (4 * 32 * 16 + 8 * 4 * (1 + NG)) : 0;
+    uint4 reg[kShared ? 1 : 4];   // word j: low codes' two registers, high codes' two
+    float2 reg_unit;              // fp32 factor of the code sums, columns 2c and 2c + 1
+    float2 reg_sum[kShared ? 1 : NG];  // sum of the group's elements (log2 units)
+    uint4* sm;
+
+    __device__ __forceinline__ float* sm_units() const { return reinterpret_cast<float*>(sm + NT * 4 * 32); }
+    __device__ __forceinline__ uint4 operand(int nt, int j, int lane) const {
+        if constexpr (kShared) return sm[(nt * 4 + j) * 32 + lane];
+        else return reg[j];
+    }
+    __device__ __forceinline__ float2 unit(int nt, int c) const {
+        if constexpr (kShared) return *reinterpret_cast<const float2*>(sm_units() + nt * 8 + 2 * c);
+        else return reg_unit;
+    }
+    __device__ __forceinline__ float2 sum(int nt, int g, int c) const {
+        if constexpr (kShared)
+            return *reinterpret_cast<const float2*>(sm_units() + (1 + g) * NT * 8 + nt * 8 + 2 * c);
+        else return reg_sum[g];
+    }
 };
 
 template <bool BF16, int NT, int NG>
 __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, int lane, Queries<NT, NG>& qs) {
     const int head = lane >> 2, c = lane & 3;
+    if (Queries<NT, NG>::kShared) __syncwarp();  // the last set's are no longer read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int row = nt * 8 + head;
@@ -196,19 +222,18 @@ __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, i
         const size_t at = (static_cast<size_t>(p.r) * a.n_q + qi) * a.Hq + static_cast<size_t>(p.h) * a.G + g;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at * KV4_D * 2);
         // This lane's channels: 32j + 8c .. + 7 for j = 0 .. 3.
-        float x[4][8];
+        uint4 raw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw[j] = has ? __ldg(src + 4 * j + c) : make_uint4(0u, 0u, 0u, 0u);
         float top = 0.f;
         float part[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint4 v = has ? __ldg(src + 4 * j + c) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
             part[j] = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float2 f = kv4_unpack2<BF16>(w[k]);
-                x[j][2 * k] = f.x;
-                x[j][2 * k + 1] = f.y;
                 top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                 part[j] += f.x + f.y;
             }
@@ -219,40 +244,47 @@ __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, i
         // that 2^e and the factor that undoes it are finite.
         int e = top > 0.f && top < INFINITY ? 12 - ilogbf(top) : 0;
         e = min(max(e, -100), 100);
-        const float up = ldexpf(1.f, e);
+        const float up = ldexpf(1.f, e), up16 = ldexpf(1.f, e - 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float* y = x[j];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= up;
-            qs.b[nt][j][0][0] = pack_half2(y[0], y[4]);
-            qs.b[nt][j][0][1] = pack_half2(y[2], y[6]);
-            qs.b[nt][j][1][0] = pack_half2(y[1] * 0.0625f, y[5] * 0.0625f);
-            qs.b[nt][j][1][1] = pack_half2(y[3] * 0.0625f, y[7] * 0.0625f);
+            const float2 f0 = kv4_unpack2<BF16>(raw[j].x), f1 = kv4_unpack2<BF16>(raw[j].y);
+            const float2 f2 = kv4_unpack2<BF16>(raw[j].z), f3 = kv4_unpack2<BF16>(raw[j].w);
+            uint4 o;
+            o.x = pack_half2(f0.x * up, f2.x * up);      // channels 0, 4
+            o.y = pack_half2(f1.x * up, f3.x * up);      // 2, 6
+            o.z = pack_half2(f0.y * up16, f2.y * up16);  // 1, 5
+            o.w = pack_half2(f1.y * up16, f3.y * up16);  // 3, 7
+            if constexpr (Queries<NT, NG>::kShared) qs.sm[(nt * 4 + j) * 32 + lane] = o;
+            else qs.reg[j] = o;
         }
         const float unit = ldexpf(a.scale_log2, 24 - e);
+        float group[NG];
+#pragma unroll
+        for (int g2 = 0; g2 < NG; ++g2) group[g2] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             part[j] *= a.scale_log2;
             part[j] += __shfl_xor_sync(FULL_MASK, part[j], 1);
             part[j] += __shfl_xor_sync(FULL_MASK, part[j], 2);
+            group[j * NG / 4] += part[j];
         }
-        float group[NG];
+        if constexpr (Queries<NT, NG>::kShared) {
+            if (c == 0) {
+                float* u = qs.sm_units() + nt * 8 + head;
+                u[0] = unit;
 #pragma unroll
-        for (int g2 = 0; g2 < NG; ++g2) {
-            group[g2] = 0.f;
+                for (int g2 = 0; g2 < NG; ++g2) u[(1 + g2) * NT * 8] = group[g2];
+            }
+        } else {
+            const int from = 8 * c;  // a lane of column 2c; column 2c + 1's is 4 further
+            qs.reg_unit = make_float2(__shfl_sync(FULL_MASK, unit, from), __shfl_sync(FULL_MASK, unit, from + 4));
 #pragma unroll
-            for (int j = 0; j < 4 / NG; ++j) group[g2] += part[g2 * (4 / NG) + j];
-        }
-#pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            const int from = (2 * c + col) * 4;
-            qs.unit[nt][col] = __shfl_sync(FULL_MASK, unit, from);
-#pragma unroll
-            for (int g2 = 0; g2 < NG; ++g2) qs.sum[nt][col][g2] = __shfl_sync(FULL_MASK, group[g2], from);
-            qs.limit[nt][col] = a.n_q - 1 - min(nt * 8 + 2 * c + col, a.rows - 1) / a.G;
+            for (int g2 = 0; g2 < NG; ++g2)
+                qs.reg_sum[g2] = make_float2(__shfl_sync(FULL_MASK, group[g2], from),
+                                             __shfl_sync(FULL_MASK, group[g2], from + 4));
         }
     }
+    if (Queries<NT, NG>::kShared) __syncwarp();
 }
 
 // One warp's running softmax of a token set.
@@ -270,7 +302,7 @@ __device__ __forceinline__ void reset(Softmax<NT, NG>& w) {
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int col = 0; col < 2; ++col) {
-            w.m[nt][col] = -INFINITY;
+            w.m[nt][col] = 0.f;
             w.l[nt][col] = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) w.z[nt][col][g] = 0.f;
@@ -284,166 +316,190 @@ __device__ __forceinline__ void reset(Softmax<NT, NG>& w) {
     }
 }
 
-// Takes one record in.  EDGE: it holds tokens that some query does not see;
-// `left` counts the tokens from its first one on.
+// 2^x and log2(x) in one instruction each; neither sees a subnormal that
+// matters (weights below 2^-126, V scales below 2^-24).
+__device__ __forceinline__ float kv4_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float kv4_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ __half2 kv4_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+
+// Takes a unit in: two records.  Rows are tokens gid and gid + 8 of record 0,
+// then of record 1; columns query rows 2c and 2c + 1 of each n8 tile.
+// first: nothing has been taken in yet.  EDGE: the unit holds tokens that some
+// query does not see; `left` counts the tokens from its first one on.
 template <int NT, int NG, bool EDGE>
-__device__ __forceinline__ void take_tile(const uint8_t* rec, int left, const Queries<NT, NG>& qs,
-                                          Softmax<NT, NG>& w, int lane) {
+__device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool first, const Kv4Args& a,
+                                          const Queries<NT, NG>& qs, Softmax<NT, NG>& w, int lane) {
+    constexpr int R = kv4_record(NG);
     const int gid = lane >> 2, c = lane & 3;
-    // ---- scores of tokens gid and gid + 8 (rows), query rows 2c and 2c + 1 of each n8 tile
-    const uint4 k0 = *reinterpret_cast<const uint4*>(rec + gid * KV4_ROW + c * 16);
-    const uint4 k1 = *reinterpret_cast<const uint4*>(rec + (gid + 8) * KV4_ROW + c * 16);
-    const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
-    float2 kp[2][NG], vp[2][NG];  // (scale, zero) of both tokens
+    // Tokens behind the last one that a column does not see.
+    auto limit = [&](int nt, int col) { return a.n_q - 1 - min(nt * 8 + 2 * c + col, a.rows - 1) / a.G; };
+    auto sees = [&](int nt, int row, int col) { return !EDGE || gid + 8 * row < left - limit(nt, col); };
+
+    // ---- scores in log2 units, relative to the reference, and the V parameters
+    float x[NT][2][4];    // [n8 tile][record][row of the record, column]
+    uint32_t vp[4][NG];   // (scale, zero) of the four rows, as they are stored
+    float big[4];         // log2 of the largest V scale
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const uint32_t* par = reinterpret_cast<const uint32_t*>(rec + kv4_param(gid + 8 * t, 0, NG, 0));
-        uint32_t raw[2 * NG];
-        if constexpr (NG == 1) {
-            const uint2 u = *reinterpret_cast<const uint2*>(par);
-            raw[0] = u.x, raw[1] = u.y;
-        } else {
+    for (int b = 0; b < 2; ++b) {
+        const uint4 k0 = *reinterpret_cast<const uint4*>(rec + b * R + gid * KV4_ROW + c * 16);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(rec + b * R + (gid + 8) * KV4_ROW + c * 16);
+        const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+        uint32_t kp[2][NG];
 #pragma unroll
-            for (int k = 0; k < NG / 2; ++k) {
-                const uint4 u = reinterpret_cast<const uint4*>(par)[k];
-                raw[4 * k] = u.x, raw[4 * k + 1] = u.y, raw[4 * k + 2] = u.z, raw[4 * k + 3] = u.w;
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t* par = rec + b * R + kv4_param(gid + 8 * t, 0, NG, 0);
+            uint32_t raw[2 * NG];
+            if constexpr (NG == 1) {
+                const uint2 u = *reinterpret_cast<const uint2*>(par);
+                raw[0] = u.x, raw[1] = u.y;
+            } else {
+#pragma unroll
+                for (int k = 0; k < NG / 2; ++k) {
+                    const uint4 u = reinterpret_cast<const uint4*>(par)[k];
+                    raw[4 * k] = u.x, raw[4 * k + 1] = u.y, raw[4 * k + 2] = u.z, raw[4 * k + 3] = u.w;
+                }
             }
+            // What lies behind the last token may be anything, NaN among it.
+            const bool there = !EDGE || gid + 8 * (2 * b + t) < left;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                kp[t][g] = there ? raw[g] : 0u;
+                vp[2 * b + t][g] = there ? raw[NG + g] : 0u;
+            }
+            __half2 most = kv4_half2(vp[2 * b + t][0]);
+#pragma unroll
+            for (int g = 1; g < NG; ++g) most = __hmax2(most, kv4_half2(vp[2 * b + t][g]));
+            big[2 * b + t] = fmaxf(kv4_log2(__low2float(most)), -24.f);
         }
-        // What lies behind the last token may be anything, NaN among it.
-        const bool there = !EDGE || gid + 8 * t < left;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const uint32_t rk = there ? raw[g] : 0u, rv = there ? raw[NG + g] : 0u;
-            kp[t][g] = __half22float2(*reinterpret_cast<const __half2*>(&rk));
-            vp[t][g] = __half22float2(*reinterpret_cast<const __half2*>(&rv));
-        }
-    }
-    float x[NT][4];
+            float s[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[nt][k] = 0.f;
+                for (int k = 0; k < 4; ++k) s[nt][k] = 0.f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        float s[NT][4];
+            for (int jj = 0; jj < 4 / NG; ++jj) {
+                const int j = g * (4 / NG) + jj;
+                const uint32_t lo[4] = {kw0[j] & LOW_CODES, kw1[j] & LOW_CODES, (kw0[j] >> 8) & LOW_CODES,
+                                        (kw1[j] >> 8) & LOW_CODES};
+                const uint32_t hi[4] = {kw0[j] & HIGH_CODES, kw1[j] & HIGH_CODES, (kw0[j] >> 8) & HIGH_CODES,
+                                        (kw1[j] >> 8) & HIGH_CODES};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[nt][k] = 0.f;
-#pragma unroll
-        for (int jj = 0; jj < 4 / NG; ++jj) {
-            const int j = g * (4 / NG) + jj;
-            const uint32_t lo[4] = {kw0[j] & LOW_CODES, kw1[j] & LOW_CODES, (kw0[j] >> 8) & LOW_CODES,
-                                    (kw1[j] >> 8) & LOW_CODES};
-            const uint32_t hi[4] = {kw0[j] & HIGH_CODES, kw1[j] & HIGH_CODES, (kw0[j] >> 8) & HIGH_CODES,
-                                    (kw1[j] >> 8) & HIGH_CODES};
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 q = qs.operand(nt, j, lane);
+                    mma_16816(s[nt], lo, q.x, q.y);
+                    mma_16816(s[nt], hi, q.z, q.w);
+                }
+            }
+            const float2 f[2] = {__half22float2(kv4_half2(kp[0][g])), __half22float2(kv4_half2(kp[1][g]))};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(s[nt], lo, qs.b[nt][j][0][0], qs.b[nt][j][0][1]);
-                mma_16816(s[nt], hi, qs.b[nt][j][1][0], qs.b[nt][j][1][1]);
+                const float2 unit = qs.unit(nt, c), sum = qs.sum(nt, g, c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 sz = f[k >> 1];
+                    const float before = g == 0 ? -w.m[nt][k & 1] : x[nt][b][k];
+                    x[nt][b][k] = fmaf(sz.x * ((k & 1) ? unit.y : unit.x), s[nt][k],
+                                       fmaf(sz.y, (k & 1) ? sum.y : sum.x, before));
+                }
             }
         }
+    }
+    bool hot = first;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float over = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int col = 0; col < 2; ++col) {
+                float& v = x[nt][t >> 1][2 * (t & 1) + col];
+                if (EDGE && !sees(nt, t, col)) v = -INFINITY;
+                over = fmaxf(over, v + big[t]);
+            }
+        hot |= over > KV4_SLACK;
+    }
+    if (__any_sync(FULL_MASK, hot)) {  // the reference moves
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[nt][k] = fmaf(kp[k >> 1][g].x, s[nt][k], x[nt][k]);
+            for (int col = 0; col < 2; ++col) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) top = fmaxf(top, x[nt][t >> 1][2 * (t & 1) + col] + big[t]);
+#pragma unroll
+                for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
+                // At the first unit to its maximum (0 where a column sees nothing), later only up.
+                const float by = first ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
+                const float al = first ? 0.f : kv4_exp2(-by);
+                w.m[nt][col] += by;
+                w.l[nt][col] *= al;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) w.z[nt][col][g] *= al;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                    for (int hl = 0; hl < 2; ++hl) {
+                        w.o[nt][ch][hl][col] *= al;
+                        w.o[nt][ch][hl][2 + col] *= al;
+                    }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) x[nt][t >> 1][2 * (t & 1) + col] -= by;
+            }
     }
-    float big[2];  // log2 of the largest V scale of each token
+
+    // ---- weights, and their product with V a record and a group at a time
+    const int tok = lane & 15, half = lane >> 4;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        float v = vp[t][0].x;
-#pragma unroll
-        for (int g = 1; g < NG; ++g) v = fmaxf(v, vp[t][g].x);
-        big[t] = fmaxf(__log2f(v), -24.f);
-    }
-    float p[NT][4];
-    bool moved = false;
-    float al[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int t = k >> 1, col = k & 1;
-            float y = x[nt][k] * qs.unit[nt][col];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) y = fmaf(kp[t][g].y, qs.sum[nt][col][g], y);
-            if (EDGE && gid + 8 * t >= left - qs.limit[nt][col]) y = -INFINITY;
-            x[nt][k] = y;
-            top[col] = fmaxf(top[col], y + big[t]);
-        }
-#pragma unroll
-        for (int off = 4; off <= 16; off <<= 1) {
-            top[0] = fmaxf(top[0], __shfl_xor_sync(FULL_MASK, top[0], off));
-            top[1] = fmaxf(top[1], __shfl_xor_sync(FULL_MASK, top[1], off));
-        }
-#pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            const float mn = fmaxf(w.m[nt][col], top[col]);
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            al[nt][col] = fast_exp2(w.m[nt][col] - ref);
-            moved |= al[nt][col] != 1.f;
-            w.m[nt][col] = mn;
-            p[nt][col] = fast_exp2(x[nt][col] - ref);
-            p[nt][2 + col] = fast_exp2(x[nt][2 + col] - ref);
-        }
-    }
-    if (__any_sync(FULL_MASK, moved)) {
+    for (int b = 0; b < 2; ++b) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int col = 0; col < 2; ++col) {
-                w.l[nt][col] *= al[nt][col];
-#pragma unroll
-                for (int g = 0; g < NG; ++g) w.z[nt][col][g] *= al[nt][col];
-            }
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                for (int hl = 0; hl < 2; ++hl)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w.o[nt][ch][hl][k] *= al[nt][k & 1];
+            for (int k = 0; k < 4; ++k) x[nt][b][k] = kv4_exp2(x[nt][b][k]);
+            w.l[nt][0] += x[nt][b][0] + x[nt][b][2];
+            w.l[nt][1] += x[nt][b][1] + x[nt][b][3];
         }
-    }
-    // ---- weights in the layout of the second product's B operand, a group each
-    uint32_t pb[NT][NG][2];
+        const uint32_t vbase = smem_u32(rec) + b * R + KV4_CODES + tok * KV4_ROW;
+        uint32_t v[4];     // chunk 2cp: tokens 0-7, 8-15; chunk 2cp + 1: the same
+        uint32_t pb[NT][2];  // the second product's B operand
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+        for (int ch = 0; ch < 4; ++ch) {  // channels 32 ch + 4 gid + 0..3
+            if (ch % (4 / NG) == 0) {
+                const int g = ch * NG / 4;
+                const float2 f[2] = {__half22float2(kv4_half2(vp[2 * b][g])), __half22float2(kv4_half2(vp[2 * b + 1][g]))};
 #pragma unroll
-        for (int col = 0; col < 2; ++col) w.l[nt][col] += p[nt][col] + p[nt][2 + col];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float y[4];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = k >> 1, col = k & 1;
-                // A query that does not see a token takes nothing from it, not even a NaN.
-                const bool sees = !EDGE || gid + 8 * t < left - qs.limit[nt][col];
-                y[k] = sees ? p[nt][k] * vp[t][g].x : 0.f;
-                w.z[nt][col][g] += sees ? p[nt][k] * vp[t][g].y : 0.f;
+                    for (int k = 0; k < 4; ++k) {
+                        // A query that does not see a token takes nothing from it, not even a NaN.
+                        const bool in = sees(nt, 2 * b + (k >> 1), k & 1);
+                        float& z = w.z[nt][k & 1][g];
+                        y[k] = in ? x[nt][b][k] * f[k >> 1].x : 0.f;
+                        z = in ? fmaf(x[nt][b][k], f[k >> 1].y, z) : z;
+                    }
+                    pb[nt][0] = movmatrix_trans(pack_half2(y[0], y[1]));  // tokens 0-7
+                    pb[nt][1] = movmatrix_trans(pack_half2(y[2], y[3]));  // tokens 8-15
+                }
             }
-            pb[nt][g][0] = movmatrix_trans(pack_half2(y[0], y[1]));  // tokens 0-7
-            pb[nt][g][1] = movmatrix_trans(pack_half2(y[2], y[3]));  // tokens 8-15
-        }
-    }
-    // ---- second product: channels 32 ch + 4 gid + 0..3 of chunk ch
-    const int tok = lane & 15, half = lane >> 4;
-    const uint32_t vbase = smem_u32(rec) + KV4_CODES + tok * KV4_ROW;
-#pragma unroll
-    for (int cp = 0; cp < 2; ++cp) {
-        uint32_t v[4];  // chunk 2cp: tokens 0-7, 8-15; chunk 2cp + 1: the same
-        ldmatrix_x4_trans(v, vbase + (((2 * cp + half) ^ ((tok >> 1) & 3)) << 4));
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int ch = 2 * cp + k, g = ch * NG / 4;
-            const uint32_t a0 = v[2 * k], a1 = v[2 * k + 1];
+            if ((ch & 1) == 0) ldmatrix_x4_trans(v, vbase + (((ch + half) ^ ((tok >> 1) & 3)) << 4));
+            const uint32_t a0 = v[2 * (ch & 1)], a1 = v[2 * (ch & 1) + 1];
             const uint32_t lo[4] = {a0 & LOW_CODES, (a0 >> 8) & LOW_CODES, a1 & LOW_CODES, (a1 >> 8) & LOW_CODES};
-            const uint32_t hi[4] = {a0 & HIGH_CODES, (a0 >> 8) & HIGH_CODES, a1 & HIGH_CODES,
-                                    (a1 >> 8) & HIGH_CODES};
+            const uint32_t hi[4] = {a0 & HIGH_CODES, (a0 >> 8) & HIGH_CODES, a1 & HIGH_CODES, (a1 >> 8) & HIGH_CODES};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(w.o[nt][ch][0], lo, pb[nt][g][0], pb[nt][g][1]);
-                mma_16816(w.o[nt][ch][1], hi, pb[nt][g][0], pb[nt][g][1]);
+                mma_16816(w.o[nt][ch][0], lo, pb[nt][0], pb[nt][1]);
+                mma_16816(w.o[nt][ch][1], hi, pb[nt][0], pb[nt][1]);
             }
         }
     }
@@ -491,7 +547,7 @@ __device__ __forceinline__ void end_set(const Kv4Args& a, const Softmax<NT, NG>&
             }
             const int row = nt * 8 + 2 * c + col;
             if (row >= a.rows) continue;
-            const float m = w.m[nt][col];
+            const float m = l == 0.f ? -INFINITY : w.m[nt][col];  // a query that saw nothing
             const bool none = bad || l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
             const size_t orow = piece == nullptr ? kv4_out_row(a, r, h, row) : 0;
@@ -519,17 +575,18 @@ __device__ __forceinline__ void end_set(const Kv4Args& a, const Softmax<NT, NG>&
 
 // Shared memory of a CTA, in bytes from its start.
 struct Kv4Layout {
-    int ring, piece, bars, prefix, total;  // ring and piece: bytes a warp
+    int ring, warp, bars, prefix, total;  // ring, warp: bytes of a warp's ring, and with its queries
 };
 
-__host__ __device__ inline Kv4Layout kv4_layout(int ng, int rows, int B) {
+__host__ __device__ inline Kv4Layout kv4_layout(int nt, int ng, int rows, int B) {
     Kv4Layout y;
+    y.ring = kv4_stages(ng) * 2 * kv4_record(ng);
+    const int queries = nt > 1 ? nt * (4 * 32 * 16 + 8 * 4 * (1 + ng)) : 0;
     const int piece = rows * KV4_PIECE_ROW * static_cast<int>(sizeof(float));
-    const int ring = KV4_STAGES * kv4_record(ng);
-    y.ring = ((ring > piece ? ring : piece) + 127) / 128 * 128;  // the last piece takes the ring's place
-    y.piece = (piece + 15) / 16 * 16;
-    y.bars = KV4_WARPS * (y.ring + y.piece);
-    y.prefix = y.bars + KV4_WARPS * KV4_STAGES * 8;
+    const int both = y.ring + queries;
+    y.warp = ((both > piece ? both : piece) + 127) / 128 * 128;  // the last piece takes their place
+    y.bars = KV4_WARPS * y.warp;
+    y.prefix = y.bars + KV4_WARPS * kv4_stages(ng) * 8;
     y.total = y.prefix + (B + 1) * static_cast<int>(sizeof(int));
     return y;
 }
@@ -539,15 +596,14 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int wsum[KV4_WARPS];
     __shared__ int piece_set[2 * KV4_WARPS];  // token set of each warp's first and last piece, or -1
-    constexpr int R = kv4_record(NG);
-    const Kv4Layout y = kv4_layout(NG, a.rows, a.B);
+    constexpr int R = kv4_record(NG), STAGES = kv4_stages(NG);
+    const Kv4Layout y = kv4_layout(NT, NG, a.rows, a.B);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* ring = smem + warp * y.ring;
-    float* first_piece = reinterpret_cast<float*>(smem + KV4_WARPS * y.ring + warp * y.piece);
-    const uint32_t bars = smem_u32(smem + y.bars) + warp * KV4_STAGES * 8;
+    uint8_t* ring = smem + warp * y.warp;
+    const uint32_t bars = smem_u32(smem + y.bars) + warp * STAGES * 8;
     int* prefix = reinterpret_cast<int*>(smem + y.prefix);
 
-    if (lane < KV4_STAGES) mbar_init(bars + lane * 8);
+    if (lane < STAGES) mbar_init(bars + lane * 8);
     if (lane < 2) piece_set[2 * warp + lane] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     pdl_wait();
@@ -564,109 +620,106 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             for (int i = threadIdx.x; i < a.n_q * a.Hq; i += KV4_THREADS) a.lse[row0 + i] = -INFINITY;
     }
 
-    // Warp g of W takes tiles [N g / W, N (g + 1) / W).
+    // Warp g of W takes units [N g / W, N (g + 1) / W).
     const long long N = prefix[a.B];
     const long long W = min(static_cast<long long>(gridDim.x) * KV4_WARPS, N);
     const long long g0 = static_cast<long long>(blockIdx.x) * KV4_WARPS;
     const long long g = g0 + warp;
     const int t0 = g < W ? static_cast<int>(N * g / W) : 0;
     const int t1 = g < W ? static_cast<int>(N * (g + 1) / W) : 0;
+    float* first_piece = a.ws_first + static_cast<size_t>(g) * a.rows * KV4_PIECE_ROW;
     if (t0 < t1) {
         const uint64_t policy = l2_evict_first_policy();
         Place pl = kv4_place(prefix, a.B, a.Hkv, t0), ps = pl;  // loading, computing
         // Block ids: lane i holds entry `base` + i of the loading request's
         // row, and the 32 after them.
-        int base = 0, ids = 0, ids_next = 0;
+        int base = 0, blocks = 0, ids = 0, ids_next = 0;
         auto load_ids = [&](int at) {
-            return at + lane < pl.nt ? __ldg(a.table + static_cast<size_t>(pl.r) * a.max_blocks + at + lane) : 0;
+            return at + lane < blocks ? __ldg(a.table + static_cast<size_t>(pl.r) * a.max_blocks + at + lane) : 0;
         };
         auto start_ids = [&]() {
-            base = pl.j;
+            blocks = (__ldg(a.ctx_len + pl.r) + KV4_BLOCK - 1) / KV4_BLOCK;
+            base = 2 * pl.j;
             ids = load_ids(base);
             ids_next = load_ids(base + 32);
         };
         start_ids();
-        uint32_t bad_slots = 0;  // stages whose record does not exist
+        uint32_t bad_slots = 0;  // stages with a record that does not exist
         auto issue = [&](int stage) {
-            if (pl.j - base == 32) {
+            if (2 * pl.j - base == 32) {
                 base += 32;
                 ids = ids_next;
                 ids_next = load_ids(base + 32);
             }
-            const int id = __shfl_sync(FULL_MASK, ids, pl.j - base);
-            const bool ok = id >= 0 && id < a.num_blocks;
-            bad_slots = ok ? bad_slots & ~(1u << stage) : bad_slots | (1u << stage);
+            // Lanes 0 and 1 take the unit's two blocks; the second may be behind the last one.
+            const int entry = 2 * pl.j + (lane & 1);
+            const int id = __shfl_sync(FULL_MASK, ids, entry - base);
+            const bool exists = entry < blocks, ok = exists && id >= 0 && id < a.num_blocks;
+            const unsigned have = __ballot_sync(FULL_MASK, ok) & 3u;
+            const bool bad = __any_sync(FULL_MASK, exists && !ok);
+            bad_slots = bad ? bad_slots | (1u << stage) : bad_slots & ~(1u << stage);
+            const uint32_t bar = bars + stage * 8;
             if (lane == 0) {
-                const uint32_t bar = bars + stage * 8;
-                if (ok) {
-                    mbar_expect(bar, R);
-                    bulk_load(smem_u32(ring) + stage * R,
-                              a.pool + (static_cast<size_t>(id) * a.Hkv + pl.h) * R, R, bar, policy);
-                } else {
-                    mbar_arrive(bar);
-                }
+                if (have != 0u) mbar_expect(bar, have == 3u ? 2 * R : R);
+                else mbar_arrive(bar);
             }
-            const int r_before = pl.r, h_before = pl.h;
-            kv4_next(prefix, a.B, a.Hkv, pl);
-            if (pl.r != r_before) {
+            __syncwarp();
+            if (lane < 2 && ok)
+                bulk_load(smem_u32(ring) + (2 * stage + lane) * R,
+                          a.pool + (static_cast<size_t>(id) * a.Hkv + pl.h) * R, R, bar, policy);
+            if (++pl.j == pl.nt) {
+                --pl.j;
+                kv4_next(prefix, a.B, a.Hkv, pl);
                 if (pl.r < a.B) start_ids();
-            } else if (pl.h != h_before) {
-                start_ids();
             }
         };
         int issued = t0;
-        for (; issued < t1 && issued - t0 < KV4_STAGES; ++issued) issue(issued - t0);
+        for (; issued < t1 && issued - t0 < STAGES; ++issued) issue(issued - t0);
 
         Queries<NT, NG> qs;
+        qs.sm = reinterpret_cast<uint4*>(ring + y.ring);
         Softmax<NT, NG> w;
-        bool bad = false, fresh = true;
-        int set_start = t0;  // first tile of the current set in this range
-        int n_tok = 0;
         int stage = 0;
         uint32_t parity = 0;
-        for (int t = t0; t < t1; ++t) {
-            if (fresh) {
-                n_tok = __ldg(a.ctx_len + ps.r);
-                load_queries<BF16, NT, NG>(a, ps, lane, qs);
-                reset(w);
-                bad = false;
-                fresh = false;
-                set_start = t;
+        for (int t = t0; t < t1;) {  // a token set, or the part of it in this range
+            const int n_tok = __ldg(a.ctx_len + ps.r);
+            load_queries<BF16, NT, NG>(a, ps, lane, qs);
+            reset(w);
+            bool bad = false;
+            const int j0 = ps.j, j1 = min(ps.nt, j0 + t1 - t);
+            for (int j = j0; j < j1; ++j) {
+                const bool came = mbar_wait(bars + stage * 8, parity);
+                if (came && ((bad_slots >> stage) & 1u) == 0u) {
+                    const uint8_t* rec = ring + 2 * stage * R;
+                    const int left = n_tok - j * KV4_UNIT;
+                    if (left >= KV4_UNIT + a.n_q - 1)
+                        take_unit<NT, NG, false>(rec, left, j == j0, a, qs, w, lane);
+                    else
+                        take_unit<NT, NG, true>(rec, left, j == j0, a, qs, w, lane);
+                } else {
+                    bad = true;
+                    if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
+                }
+                __syncwarp();
+                if (issued < t1) {
+                    issue(stage);
+                    ++issued;
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    parity ^= 1;
+                }
             }
-            const bool came = mbar_wait(bars + stage * 8, parity);
-            if (!came) {
-                if (lane == 0) report_error(a.err_flag, CLO_FLAG_TIMEOUT);
-                bad = true;
+            t += j1 - j0;
+            const bool set_done = j1 == ps.nt, last = t == t1;
+            const bool whole = set_done && j0 == 0;
+            float* piece = whole ? nullptr : last ? reinterpret_cast<float*>(ring) : first_piece;
+            if (lane == 0 && !whole) piece_set[2 * warp + (last ? 1 : 0)] = ps.r * a.Hkv + ps.h;
+            end_set<BF16, NT, NG>(a, w, ps.r, ps.h, bad, piece, lane);
+            if (!last) {
+                ps.j = ps.nt - 1;
+                kv4_next(prefix, a.B, a.Hkv, ps);
             }
-            const int left = n_tok - ps.j * KV4_BLOCK;
-            if ((bad_slots >> stage) & 1u) {
-                bad = true;
-                if (lane == 0) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
-            } else if (came) {
-                const uint8_t* rec = ring + stage * R;
-                if (left >= KV4_BLOCK + a.n_q - 1)
-                    take_tile<NT, NG, false>(rec, left, qs, w, lane);
-                else
-                    take_tile<NT, NG, true>(rec, left, qs, w, lane);
-            }
-            __syncwarp();
-            if (issued < t1) {
-                issue(stage);
-                ++issued;
-            }
-            if (++stage == KV4_STAGES) {
-                stage = 0;
-                parity ^= 1;
-            }
-            const bool set_done = ps.j + 1 == ps.nt, last = t + 1 == t1;
-            if (set_done || last) {
-                const bool whole = set_done && t - set_start == ps.j;  // all of its tiles were here
-                float* piece = whole ? nullptr : last ? reinterpret_cast<float*>(ring) : first_piece;
-                if (lane == 0 && !whole) piece_set[2 * warp + (last ? 1 : 0)] = ps.r * a.Hkv + ps.h;
-                end_set<BF16, NT, NG>(a, w, ps.r, ps.h, bad, piece, lane);
-                fresh = true;
-            }
-            kv4_next(prefix, a.B, a.Hkv, ps);
         }
     }
     __syncthreads();
@@ -675,6 +728,12 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     // next to each other.
     const int c0 = g0 < W ? static_cast<int>(N * g0 / W) : 0;
     const int c1 = g0 < W ? static_cast<int>(N * min(g0 + KV4_WARPS, W) / W) : 0;
+    // Each warp's last piece is in shared memory, its first one (written in
+    // this CTA too) in the workspace.
+    auto piece_at = [&](int k) {
+        return (k & 1) ? reinterpret_cast<const float*>(smem + (k >> 1) * y.warp)
+                       : a.ws_first + static_cast<size_t>(g0 + (k >> 1)) * a.rows * KV4_PIECE_ROW;
+    };
     int tail_set = 0, tail_ctas = 0;
     for (int i = 0; i < 2 * KV4_WARPS;) {
         const int set = piece_set[i];
@@ -687,7 +746,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             }
             const int r = set / a.Hkv, h = set - r * a.Hkv;
             const int nt = (prefix[r + 1] - prefix[r]) / a.Hkv;
-            const int s0 = prefix[r] + h * nt, s1 = s0 + nt;  // its tiles
+            const int s0 = prefix[r] + h * nt, s1 = s0 + nt;  // its units
             const bool done = s0 >= c0 && s1 <= c1;
             const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s0 < c0 ? 0 : 1);
             if (s0 >= c0 && s1 > c1) {
@@ -701,8 +760,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
                 bool bad = false;
                 for (int k = i; k < end; ++k)
                     if (piece_set[k] == set) {
-                        const float* pc = reinterpret_cast<const float*>(
-                            (k & 1) ? smem + (k >> 1) * y.ring : smem + KV4_WARPS * y.ring + (k >> 1) * y.piece);
+                        const float* pc = piece_at(k);
                         M = fmaxf(M, pc[row * KV4_PIECE_ROW + KV4_D]);
                         bad |= pc[row * KV4_PIECE_ROW + KV4_D + 1] == -1.f;
                     }
@@ -711,8 +769,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
                 const float ref = M == -INFINITY ? 0.f : M;
                 for (int k = i; k < end; ++k)
                     if (piece_set[k] == set) {
-                        const float* pc = reinterpret_cast<const float*>(
-                            (k & 1) ? smem + (k >> 1) * y.ring : smem + KV4_WARPS * y.ring + (k >> 1) * y.piece);
+                        const float* pc = piece_at(k);
                         const float e = fast_exp2(pc[row * KV4_PIECE_ROW + KV4_D] - ref);
                         const float4 v = *reinterpret_cast<const float4*>(pc + row * KV4_PIECE_ROW + 4 * col);
                         L = fmaf(pc[row * KV4_PIECE_ROW + KV4_D + 1], e, L);
@@ -840,7 +897,8 @@ static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 static size_t kv4_workspace(int ctas, int rows) {
     const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
     return round256(slots * KV4_D * sizeof(float)) + round256(slots * sizeof(float2)) +
-           round256(static_cast<size_t>(ctas) * sizeof(int2));
+           round256(static_cast<size_t>(ctas) * sizeof(int2)) +
+           static_cast<size_t>(ctas) * KV4_WARPS * rows * KV4_PIECE_ROW * sizeof(float);
 }
 
 }  // namespace clo
@@ -876,18 +934,20 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, 
     if (d != KV4_D || block_size != KV4_BLOCK || ng == 0 || B > KV4_MAX_B ||
         static_cast<long long>(Hq / Hkv) * n_q > KV4_MAX_ROWS)
         return CLO_ERR_UNSUPPORTED;
-    const long long tiles = static_cast<long long>(B) * Hkv * max_blocks;  // at most: the lengths are on the device
-    if (tiles >= (1ll << 31) || max_blocks > (1 << 26)) return CLO_ERR_UNSUPPORTED;
+    const long long blocks = static_cast<long long>(B) * Hkv * max_blocks;
+    if (blocks >= (1ll << 31) || max_blocks > (1 << 26)) return CLO_ERR_UNSUPPORTED;
     if (opts != nullptr && opts->num_ctas > (1 << 20)) return CLO_ERR_UNSUPPORTED;
     if (B == 0) return CLO_OK;
 
     Kv4Args a;
     a.rows = Hq / Hkv * n_q;
-    const int smem = kv4_layout(ng, a.rows, B).total;
+    const int nt = kv4_row_tiles(a.rows);
+    const int smem = kv4_layout(nt, ng, a.rows, B).total;
     // One wave: as many CTAs an SM as registers and shared memory allow.
-    const int per_sm = std::min(kv4_ctas_per_sm(kv4_row_tiles(a.rows)), KV4_SMEM_PER_SM / (smem + 1024 + 128));
+    const int per_sm = std::min(kv4_ctas_per_sm(nt), KV4_SMEM_PER_SM / (smem + 1024 + 128));
     int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count() * per_sm;
-    const long long most = (tiles + KV4_WARPS - 1) / KV4_WARPS;
+    // At most a unit a warp (the lengths are on the device).
+    const long long most = (static_cast<long long>(B) * Hkv * ((max_blocks + 1) / 2) + KV4_WARPS - 1) / KV4_WARPS;
     if (ctas > most) ctas = static_cast<int>(most);
     if (workspace == nullptr || !kv4_aligned(workspace, 16) ||
         ws_bytes < clo_kv4_paged_workspace_size(B, n_q, Hq, Hkv, d, opts != nullptr ? opts->num_ctas : 0))
@@ -899,6 +959,8 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, 
     a.ws_o = reinterpret_cast<float*>(ws);
     a.ws_ml = reinterpret_cast<float2*>(ws + round256(slots * KV4_D * sizeof(float)));
     a.ws_tail = reinterpret_cast<int2*>(ws + round256(slots * KV4_D * sizeof(float)) + round256(slots * sizeof(float2)));
+    a.ws_first = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws_tail) +
+                                          round256(static_cast<size_t>(ctas) * sizeof(int2)));
     a.q = q;
     a.out = out;
     a.lse = lse;
@@ -914,10 +976,9 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, 
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
-    const int nt = kv4_row_tiles(a.rows);
     const Kv4Kernel kernel = dtype == CLO_BF16 ? attn_kernel<true>(nt, ng) : attn_kernel<false>(nt, ng);
     const Kv4Kernel merge = dtype == CLO_BF16 ? kv4_merge_kernel<true> : kv4_merge_kernel<false>;
-    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), kv4_layout(ng, a.rows, KV4_MAX_B).total) ||
+    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), kv4_layout(nt, ng, a.rows, KV4_MAX_B).total) ||
         !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
         return CLO_ERR_CUDA;
     if (opts != nullptr && opts->ev_begin != nullptr && !record_event(opts->ev_begin, stream)) return CLO_ERR_CUDA;
