@@ -50,8 +50,10 @@ constexpr int KV4_THREADS = KV4_WARPS * 32;
 constexpr int KV4_UNIT = 2 * KV4_BLOCK;  // tokens of a unit
 constexpr int KV4_MAX_ROWS = 32;   // query rows of a KV head: G * n_q
 constexpr int KV4_PIECE_ROW = KV4_D + 4;  // floats of a row of a piece; the four behind: m, l
-constexpr int KV4_SMEM_PER_SM = 228 * 1024;  // 1 KB of it reserved for each CTA
+constexpr int KV4_SMEM_PER_SM = 228 * 1024;
+constexpr int KV4_SMEM_RESERVED = 1024 + 256;  // of a CTA: the system's, and the static arrays
 constexpr long long KV4_WAIT_CLOCKS = 1ll << 32;  // about 2 s
+constexpr int KV4_SET_COST = 2;  // what starting and ending a token set costs a warp, in units
 constexpr float KV4_SLACK = 8.f;  // how far x + log2(V scale) may pass the reference, log2
 constexpr uint32_t LOW_CODES = 0x000f000fu, HIGH_CODES = 0x00f000f0u;
 
@@ -120,7 +122,14 @@ __device__ __forceinline__ int kv4_units(const Kv4Args& a, int r, bool& bad) {
     return bad ? 0 : (n + KV4_UNIT - 1) / KV4_UNIT;
 }
 
-// prefix[r] = units of the requests before r (all heads), r <= B.
+// The stream the warps share: each token set (request, KV head) with a token
+// is KV4_SET_COST steps for its start and end, then a step a unit.  prefix[r] =
+// steps of the requests before r (all heads), r <= B.
+__device__ __forceinline__ int kv4_steps(const Kv4Args& a, int r, bool& bad) {
+    const int n = kv4_units(a, r, bad);
+    return n > 0 ? (n + KV4_SET_COST) * a.Hkv : 0;
+}
+
 __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* wsum) {
     const int per = (a.B + KV4_THREADS - 1) / KV4_THREADS;
     const int r0 = min(a.B, static_cast<int>(threadIdx.x) * per), r1 = min(a.B, r0 + per);
@@ -128,7 +137,7 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     bool bad, any_bad = false;
     int mine = 0;
     for (int r = r0; r < r1; ++r) {
-        mine += kv4_units(a, r, bad) * a.Hkv;
+        mine += kv4_steps(a, r, bad);
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
@@ -144,76 +153,97 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     for (int w = 0; w < warp; ++w) run += wsum[w];
     if (threadIdx.x == 0) prefix[0] = 0;
     for (int r = r0; r < r1; ++r) {
-        run += kv4_units(a, r, bad) * a.Hkv;
+        run += kv4_steps(a, r, bad);
         prefix[r + 1] = run;
     }
     __syncthreads();
 }
 
-// A position in the stream: unit j of nt of request r's head h.
+// A unit: j of nt of request r's head h.
 struct Place {
     int r, h, j, nt;
 };
 
+// The first unit at step t or behind it (r == B: there is none).
 __device__ __forceinline__ Place kv4_place(const int* prefix, int B, int Hkv, int t) {
+    Place p;
+    if (t >= prefix[B]) {
+        p.r = B;
+        p.h = p.j = p.nt = 0;
+        return p;
+    }
     int lo = 0, hi = B - 1;  // the last request with prefix[r] <= t: skips empty ones
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    Place p;
+    const int steps = (prefix[lo + 1] - prefix[lo]) / Hkv;
     p.r = lo;
-    p.nt = (prefix[lo + 1] - prefix[lo]) / Hkv;
-    p.h = (t - prefix[lo]) / p.nt;
-    p.j = t - prefix[lo] - p.h * p.nt;
+    p.nt = steps - KV4_SET_COST;
+    p.h = (t - prefix[lo]) / steps;
+    p.j = max(t - prefix[lo] - p.h * steps - KV4_SET_COST, 0);
     return p;
 }
 
-// The next unit's place (one past the last: r == B, nt == 0).
-__device__ __forceinline__ void kv4_next(const int* prefix, int B, int Hkv, Place& p) {
-    if (++p.j < p.nt) return;
+// The first unit of the next set (r == B: there is none).
+__device__ __forceinline__ void kv4_next_set(const int* prefix, int B, int Hkv, Place& p) {
     p.j = 0;
     if (++p.h < Hkv) return;
     p.h = 0;
     do {
         ++p.r;
     } while (p.r < B && prefix[p.r + 1] == prefix[p.r]);
-    p.nt = p.r < B ? (prefix[p.r + 1] - prefix[p.r]) / Hkv : 0;
+    p.nt = p.r < B ? (prefix[p.r + 1] - prefix[p.r]) / Hkv - KV4_SET_COST : 0;
 }
 
-// The queries of one KV head: the B operand of the first product, and what
-// the scores need in fp32.  One n8 tile is kept in registers, more in the
-// warp's shared memory.
+// The queries of one KV head.  The B operand of the first product: one n8 tile
+// is kept in registers, more in the warp's shared memory.  What the scores need
+// in fp32, in shared memory: a row's factor of the code sums, and the sum of
+// each group's elements (log2 units).
 template <int NT, int NG>
 struct Queries {
     static constexpr bool kShared = NT > 1;
-    // Shared: [NT][4][32] operands, then [NT * 8] units and [NG][NT * 8] sums.
-    static constexpr int kBytes = kShared ? NT * (4 * 32 * 16 + 8 * 4 * (1 + NG)) : 0;
-    uint4 reg[kShared ? 1 : 4];   // word j: low codes' two registers, high codes' two
-    float2 reg_unit;              // fp32 factor of the code sums, columns 2c and 2c + 1
-    float2 reg_sum[kShared ? 1 : NG];  // sum of the group's elements (log2 units)
-    uint4* sm;
+    uint4 reg[kShared ? 1 : 4];  // word j: low codes' two registers, high codes' two
+    float* sm;                   // [NT * 8] factors, [NG][NT * 8] sums, then operands [NT][4][32]
 
-    __device__ __forceinline__ float* sm_units() const { return reinterpret_cast<float*>(sm + NT * 4 * 32); }
+    __device__ __forceinline__ uint4* sm_operands() const {
+        return reinterpret_cast<uint4*>(sm + (1 + NG) * NT * 8);
+    }
     __device__ __forceinline__ uint4 operand(int nt, int j, int lane) const {
-        if constexpr (kShared) return sm[(nt * 4 + j) * 32 + lane];
+        if constexpr (kShared) return sm_operands()[(nt * 4 + j) * 32 + lane];
         else return reg[j];
     }
-    __device__ __forceinline__ float2 unit(int nt, int c) const {
-        if constexpr (kShared) return *reinterpret_cast<const float2*>(sm_units() + nt * 8 + 2 * c);
-        else return reg_unit;
+    // Of columns 2c and 2c + 1.
+    __device__ __forceinline__ float2 factor(int nt, int c) const {
+        return *reinterpret_cast<const float2*>(sm + nt * 8 + 2 * c);
     }
     __device__ __forceinline__ float2 sum(int nt, int g, int c) const {
-        if constexpr (kShared)
-            return *reinterpret_cast<const float2*>(sm_units() + (1 + g) * NT * 8 + nt * 8 + 2 * c);
-        else return reg_sum[g];
+        return *reinterpret_cast<const float2*>(sm + (1 + g) * NT * 8 + nt * 8 + 2 * c);
     }
 };
+
+__host__ __device__ constexpr int kv4_query_bytes(int nt, int ng) {
+    return (1 + ng) * nt * 8 * 4 + (nt > 1 ? nt * 4 * 32 * 16 : 0);
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float kv4_power2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p)); }
+
+// Asks for the queries of a set ahead of its start.
+__device__ __forceinline__ void prefetch_queries(const Kv4Args& a, const Place& p, int lane) {
+    for (int line = lane; line < 2 * a.rows; line += 32) {
+        const int qi = (line >> 1) / a.G, g = (line >> 1) - qi * a.G;
+        const size_t at = (static_cast<size_t>(p.r) * a.n_q + qi) * a.Hq + static_cast<size_t>(p.h) * a.G + g;
+        prefetch_l1(static_cast<const uint8_t*>(a.q) + at * KV4_D * 2 + (line & 1) * 128);
+    }
+}
 
 template <bool BF16, int NT, int NG>
 __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, int lane, Queries<NT, NG>& qs) {
     const int head = lane >> 2, c = lane & 3;
-    if (Queries<NT, NG>::kShared) __syncwarp();  // the last set's are no longer read
+    __syncwarp();  // the last set's are no longer read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int row = nt * 8 + head;
@@ -242,9 +272,8 @@ __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, i
         top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
         // 2^e brings the largest element into [2^12, 2^13); e is bounded so
         // that 2^e and the factor that undoes it are finite.
-        int e = top > 0.f && top < INFINITY ? 12 - ilogbf(top) : 0;
-        e = min(max(e, -100), 100);
-        const float up = ldexpf(1.f, e), up16 = ldexpf(1.f, e - 4);
+        const int e = min(max(139 - static_cast<int>(__float_as_uint(top) >> 23), -100), 100);
+        const float up = kv4_power2(e), up16 = kv4_power2(e - 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f0 = kv4_unpack2<BF16>(raw[j].x), f1 = kv4_unpack2<BF16>(raw[j].y);
@@ -254,10 +283,9 @@ __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, i
             o.y = pack_half2(f1.x * up, f3.x * up);      // 2, 6
             o.z = pack_half2(f0.y * up16, f2.y * up16);  // 1, 5
             o.w = pack_half2(f1.y * up16, f3.y * up16);  // 3, 7
-            if constexpr (Queries<NT, NG>::kShared) qs.sm[(nt * 4 + j) * 32 + lane] = o;
+            if constexpr (Queries<NT, NG>::kShared) qs.sm_operands()[(nt * 4 + j) * 32 + lane] = o;
             else qs.reg[j] = o;
         }
-        const float unit = ldexpf(a.scale_log2, 24 - e);
         float group[NG];
 #pragma unroll
         for (int g2 = 0; g2 < NG; ++g2) group[g2] = 0.f;
@@ -268,23 +296,14 @@ __device__ __forceinline__ void load_queries(const Kv4Args& a, const Place& p, i
             part[j] += __shfl_xor_sync(FULL_MASK, part[j], 2);
             group[j * NG / 4] += part[j];
         }
-        if constexpr (Queries<NT, NG>::kShared) {
-            if (c == 0) {
-                float* u = qs.sm_units() + nt * 8 + head;
-                u[0] = unit;
+        if (c == 0) {
+            float* u = qs.sm + nt * 8 + head;
+            u[0] = a.scale_log2 * kv4_power2(24 - e);
 #pragma unroll
-                for (int g2 = 0; g2 < NG; ++g2) u[(1 + g2) * NT * 8] = group[g2];
-            }
-        } else {
-            const int from = 8 * c;  // a lane of column 2c; column 2c + 1's is 4 further
-            qs.reg_unit = make_float2(__shfl_sync(FULL_MASK, unit, from), __shfl_sync(FULL_MASK, unit, from + 4));
-#pragma unroll
-            for (int g2 = 0; g2 < NG; ++g2)
-                qs.reg_sum[g2] = make_float2(__shfl_sync(FULL_MASK, group[g2], from),
-                                             __shfl_sync(FULL_MASK, group[g2], from + 4));
+            for (int g2 = 0; g2 < NG; ++g2) u[(1 + g2) * NT * 8] = group[g2];
         }
     }
-    if (Queries<NT, NG>::kShared) __syncwarp();
+    __syncwarp();
 }
 
 // One warp's running softmax of a token set.
@@ -329,55 +348,70 @@ __device__ __forceinline__ float kv4_log2(float x) {
     return y;
 }
 
+// As mma_16816 and movmatrix_trans, but not volatile: they depend on their
+// operands alone, and the compiler may interleave them.
+__device__ __forceinline__ void kv4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t kv4_transpose(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+    return d;
+}
+
 __device__ __forceinline__ __half2 kv4_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
-// Takes a unit in: two records.  Rows are tokens gid and gid + 8 of record 0,
-// then of record 1; columns query rows 2c and 2c + 1 of each n8 tile.
-// first: nothing has been taken in yet.  EDGE: the unit holds tokens that some
-// query does not see; `left` counts the tokens from its first one on.
-template <int NT, int NG, bool EDGE>
-__device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool first, const Kv4Args& a,
-                                          const Queries<NT, NG>& qs, Softmax<NT, NG>& w, int lane) {
+// The NG (scale, zero) pairs of one token's K (kv = 0) or V, as stored.
+template <int NG>
+__device__ __forceinline__ void load_params(const uint8_t* rec, int t, int kv, bool there, uint32_t (&p)[NG]) {
+    const uint8_t* at = rec + kv4_param(t, kv, NG, 0);
+    if constexpr (NG == 1) {
+        p[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else if constexpr (NG == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(at);
+        p[0] = u.x, p[1] = u.y;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(at);
+        p[0] = u.x, p[1] = u.y, p[2] = u.z, p[3] = u.w;
+    }
+    // What lies behind the last token may be anything, NaN among it.
+#pragma unroll
+    for (int g = 0; g < NG; ++g) p[g] = there ? p[g] : 0u;
+}
+
+// Takes NB records in.  Rows are tokens gid and gid + 8 of each record, columns
+// query rows 2c and 2c + 1 of each n8 tile.  first: nothing has been taken in
+// yet.  EDGE: there are tokens that some query does not see; `left` counts the
+// tokens from the first record's first one on.
+template <int NT, int NG, int NB, bool EDGE>
+__device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool first, const Kv4Args& a,
+                                             const Queries<NT, NG>& qs, Softmax<NT, NG>& w, int lane) {
     constexpr int R = kv4_record(NG);
     const int gid = lane >> 2, c = lane & 3;
     // Tokens behind the last one that a column does not see.
     auto limit = [&](int nt, int col) { return a.n_q - 1 - min(nt * 8 + 2 * c + col, a.rows - 1) / a.G; };
     auto sees = [&](int nt, int row, int col) { return !EDGE || gid + 8 * row < left - limit(nt, col); };
+    auto there = [&](int row) { return !EDGE || gid + 8 * row < left; };
 
-    // ---- scores in log2 units, relative to the reference, and the V parameters
-    float x[NT][2][4];    // [n8 tile][record][row of the record, column]
-    uint32_t vp[4][NG];   // (scale, zero) of the four rows, as they are stored
-    float big[4];         // log2 of the largest V scale
+    // ---- scores in log2 units, relative to the reference
+    float x[NT][NB][4];  // [n8 tile][record][row of the record, column]
+    float big[2 * NB];   // log2 of the largest V scale of a row
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
         const uint4 k0 = *reinterpret_cast<const uint4*>(rec + b * R + gid * KV4_ROW + c * 16);
         const uint4 k1 = *reinterpret_cast<const uint4*>(rec + b * R + (gid + 8) * KV4_ROW + c * 16);
         const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
         uint32_t kp[2][NG];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint8_t* par = rec + b * R + kv4_param(gid + 8 * t, 0, NG, 0);
-            uint32_t raw[2 * NG];
-            if constexpr (NG == 1) {
-                const uint2 u = *reinterpret_cast<const uint2*>(par);
-                raw[0] = u.x, raw[1] = u.y;
-            } else {
+            uint32_t vp[NG];
+            load_params<NG>(rec + b * R, gid + 8 * t, 0, there(2 * b + t), kp[t]);
+            load_params<NG>(rec + b * R, gid + 8 * t, 1, there(2 * b + t), vp);
+            __half2 most = kv4_half2(vp[0]);
 #pragma unroll
-                for (int k = 0; k < NG / 2; ++k) {
-                    const uint4 u = reinterpret_cast<const uint4*>(par)[k];
-                    raw[4 * k] = u.x, raw[4 * k + 1] = u.y, raw[4 * k + 2] = u.z, raw[4 * k + 3] = u.w;
-                }
-            }
-            // What lies behind the last token may be anything, NaN among it.
-            const bool there = !EDGE || gid + 8 * (2 * b + t) < left;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                kp[t][g] = there ? raw[g] : 0u;
-                vp[2 * b + t][g] = there ? raw[NG + g] : 0u;
-            }
-            __half2 most = kv4_half2(vp[2 * b + t][0]);
-#pragma unroll
-            for (int g = 1; g < NG; ++g) most = __hmax2(most, kv4_half2(vp[2 * b + t][g]));
+            for (int g = 1; g < NG; ++g) most = __hmax2(most, kv4_half2(vp[g]));
             big[2 * b + t] = fmaxf(kv4_log2(__low2float(most)), -24.f);
         }
 #pragma unroll
@@ -397,22 +431,33 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint4 q = qs.operand(nt, j, lane);
-                    mma_16816(s[nt], lo, q.x, q.y);
-                    mma_16816(s[nt], hi, q.z, q.w);
+                    kv4_mma(s[nt], lo, q.x, q.y);
+                    kv4_mma(s[nt], hi, q.z, q.w);
                 }
             }
-            const float2 f[2] = {__half22float2(kv4_half2(kp[0][g])), __half22float2(kv4_half2(kp[1][g]))};
+            const float f[2] = {__low2float(kv4_half2(kp[0][g])), __low2float(kv4_half2(kp[1][g]))};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float2 unit = qs.unit(nt, c), sum = qs.sum(nt, g, c);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 sz = f[k >> 1];
-                    const float before = g == 0 ? -w.m[nt][k & 1] : x[nt][b][k];
-                    x[nt][b][k] = fmaf(sz.x * ((k & 1) ? unit.y : unit.x), s[nt][k],
-                                       fmaf(sz.y, (k & 1) ? sum.y : sum.x, before));
-                }
+                for (int k = 0; k < 4; ++k)
+                    x[nt][b][k] = g == 0 ? f[k >> 1] * s[nt][k] : fmaf(f[k >> 1], s[nt][k], x[nt][b][k]);
             }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 factor = qs.factor(nt, c);
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = fmaf(x[nt][b][k], (k & 1) ? factor.y : factor.x, -w.m[nt][k & 1]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float2 sum = qs.sum(nt, g, c);
+                const float z[2] = {__high2float(kv4_half2(kp[0][g])), __high2float(kv4_half2(kp[1][g]))};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = fmaf(z[k >> 1], (k & 1) ? sum.y : sum.x, y[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[nt][b][k] = y[k];
         }
     }
     bool hot = first;
@@ -420,7 +465,7 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
     for (int nt = 0; nt < NT; ++nt) {
         float over = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2 * NB; ++t)
 #pragma unroll
             for (int col = 0; col < 2; ++col) {
                 float& v = x[nt][t >> 1][2 * (t & 1) + col];
@@ -436,10 +481,10 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
             for (int col = 0; col < 2; ++col) {
                 float top = -INFINITY;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) top = fmaxf(top, x[nt][t >> 1][2 * (t & 1) + col] + big[t]);
+                for (int t = 0; t < 2 * NB; ++t) top = fmaxf(top, x[nt][t >> 1][2 * (t & 1) + col] + big[t]);
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
-                // At the first unit to its maximum (0 where a column sees nothing), later only up.
+                // At the first records to their maximum (0 where a column sees nothing), later only up.
                 const float by = first ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
                 const float al = first ? 0.f : kv4_exp2(-by);
                 w.m[nt][col] += by;
@@ -454,14 +499,14 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
                         w.o[nt][ch][hl][2 + col] *= al;
                     }
 #pragma unroll
-                for (int t = 0; t < 4; ++t) x[nt][t >> 1][2 * (t & 1) + col] -= by;
+                for (int t = 0; t < 2 * NB; ++t) x[nt][t >> 1][2 * (t & 1) + col] -= by;
             }
     }
 
     // ---- weights, and their product with V a record and a group at a time
     const int tok = lane & 15, half = lane >> 4;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -469,14 +514,17 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
             w.l[nt][0] += x[nt][b][0] + x[nt][b][2];
             w.l[nt][1] += x[nt][b][1] + x[nt][b][3];
         }
+        uint32_t vp[2][NG];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) load_params<NG>(rec + b * R, gid + 8 * t, 1, there(2 * b + t), vp[t]);
         const uint32_t vbase = smem_u32(rec) + b * R + KV4_CODES + tok * KV4_ROW;
-        uint32_t v[4];     // chunk 2cp: tokens 0-7, 8-15; chunk 2cp + 1: the same
+        uint32_t v[4];       // chunk 2cp: tokens 0-7, 8-15; chunk 2cp + 1: the same
         uint32_t pb[NT][2];  // the second product's B operand
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {  // channels 32 ch + 4 gid + 0..3
             if (ch % (4 / NG) == 0) {
                 const int g = ch * NG / 4;
-                const float2 f[2] = {__half22float2(kv4_half2(vp[2 * b][g])), __half22float2(kv4_half2(vp[2 * b + 1][g]))};
+                const float2 f[2] = {__half22float2(kv4_half2(vp[0][g])), __half22float2(kv4_half2(vp[1][g]))};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float y[4];
@@ -488,8 +536,8 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
                         y[k] = in ? x[nt][b][k] * f[k >> 1].x : 0.f;
                         z = in ? fmaf(x[nt][b][k], f[k >> 1].y, z) : z;
                     }
-                    pb[nt][0] = movmatrix_trans(pack_half2(y[0], y[1]));  // tokens 0-7
-                    pb[nt][1] = movmatrix_trans(pack_half2(y[2], y[3]));  // tokens 8-15
+                    pb[nt][0] = kv4_transpose(pack_half2(y[0], y[1]));  // tokens 0-7
+                    pb[nt][1] = kv4_transpose(pack_half2(y[2], y[3]));  // tokens 8-15
                 }
             }
             if ((ch & 1) == 0) ldmatrix_x4_trans(v, vbase + (((ch + half) ^ ((tok >> 1) & 3)) << 4));
@@ -498,8 +546,8 @@ __device__ __forceinline__ void take_unit(const uint8_t* rec, int left, bool fir
             const uint32_t hi[4] = {a0 & HIGH_CODES, (a0 >> 8) & HIGH_CODES, a1 & HIGH_CODES, (a1 >> 8) & HIGH_CODES};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(w.o[nt][ch][0], lo, pb[nt][0], pb[nt][1]);
-                mma_16816(w.o[nt][ch][1], hi, pb[nt][0], pb[nt][1]);
+                kv4_mma(w.o[nt][ch][0], lo, pb[nt][0], pb[nt][1]);
+                kv4_mma(w.o[nt][ch][1], hi, pb[nt][0], pb[nt][1]);
             }
         }
     }
@@ -581,9 +629,8 @@ struct Kv4Layout {
 __host__ __device__ inline Kv4Layout kv4_layout(int nt, int ng, int rows, int B) {
     Kv4Layout y;
     y.ring = kv4_stages(ng) * 2 * kv4_record(ng);
-    const int queries = nt > 1 ? nt * (4 * 32 * 16 + 8 * 4 * (1 + ng)) : 0;
     const int piece = rows * KV4_PIECE_ROW * static_cast<int>(sizeof(float));
-    const int both = y.ring + queries;
+    const int both = y.ring + kv4_query_bytes(nt, ng);
     y.warp = ((both > piece ? both : piece) + 127) / 128 * 128;  // the last piece takes their place
     y.bars = KV4_WARPS * y.warp;
     y.prefix = y.bars + KV4_WARPS * kv4_stages(ng) * 8;
@@ -595,6 +642,7 @@ template <bool BF16, int NT, int NG>
 __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_kernel(const Kv4Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int wsum[KV4_WARPS];
+    __shared__ Place walks[KV4_WARPS][3];
     __shared__ int piece_set[2 * KV4_WARPS];  // token set of each warp's first and last piece, or -1
     constexpr int R = kv4_record(NG), STAGES = kv4_stages(NG);
     const Kv4Layout y = kv4_layout(NT, NG, a.rows, a.B);
@@ -620,113 +668,152 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             for (int i = threadIdx.x; i < a.n_q * a.Hq; i += KV4_THREADS) a.lse[row0 + i] = -INFINITY;
     }
 
-    // Warp g of W takes units [N g / W, N (g + 1) / W).
+    // Warp g of W takes the units of steps [N g / W, N (g + 1) / W).
     const long long N = prefix[a.B];
     const long long W = min(static_cast<long long>(gridDim.x) * KV4_WARPS, N);
     const long long g0 = static_cast<long long>(blockIdx.x) * KV4_WARPS;
     const long long g = g0 + warp;
-    const int t0 = g < W ? static_cast<int>(N * g / W) : 0;
-    const int t1 = g < W ? static_cast<int>(N * (g + 1) / W) : 0;
+    const int x0 = g < W ? static_cast<int>(N * g / W) : 0;
+    const int x1 = g < W ? static_cast<int>(N * (g + 1) / W) : 0;
+    // Where this warp's range begins and ends, and where its loads and its
+    // computation stand: read when one goes on to another token set.
+    Place* const walk = walks[warp];
+    {
+        const Place begin = kv4_place(prefix, a.B, a.Hkv, x0), end = kv4_place(prefix, a.B, a.Hkv, x1);
+        if (lane == 0) {
+            walk[0] = walk[1] = begin;
+            walk[2] = end;
+        }
+    }
+    __syncwarp();
+    const bool any = x0 < x1 && (walk[0].r != walk[2].r || walk[0].h != walk[2].h || walk[0].j != walk[2].j);
     float* first_piece = a.ws_first + static_cast<size_t>(g) * a.rows * KV4_PIECE_ROW;
-    if (t0 < t1) {
+    if (any) {
         const uint64_t policy = l2_evict_first_policy();
-        Place pl = kv4_place(prefix, a.B, a.Hkv, t0), ps = pl;  // loading, computing
-        // Block ids: lane i holds entry `base` + i of the loading request's
-        // row, and the 32 after them.
-        int base = 0, blocks = 0, ids = 0, ids_next = 0;
-        auto load_ids = [&](int at) {
-            return at + lane < blocks ? __ldg(a.table + static_cast<size_t>(pl.r) * a.max_blocks + at + lane) : 0;
+        // ---- loads.  Lane i holds entry `at0` + i of the row of block ids (-1
+        // behind its last block, -2 for an id that is none); the next unit is
+        // entries at0 + at and the one behind it.
+        int ids, at, to_load;       // to_load: units of this set that are still to load
+        const uint8_t* head_pool;   // the pool from this KV head's record on
+        const int32_t* row;         // the request's ids from at0 on, and how many there are
+        int row_left;
+        auto load_ids = [&]() {
+            ids = lane < row_left ? __ldg(row + lane) : -1;
+            if (lane < row_left && (ids < 0 || ids >= a.num_blocks)) ids = -2;
+            if (lane == 0 && row_left > 32) prefetch_l1(row + 32);
+            at = 0;
         };
-        auto start_ids = [&]() {
-            blocks = (__ldg(a.ctx_len + pl.r) + KV4_BLOCK - 1) / KV4_BLOCK;
-            base = 2 * pl.j;
-            ids = load_ids(base);
-            ids_next = load_ids(base + 32);
+        auto start_loads = [&](const Place& p) {
+            row = a.table + static_cast<size_t>(p.r) * a.max_blocks + 2 * p.j;
+            row_left = (__ldg(a.ctx_len + p.r) + KV4_BLOCK - 1) / KV4_BLOCK - 2 * p.j;
+            head_pool = a.pool + static_cast<size_t>(p.h) * R;
+            to_load = (p.r == walk[2].r && p.h == walk[2].h ? walk[2].j : p.nt) - p.j;
+            load_ids();
         };
-        start_ids();
+        start_loads(walk[0]);
         uint32_t bad_slots = 0;  // stages with a record that does not exist
+        const size_t block_bytes = static_cast<size_t>(a.Hkv) * R;
         auto issue = [&](int stage) {
-            if (2 * pl.j - base == 32) {
-                base += 32;
-                ids = ids_next;
-                ids_next = load_ids(base + 32);
+            if (at == 32) {
+                row += 32;
+                row_left -= 32;
+                load_ids();
             }
             // Lanes 0 and 1 take the unit's two blocks; the second may be behind the last one.
-            const int entry = 2 * pl.j + (lane & 1);
-            const int id = __shfl_sync(FULL_MASK, ids, entry - base);
-            const bool exists = entry < blocks, ok = exists && id >= 0 && id < a.num_blocks;
-            const unsigned have = __ballot_sync(FULL_MASK, ok) & 3u;
-            const bool bad = __any_sync(FULL_MASK, exists && !ok);
-            bad_slots = bad ? bad_slots | (1u << stage) : bad_slots & ~(1u << stage);
+            const int id = __shfl_sync(FULL_MASK, ids, at + (lane & 1));
+            const uint32_t have = __ballot_sync(FULL_MASK, id >= 0) & 3u;
+            bad_slots &= ~(1u << stage);
+            if (__any_sync(FULL_MASK, id == -2)) bad_slots |= 1u << stage;
             const uint32_t bar = bars + stage * 8;
             if (lane == 0) {
                 if (have != 0u) mbar_expect(bar, have == 3u ? 2 * R : R);
                 else mbar_arrive(bar);
             }
             __syncwarp();
-            if (lane < 2 && ok)
-                bulk_load(smem_u32(ring) + (2 * stage + lane) * R,
-                          a.pool + (static_cast<size_t>(id) * a.Hkv + pl.h) * R, R, bar, policy);
-            if (++pl.j == pl.nt) {
-                --pl.j;
-                kv4_next(prefix, a.B, a.Hkv, pl);
-                if (pl.r < a.B) start_ids();
+            if (lane < 2 && id >= 0)
+                bulk_load(smem_u32(ring) + (2 * stage + lane) * R, head_pool + id * block_bytes, R, bar, policy);
+            at += 2;
+            if (--to_load == 0) {  // on to the next set, if its first unit is this warp's
+                Place p = walk[0];
+                const Place end = walk[2];
+                if (p.r == end.r && p.h == end.h) return;
+                kv4_next_set(prefix, a.B, a.Hkv, p);
+                if (p.r == a.B || (p.r == end.r && p.h == end.h && end.j == 0)) return;
+                __syncwarp();
+                if (lane == 0) walk[0] = p;
+                __syncwarp();
+                start_loads(p);
+                prefetch_queries(a, p, lane);
             }
         };
-        int issued = t0;
-        for (; issued < t1 && issued - t0 < STAGES; ++issued) issue(issued - t0);
+#pragma unroll 1
+        for (int i = 0; i < STAGES && to_load > 0; ++i) issue(i);
 
+        // ---- computation
         Queries<NT, NG> qs;
-        qs.sm = reinterpret_cast<uint4*>(ring + y.ring);
+        qs.sm = reinterpret_cast<float*>(ring + y.ring);
         Softmax<NT, NG> w;
         int stage = 0;
         uint32_t parity = 0;
-        for (int t = t0; t < t1;) {  // a token set, or the part of it in this range
-            const int n_tok = __ldg(a.ctx_len + ps.r);
-            load_queries<BF16, NT, NG>(a, ps, lane, qs);
+        for (bool last = false; !last;) {  // a token set, or the part of it in this range
+            load_queries<BF16, NT, NG>(a, walk[1], lane, qs);
             reset(w);
-            bool bad = false;
-            const int j0 = ps.j, j1 = min(ps.nt, j0 + t1 - t);
-            for (int j = j0; j < j1; ++j) {
+            bool bad = false, first = true;
+            int units, left;  // still to take in; tokens from the next unit's first one on
+            {
+                const Place p = walk[1], end = walk[2];
+                units = (p.r == end.r && p.h == end.h ? end.j : p.nt) - p.j;
+                left = __ldg(a.ctx_len + p.r) - p.j * KV4_UNIT;
+            }
+            for (; units > 0; --units, left -= KV4_UNIT) {
                 const bool came = mbar_wait(bars + stage * 8, parity);
                 if (came && ((bad_slots >> stage) & 1u) == 0u) {
                     const uint8_t* rec = ring + 2 * stage * R;
-                    const int left = n_tok - j * KV4_UNIT;
-                    if (left >= KV4_UNIT + a.n_q - 1)
-                        take_unit<NT, NG, false>(rec, left, j == j0, a, qs, w, lane);
-                    else
-                        take_unit<NT, NG, true>(rec, left, j == j0, a, qs, w, lane);
+                    constexpr int NB = NT == 4 ? 1 : 2;  // registers
+#pragma unroll
+                    for (int b = 0; b < 2; b += NB) {
+                        const int from_here = left - b * KV4_BLOCK;
+                        if (from_here >= NB * KV4_BLOCK + a.n_q - 1)
+                            take_records<NT, NG, NB, false>(rec + b * R, from_here, first && b == 0, a, qs, w, lane);
+                        else if (from_here > 0)
+                            take_records<NT, NG, NB, true>(rec + b * R, from_here, first && b == 0, a, qs, w, lane);
+                    }
+                    first = false;
                 } else {
                     bad = true;
                     if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
                 }
                 __syncwarp();
-                if (issued < t1) {
-                    issue(stage);
-                    ++issued;
-                }
+                if (to_load > 0) issue(stage);
                 if (++stage == STAGES) {
                     stage = 0;
                     parity ^= 1;
                 }
             }
-            t += j1 - j0;
-            const bool set_done = j1 == ps.nt, last = t == t1;
-            const bool whole = set_done && j0 == 0;
-            float* piece = whole ? nullptr : last ? reinterpret_cast<float*>(ring) : first_piece;
-            if (lane == 0 && !whole) piece_set[2 * warp + (last ? 1 : 0)] = ps.r * a.Hkv + ps.h;
-            end_set<BF16, NT, NG>(a, w, ps.r, ps.h, bad, piece, lane);
-            if (!last) {
-                ps.j = ps.nt - 1;
-                kv4_next(prefix, a.B, a.Hkv, ps);
+            Place p = walk[1];
+            const Place end = walk[2];
+            const int set = p.r * a.Hkv + p.h, r = p.r, h = p.h;
+            const bool ends_here = !(p.r == end.r && p.h == end.h), whole = ends_here && p.j == 0;
+            last = !ends_here;
+            if (ends_here) {
+                kv4_next_set(prefix, a.B, a.Hkv, p);
+                last = p.r == a.B || (p.r == end.r && p.h == end.h && end.j == 0);
             }
+            __syncwarp();
+            if (lane == 0) {
+                walk[1] = p;
+                if (!whole) piece_set[2 * warp + (last ? 1 : 0)] = set;
+            }
+            __syncwarp();
+            float* piece = whole ? nullptr : last ? reinterpret_cast<float*>(ring) : first_piece;
+            end_set<BF16, NT, NG>(a, w, r, h, bad, piece, lane);
         }
     }
     __syncthreads();
 
     // The CTA's pieces, in the order of the stream; those of one token set are
     // next to each other.
-    const int c0 = g0 < W ? static_cast<int>(N * g0 / W) : 0;
+    const int c0 = g0 < W ? static_cast<int>(N * g0 / W) : 0;  // the CTA's steps
     const int c1 = g0 < W ? static_cast<int>(N * min(g0 + KV4_WARPS, W) / W) : 0;
     // Each warp's last piece is in shared memory, its first one (written in
     // this CTA too) in the workspace.
@@ -745,8 +832,8 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
                 else if (piece_set[k] >= 0) break;
             }
             const int r = set / a.Hkv, h = set - r * a.Hkv;
-            const int nt = (prefix[r + 1] - prefix[r]) / a.Hkv;
-            const int s0 = prefix[r] + h * nt, s1 = s0 + nt;  // its units
+            const int steps = (prefix[r + 1] - prefix[r]) / a.Hkv;
+            const int s0 = prefix[r] + h * steps + KV4_SET_COST, s1 = prefix[r] + (h + 1) * steps;  // its units' steps
             const bool done = s0 >= c0 && s1 <= c1;
             const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s0 < c0 ? 0 : 1);
             if (s0 >= c0 && s1 > c1) {
@@ -935,7 +1022,10 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, 
         static_cast<long long>(Hq / Hkv) * n_q > KV4_MAX_ROWS)
         return CLO_ERR_UNSUPPORTED;
     const long long blocks = static_cast<long long>(B) * Hkv * max_blocks;
-    if (blocks >= (1ll << 31) || max_blocks > (1 << 26)) return CLO_ERR_UNSUPPORTED;
+    const long long units = static_cast<long long>(B) * Hkv * ((max_blocks + 1) / 2);  // at most: the lengths are on the device
+    if (blocks >= (1ll << 31) || max_blocks > (1 << 26) ||
+        units + static_cast<long long>(B) * Hkv * KV4_SET_COST >= (1ll << 31))
+        return CLO_ERR_UNSUPPORTED;
     if (opts != nullptr && opts->num_ctas > (1 << 20)) return CLO_ERR_UNSUPPORTED;
     if (B == 0) return CLO_OK;
 
@@ -944,10 +1034,9 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, 
     const int nt = kv4_row_tiles(a.rows);
     const int smem = kv4_layout(nt, ng, a.rows, B).total;
     // One wave: as many CTAs an SM as registers and shared memory allow.
-    const int per_sm = std::min(kv4_ctas_per_sm(nt), KV4_SMEM_PER_SM / (smem + 1024 + 128));
+    const int per_sm = std::min(kv4_ctas_per_sm(nt), KV4_SMEM_PER_SM / (smem + KV4_SMEM_RESERVED));
     int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count() * per_sm;
-    // At most a unit a warp (the lengths are on the device).
-    const long long most = (static_cast<long long>(B) * Hkv * ((max_blocks + 1) / 2) + KV4_WARPS - 1) / KV4_WARPS;
+    const long long most = (units + KV4_WARPS - 1) / KV4_WARPS;  // a unit a warp
     if (ctas > most) ctas = static_cast<int>(most);
     if (workspace == nullptr || !kv4_aligned(workspace, 16) ||
         ws_bytes < clo_kv4_paged_workspace_size(B, n_q, Hq, Hkv, d, opts != nullptr ? opts->num_ctas : 0))
