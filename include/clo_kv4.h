@@ -19,7 +19,8 @@
  * data-dependent errors ORed into *err_flag, no allocation, no exception
  * across the interface).  The data type of 16-bit tensors is an argument
  * (clo_dtype).  d (head dimension) must be 128 and block_size 16 in this
- * build.
+ * build.  Each call takes its arguments in a struct, which it only reads
+ * before it returns; a program that makes a call again each step keeps one.
  *
  * The cache.  pool is [num_blocks][Hkv][R] bytes: a record of
  * R = clo_kv4_block_bytes(16, 128, group) bytes holds the 16 tokens of one
@@ -102,11 +103,27 @@ size_t clo_kv4_block_bytes(int block_size, int d, int group);
  * max_new <= 2^30, ring_size <= 2^30.
  * With B == 0 the padding, offsets[0] = 0 and ring_out are still written.
  */
-clo_status clo_paged_plan(const int32_t* len_in, const int32_t* keep, const int32_t* add, int B,
-                          int block_size, int32_t* block_table, int max_blocks, int32_t* free_ring,
-                          int ring_size, const int32_t* ring_in, int32_t* ring_out,
-                          int32_t* len_out, int32_t* start, int32_t* offsets, int32_t* slot_map,
-                          int max_new, int32_t* err_flag, cudaStream_t stream);
+typedef struct clo_paged_plan_args {
+    const int32_t* len_in;
+    const int32_t* keep;
+    const int32_t* add;
+    int32_t* block_table;
+    int32_t* free_ring;
+    const int32_t* ring_in;
+    int32_t* ring_out;
+    int32_t* len_out;
+    int32_t* start;
+    int32_t* offsets;
+    int32_t* slot_map;
+    int32_t* err_flag;
+    int B;
+    int block_size;
+    int max_blocks;
+    int ring_size;
+    int max_new;
+} clo_paged_plan_args;
+
+clo_status clo_paged_plan(const clo_paged_plan_args* args, cudaStream_t stream);
 
 /*
  * clo_kv4_append -- writes the K and V rows of N new tokens into the cache.
@@ -124,24 +141,51 @@ clo_status clo_paged_plan(const int32_t* len_in, const int32_t* keep, const int3
  *           Hkv * d), so both may be parts of a fused projection's output.
  * slot_map: [N] int32, distinct slots; -1 skips the row.  Any other slot
  *           outside [0, num_blocks * 16) sets CLO_FLAG_BAD_INDEX and skips it.
- * Requires k, v and pool 16-byte aligned, N * Hkv < 2^31.
+ * Requires k, v and pool 16-byte aligned, N * Hkv < 2^31 - 2^20.
  */
-clo_status clo_kv4_append(const void* k, const void* v, long long k_stride, long long v_stride,
-                          clo_dtype dtype, const int32_t* slot_map, int N, int Hkv, int d,
-                          uint8_t* pool, int num_blocks, int block_size, int group,
-                          int32_t* err_flag, cudaStream_t stream);
+typedef struct clo_kv4_append_args {
+    const void* k;
+    const void* v;
+    long long k_stride;
+    long long v_stride;
+    const int32_t* slot_map;
+    uint8_t* pool;
+    int32_t* err_flag;
+    clo_dtype dtype;
+    int N;
+    int Hkv;
+    int d;
+    int num_blocks;
+    int block_size;
+    int group;
+} clo_kv4_append_args;
+
+clo_status clo_kv4_append(const clo_kv4_append_args* args, cudaStream_t stream);
 
 /*
  * clo_kv4_gather -- reads the rows of N slots back in 16 bits: what the
- * attention takes as their K and V, code * scale + zero in fp32 rounded to
- * the nearest value of `dtype`.
+ * attention takes as their K and V, code * scale + zero rounded to the nearest
+ * value of `dtype` (for bf16 by way of fp32).
  * slot_map: [N] int32; a slot may repeat.  -1 gives a row of zeros, any other
  *           slot outside [0, num_blocks * 16) too (and CLO_FLAG_BAD_INDEX).
  * k, v:     [N][Hkv][d] of type `dtype`, contiguous, 16-byte aligned.
  */
-clo_status clo_kv4_gather(const uint8_t* pool, int num_blocks, int block_size, int group,
-                          const int32_t* slot_map, int N, int Hkv, int d, void* k, void* v,
-                          clo_dtype dtype, int32_t* err_flag, cudaStream_t stream);
+typedef struct clo_kv4_gather_args {
+    const uint8_t* pool;
+    const int32_t* slot_map;
+    void* k;
+    void* v;
+    int32_t* err_flag;
+    clo_dtype dtype;
+    int N;
+    int Hkv;
+    int d;
+    int num_blocks;
+    int block_size;
+    int group;
+} clo_kv4_gather_args;
+
+clo_status clo_kv4_gather(const clo_kv4_gather_args* args, cudaStream_t stream);
 
 /* Workspace bytes clo_kv4_paged_decode_attn needs when run with num_ctas CTAs
  * (0 = the default grid on the current device); 0 for invalid sizes.  It needs
@@ -168,13 +212,31 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  * Requires d == 128, block_size == 16, (Hq / Hkv) * n_q <= 32, B <= 4096,
  * B * Hkv * max_blocks < 2^31.
  */
-clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, const uint8_t* pool,
-                                     const int32_t* block_table, int max_blocks,
-                                     const int32_t* ctx_len, int num_blocks, int B, int n_q, int Hq,
-                                     int Hkv, int d, int block_size, int group, float scale,
-                                     void* out, float* lse, void* workspace, size_t ws_bytes,
-                                     int32_t* err_flag, const clo_attn_opts* opts,
-                                     cudaStream_t stream);
+typedef struct clo_kv4_attn_args {
+    const void* q;
+    const uint8_t* pool;
+    const int32_t* block_table;
+    const int32_t* ctx_len;
+    void* out;
+    float* lse;
+    void* workspace;
+    size_t ws_bytes;
+    int32_t* err_flag;
+    const clo_attn_opts* opts;
+    clo_dtype dtype;
+    float scale;
+    int B;
+    int n_q;
+    int Hq;
+    int Hkv;
+    int d;
+    int num_blocks;
+    int block_size;
+    int max_blocks;
+    int group;
+} clo_kv4_attn_args;
+
+clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

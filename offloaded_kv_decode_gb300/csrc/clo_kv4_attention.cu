@@ -1000,13 +1000,21 @@ extern "C" size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, 
     return ctas > 0 ? kv4_workspace(ctas, rows) : 0;
 }
 
-extern "C" clo_status clo_kv4_paged_decode_attn(const void* q, clo_dtype dtype, const uint8_t* pool,
-                                                const int32_t* block_table, int max_blocks,
-                                                const int32_t* ctx_len, int num_blocks, int B, int n_q,
-                                                int Hq, int Hkv, int d, int block_size, int group,
-                                                float scale, void* out, float* lse, void* workspace,
-                                                size_t ws_bytes, int32_t* err_flag,
-                                                const clo_attn_opts* opts, cudaStream_t stream) {
+extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, cudaStream_t stream) {
+    if (args == nullptr) return CLO_ERR_INVALID_ARG;
+    const void* q = args->q;
+    const uint8_t* pool = args->pool;
+    const int32_t *block_table = args->block_table, *ctx_len = args->ctx_len;
+    int32_t* err_flag = args->err_flag;
+    void *out = args->out, *workspace = args->workspace;
+    float* lse = args->lse;
+    const size_t ws_bytes = args->ws_bytes;
+    const clo_attn_opts* opts = args->opts;
+    const clo_dtype dtype = args->dtype;
+    const float scale = args->scale;
+    const int B = args->B, n_q = args->n_q, Hq = args->Hq, Hkv = args->Hkv, d = args->d;
+    const int num_blocks = args->num_blocks, block_size = args->block_size, max_blocks = args->max_blocks;
+    const int group = args->group;
     if (B < 0 || n_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_blocks < 1 || num_blocks < 1)
         return CLO_ERR_INVALID_ARG;
     if (dtype != CLO_F16 && dtype != CLO_BF16) return CLO_ERR_INVALID_ARG;

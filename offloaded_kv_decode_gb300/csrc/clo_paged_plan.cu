@@ -25,22 +25,6 @@ constexpr int PLAN_PER = KV4_MAX_B / PLAN_THREADS;  // requests a thread, at mos
 constexpr int PLAN_CLUSTER = 8;
 constexpr int PLAN_MAX_NEW = 1 << 30;  // strided 32-bit loops stay in range
 
-struct PlanArgs {
-    const int32_t* len_in;
-    const int32_t* keep;
-    const int32_t* add;
-    int32_t* table;
-    int32_t* ring;
-    const int32_t* ring_in;
-    int32_t* ring_out;
-    int32_t* len_out;
-    int32_t* start;
-    int32_t* offsets;
-    int32_t* slots;
-    int32_t* err_flag;
-    int B, max_blocks, ring_size, max_new;
-};
-
 // Exclusive sums of two 32-bit counts a thread (each total below 2^31) over
 // the block, as the two halves of one 64-bit sum; total gets the block's.
 __device__ __forceinline__ unsigned long long plan_scan(unsigned long long v, unsigned long long* wsum,
@@ -94,7 +78,7 @@ __device__ __forceinline__ int plan_wrap(int head, int j, int size) {
     return static_cast<int>(x >= static_cast<unsigned>(size) ? x - static_cast<unsigned>(size) : x);
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const clo_paged_plan_args a) {
     extern __shared__ int psm[];
     __shared__ unsigned long long wsum[32];
     const int B = a.B;
@@ -216,14 +200,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanArgs
     // Blocks taken: column had + j of a row is the ring's entry head + (blocks taken before) + j.
     for (int i = tid; i < n_taken; i += nthr) {
         const int r = plan_owner(taken, B, i);
-        a.table[static_cast<long long>(r) * a.max_blocks + had[r] + (i - taken[r])] =
-            a.ring[plan_wrap(head, i, a.ring_size)];
+        a.block_table[static_cast<long long>(r) * a.max_blocks + had[r] + (i - taken[r])] =
+            a.free_ring[plan_wrap(head, i, a.ring_size)];
     }
     // Blocks given back go behind the free ones; those are taken from its other end.
     for (int i = tid; i < n_back; i += nthr) {
         const int r = plan_owner(given, B, i);
-        a.ring[plan_wrap(plan_wrap(head, count, a.ring_size), i, a.ring_size)] =
-            a.table[static_cast<long long>(r) * a.max_blocks + has[r] + (i - given[r])];
+        a.free_ring[plan_wrap(plan_wrap(head, count, a.ring_size), i, a.ring_size)] =
+            a.block_table[static_cast<long long>(r) * a.max_blocks + has[r] + (i - given[r])];
     }
     // Slots, and the padding behind them.
     bool bad = false;
@@ -234,14 +218,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanArgs
             if (first[r] >= 0) {
                 const int pos = first[r] + i - off[r], col = pos / KV4_BLOCK;
                 const int id = col < had[r]
-                                   ? a.table[static_cast<long long>(r) * a.max_blocks + col]
-                                   : a.ring[plan_wrap(head, taken[r] + col - had[r], a.ring_size)];
+                                   ? a.block_table[static_cast<long long>(r) * a.max_blocks + col]
+                                   : a.free_ring[plan_wrap(head, taken[r] + col - had[r], a.ring_size)];
                 const bool ok = id >= 0 && id < (1 << 27);
                 bad |= !ok;
                 slot = ok ? id * KV4_BLOCK + pos % KV4_BLOCK : -1;
             }
         }
-        a.slots[i] = slot;
+        a.slot_map[i] = slot;
     }
     if (bad) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
 }
@@ -250,53 +234,32 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PlanArgs
 
 using namespace clo;
 
-extern "C" clo_status clo_paged_plan(const int32_t* len_in, const int32_t* keep, const int32_t* add, int B,
-                                     int block_size, int32_t* block_table, int max_blocks,
-                                     int32_t* free_ring, int ring_size, const int32_t* ring_in,
-                                     int32_t* ring_out, int32_t* len_out, int32_t* start,
-                                     int32_t* offsets, int32_t* slot_map, int max_new,
-                                     int32_t* err_flag, cudaStream_t stream) {
-    if (B < 0 || max_blocks < 1 || ring_size < 1 || max_new < 0) return CLO_ERR_INVALID_ARG;
-    if (free_ring == nullptr || ring_in == nullptr || ring_out == nullptr || offsets == nullptr ||
-        (max_new > 0 && slot_map == nullptr))
+extern "C" clo_status clo_paged_plan(const clo_paged_plan_args* args, cudaStream_t stream) {
+    if (args == nullptr) return CLO_ERR_INVALID_ARG;
+    const clo_paged_plan_args& a = *args;
+    if (a.B < 0 || a.max_blocks < 1 || a.ring_size < 1 || a.max_new < 0) return CLO_ERR_INVALID_ARG;
+    if (a.free_ring == nullptr || a.ring_in == nullptr || a.ring_out == nullptr || a.offsets == nullptr ||
+        (a.max_new > 0 && a.slot_map == nullptr))
         return CLO_ERR_INVALID_ARG;
-    if (B > 0 && (len_in == nullptr || add == nullptr || block_table == nullptr || len_out == nullptr ||
-                  start == nullptr))
+    if (a.B > 0 && (a.len_in == nullptr || a.add == nullptr || a.block_table == nullptr ||
+                    a.len_out == nullptr || a.start == nullptr))
         return CLO_ERR_INVALID_ARG;
-    for (const void* p : {static_cast<const void*>(len_in), static_cast<const void*>(keep),
-                          static_cast<const void*>(add), static_cast<const void*>(block_table),
-                          static_cast<const void*>(free_ring), static_cast<const void*>(ring_in),
-                          static_cast<const void*>(ring_out), static_cast<const void*>(len_out),
-                          static_cast<const void*>(start), static_cast<const void*>(offsets),
-                          static_cast<const void*>(slot_map), static_cast<const void*>(err_flag)})
+    for (const int32_t* p : {a.len_in, a.keep, a.add, static_cast<const int32_t*>(a.block_table),
+                             static_cast<const int32_t*>(a.free_ring), a.ring_in,
+                             static_cast<const int32_t*>(a.ring_out), static_cast<const int32_t*>(a.len_out),
+                             static_cast<const int32_t*>(a.start), static_cast<const int32_t*>(a.offsets),
+                             static_cast<const int32_t*>(a.slot_map), static_cast<const int32_t*>(a.err_flag)})
         if (!kv4_aligned(p, 4)) return CLO_ERR_INVALID_ARG;
-    if (block_size != KV4_BLOCK || B > KV4_MAX_B || max_new > PLAN_MAX_NEW || ring_size > PLAN_MAX_NEW) return CLO_ERR_UNSUPPORTED;
-    if (static_cast<long long>(B > 0 ? B : 1) * max_blocks * KV4_BLOCK >= (1ll << 31))
+    if (a.block_size != KV4_BLOCK || a.B > KV4_MAX_B || a.max_new > PLAN_MAX_NEW || a.ring_size > PLAN_MAX_NEW)
         return CLO_ERR_UNSUPPORTED;
-
-    PlanArgs a;
-    a.len_in = len_in;
-    a.keep = keep;
-    a.add = add;
-    a.table = block_table;
-    a.ring = free_ring;
-    a.ring_in = ring_in;
-    a.ring_out = ring_out;
-    a.len_out = len_out;
-    a.start = start;
-    a.offsets = offsets;
-    a.slots = slot_map;
-    a.err_flag = err_flag;
-    a.B = B;
-    a.max_blocks = max_blocks;
-    a.ring_size = ring_size;
-    a.max_new = max_new;
-    const size_t smem = (6 * static_cast<size_t>(B) + 3) * sizeof(int);
+    if (static_cast<long long>(a.B > 0 ? a.B : 1) * a.max_blocks * KV4_BLOCK >= (1ll << 31))
+        return CLO_ERR_UNSUPPORTED;
+    const size_t smem = (6 * static_cast<size_t>(a.B) + 3) * sizeof(int);
     if (!prepare_kernel(reinterpret_cast<const void*>(paged_plan_kernel),
                         static_cast<int>((6 * static_cast<size_t>(KV4_MAX_B) + 3) * sizeof(int))))
         return CLO_ERR_CUDA;
     // One CTA writes 4096 slots in the time that a cluster's launch adds.
-    const unsigned ctas = max_new > 4 * PLAN_THREADS ? PLAN_CLUSTER : 1;
+    const unsigned ctas = a.max_new > 4 * PLAN_THREADS ? PLAN_CLUSTER : 1;
     return launch_pdl_cluster(paged_plan_kernel, dim3(ctas), dim3(PLAN_THREADS), smem, stream, ctas, a) ==
                    cudaSuccess
                ? CLO_OK

@@ -19,26 +19,53 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (_F, _I, _P, _SIGS, _SZ, CLO_ERR_INVALID_ARG, HEAD_DIM, CloError, PreparedCall, _dev, _opts, _run,
-               lib)
+from . import (_F, _I, _P, _SIGS, _SZ, CLO_ERR_INVALID_ARG, CLO_OK, HEAD_DIM, CloError, PreparedCall, _check, _dev,
+               _opts, _run, lib)
 
 FLAG_NO_ROOM = 0x10
 KV4_BLOCK_SIZE = 16
 KV4_GROUPS = (32, 64, 128)
 
 _LL = ctypes.c_longlong
+
+
+class PlanArgs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("len_in", "keep", "add", "block_table", "free_ring", "ring_in", "ring_out", "len_out",
+                                  "start", "offsets", "slot_map", "err_flag")] + \
+               [(n, _I) for n in ("B", "block_size", "max_blocks", "ring_size", "max_new")]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_stride", _LL), ("v_stride", _LL), ("slot_map", _P), ("pool", _P),
+                ("err_flag", _P)] + \
+               [(n, _I) for n in ("dtype", "N", "Hkv", "d", "num_blocks", "block_size", "group")]
+
+
+class GatherArgs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("pool", "slot_map", "k", "v", "err_flag")] + \
+               [(n, _I) for n in ("dtype", "N", "Hkv", "d", "num_blocks", "block_size", "group")]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("q", "pool", "block_table", "ctx_len", "out", "lse", "workspace")] + \
+               [("ws_bytes", _SZ), ("err_flag", _P), ("opts", _P), ("dtype", _I), ("scale", _F)] + \
+               [(n, _I) for n in ("B", "n_q", "Hq", "Hkv", "d", "num_blocks", "block_size", "max_blocks", "group")]
+
+
 _SIGS.update({
     "clo_kv4_block_bytes": ([_I, _I, _I], _SZ),
-    "clo_paged_plan": ([_P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P], _I),
-    "clo_kv4_append": ([_P, _P, _LL, _LL, _I, _P, _I, _I, _I, _P, _I, _I, _I, _P, _P], _I),
-    "clo_kv4_gather": ([_P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _I, _P, _P], _I),
+    "clo_paged_plan": ([_P, _P], _I),
+    "clo_kv4_append": ([_P, _P], _I),
+    "clo_kv4_gather": ([_P, _P], _I),
     "clo_kv4_paged_workspace_size": ([_I, _I, _I, _I, _I, _I], _SZ),
-    "clo_kv4_paged_decode_attn": ([_P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ,
-                                   _P, _P, _P], _I),
+    "clo_kv4_paged_decode_attn": ([_P, _P], _I),
 })
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _GROUP_OF_RECORD = {2048 + 128 * (HEAD_DIM // g): g for g in KV4_GROUPS}
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # as current_stream(), without the object
 
 
 class _Prepared(PreparedCall):
@@ -55,7 +82,12 @@ class _Prepared(PreparedCall):
         if torch.cuda.current_device() != self._device:
             raise CloError(f"the call's tensors are on cuda:{self._device}, which is not the current device",
                            CLO_ERR_INVALID_ARG)
-        super().__call__()
+        st = self._stream
+        if st is None:
+            st = torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(self._device)
+        status = self._fn(self._args[0], st)
+        if status != CLO_OK:
+            _check(status, self._what)
 
 
 def _device_of(*tensors) -> int:
@@ -130,8 +162,9 @@ def _plan_call(len_in, add, block_table, free_ring, ring_in, ring_out, len_out, 
         raise CloError("plan buffer sizes do not match len_in", CLO_ERR_INVALID_ARG)
     keepalive = (len_in, add, block_table, free_ring, ring_in, ring_out, len_out, start, offsets, slot_map, keep,
                  err_flag)
-    return ("clo_paged_plan", (pl, pk, pa, B, int(block_size), pt, block_table.shape[1], pr, free_ring.numel(), pi,
-                               po, plo, ps, pof, psl, slot_map.numel(), pe), keepalive), _device_of(*keepalive)
+    args = PlanArgs(pl, pk or None, pa, pt, pr, pi, po, plo, ps, pof, psl, pe or None, B, int(block_size),
+                    block_table.shape[1], free_ring.numel(), slot_map.numel())
+    return ("clo_paged_plan", (ctypes.byref(args),), keepalive + (args,)), _device_of(*keepalive)
 
 
 # ---------------------------------------------------------------- append and gather
@@ -170,8 +203,9 @@ def _append_call(k, v, slot_map, pool, err_flag):
     pe = _dev(err_flag, "err_flag", torch.int32, optional=True)
     if v.dtype != k.dtype or v.shape != k.shape or slot_map.numel() != k.shape[0] or k.shape[1] != Hkv:
         raise CloError("append shapes do not match", CLO_ERR_INVALID_ARG)
-    return ("clo_kv4_append", (pk, pv, ks, vs, dt, psl, k.shape[0], Hkv, k.shape[2], pp, nb, KV4_BLOCK_SIZE, group,
-                               pe), (k, v, slot_map, pool, err_flag)), _device_of(k, v, slot_map, pool, err_flag)
+    args = AppendArgs(pk, pv, ks, vs, psl, pp, pe or None, dt, k.shape[0], Hkv, k.shape[2], nb, KV4_BLOCK_SIZE, group)
+    keepalive = (k, v, slot_map, pool, err_flag)
+    return ("clo_kv4_append", (ctypes.byref(args),), keepalive + (args,)), _device_of(*keepalive)
 
 
 def clo_kv4_gather(pool: torch.Tensor, slot_map: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -195,8 +229,9 @@ def _gather_call(pool, slot_map, k, v, err_flag):
     pe = _dev(err_flag, "err_flag", torch.int32, optional=True)
     if v.shape != k.shape or slot_map.numel() != k.shape[0] or k.shape[1] != Hkv:
         raise CloError("gather shapes do not match", CLO_ERR_INVALID_ARG)
-    return ("clo_kv4_gather", (pp, nb, KV4_BLOCK_SIZE, group, psl, k.shape[0], Hkv, k.shape[2], pk, pv, dt, pe),
-            (pool, slot_map, k, v, err_flag)), _device_of(pool, slot_map, k, v, err_flag)
+    args = GatherArgs(pp, psl, pk, pv, pe or None, dt, k.shape[0], Hkv, k.shape[2], nb, KV4_BLOCK_SIZE, group)
+    keepalive = (pool, slot_map, k, v, err_flag)
+    return ("clo_kv4_gather", (ctypes.byref(args),), keepalive + (args,)), _device_of(*keepalive)
 
 
 # ---------------------------------------------------------------- attention
@@ -247,7 +282,7 @@ def _attn_call(q, pool, block_table, ctx_len, out, workspace, lse, err_flag, sca
         scale = 1.0 / math.sqrt(d)
     opts = _opts(num_ctas, events)
     keepalive = (q, pool, block_table, ctx_len, out, workspace, lse, err_flag)
-    return ("clo_kv4_paged_decode_attn",
-            (pq, dt, pp, pt, block_table.shape[1], pc, nb, B, n_q, Hq, Hkv, d, KV4_BLOCK_SIZE, group, float(scale),
-             po, plse, pws, workspace.numel(), pe, ctypes.byref(opts) if opts is not None else None),
-            keepalive + (opts,)), _device_of(*keepalive)
+    args = AttnArgs(pq, pp, pt, pc, po, plse or None, pws, workspace.numel(), pe or None,
+                    ctypes.addressof(opts) if opts is not None else None, dt, float(scale), B, n_q, Hq, Hkv, d, nb,
+                    KV4_BLOCK_SIZE, block_table.shape[1], group)
+    return ("clo_kv4_paged_decode_attn", (ctypes.byref(args),), keepalive + (opts, args)), _device_of(*keepalive)

@@ -1,6 +1,7 @@
 """The 4-bit paged cache's entry points without a GPU: the exported symbols,
 what each call refuses before it launches anything, and the reference's own
 layout and quantiser."""
+import ctypes
 import os
 import re
 
@@ -11,6 +12,7 @@ import torch
 import kv4_ref as ref
 import offloaded_kv_decode_gb300 as clo
 from offloaded_kv_decode_gb300 import build as libbuild
+from offloaded_kv_decode_gb300 import kv4
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 1 << 20  # aligned non-null stand-in pointer: never dereferenced on these paths
@@ -43,16 +45,26 @@ def test_record_sizes(L):
     assert clo.clo_kv4_block_bytes(64, d=64) == 0
 
 
+def call(L, what, struct, values):
+    return getattr(L, what)(ctypes.byref(struct(**values)), None)
+
+
 def _plan(L, B=4, bs=16, mb=8, rs=64, mn=32, **kw):
-    p = dict(len_in=FAKE, keep=None, add=FAKE, table=FAKE, ring=FAKE, ring_in=FAKE, ring_out=FAKE, len_out=FAKE,
-             start=FAKE, offsets=FAKE, slots=FAKE)
+    p = dict(len_in=FAKE, keep=None, add=FAKE, block_table=FAKE, free_ring=FAKE, ring_in=FAKE, ring_out=FAKE,
+             len_out=FAKE, start=FAKE, offsets=FAKE, slot_map=FAKE, B=B, block_size=bs, max_blocks=mb, ring_size=rs,
+             max_new=mn)
     p.update(kw)
-    return L.clo_paged_plan(p["len_in"], p["keep"], p["add"], B, bs, p["table"], mb, p["ring"], rs, p["ring_in"],
-                            p["ring_out"], p["len_out"], p["start"], p["offsets"], p["slots"], mn, None, None)
+    return call(L, "clo_paged_plan", kv4.PlanArgs, p)
+
+
+def test_no_arguments(L):
+    for what in ("clo_paged_plan", "clo_kv4_append", "clo_kv4_gather", "clo_kv4_paged_decode_attn"):
+        assert getattr(L, what)(None, None) == INVALID
 
 
 def test_plan_rejects(L):
-    for name in ("len_in", "add", "table", "ring", "ring_in", "ring_out", "len_out", "start", "offsets", "slots"):
+    for name in ("len_in", "add", "block_table", "free_ring", "ring_in", "ring_out", "len_out", "start", "offsets",
+                 "slot_map"):
         assert _plan(L, **{name: None}) == INVALID, name
         assert _plan(L, **{name: FAKE + 2}) == INVALID, name
     assert _plan(L, keep=FAKE + 1) == INVALID
@@ -69,7 +81,9 @@ def test_plan_rejects(L):
 
 def _append(L, k=FAKE, v=FAKE, ks=1024, vs=1024, dt=0, slots=FAKE, N=4, Hkv=8, d=128, pool=FAKE, nb=16, bs=16,
             group=64, err=None):
-    return L.clo_kv4_append(k, v, ks, vs, dt, slots, N, Hkv, d, pool, nb, bs, group, err, None)
+    return call(L, "clo_kv4_append", kv4.AppendArgs, dict(
+        k=k, v=v, k_stride=ks, v_stride=vs, slot_map=slots, pool=pool, err_flag=err, dtype=dt, N=N, Hkv=Hkv, d=d,
+        num_blocks=nb, block_size=bs, group=group))
 
 
 def test_append_rejects(L):
@@ -94,7 +108,8 @@ def test_append_rejects(L):
 
 
 def _gather(L, k=FAKE, v=FAKE, dt=0, slots=FAKE, N=4, Hkv=8, d=128, pool=FAKE, nb=16, bs=16, group=64):
-    return L.clo_kv4_gather(pool, nb, bs, group, slots, N, Hkv, d, k, v, dt, None, None)
+    return call(L, "clo_kv4_gather", kv4.GatherArgs, dict(
+        pool=pool, slot_map=slots, k=k, v=v, dtype=dt, N=N, Hkv=Hkv, d=d, num_blocks=nb, block_size=bs, group=group))
 
 
 def test_gather_rejects(L):
@@ -111,9 +126,10 @@ def test_gather_rejects(L):
 def _attn(L, q=FAKE, dt=0, pool=FAKE, bt=FAKE, mb=8, cl=FAKE, nb=64, B=4, n_q=1, Hq=32, Hkv=8, d=128, bs=16,
           group=64, scale=0.088, out=FAKE, lse=None, ws=FAKE, wsb=1 << 40, num_ctas=7):
     opts = clo.AttnOpts(num_ctas, None, None)
-    import ctypes
-    return L.clo_kv4_paged_decode_attn(q, dt, pool, bt, mb, cl, nb, B, n_q, Hq, Hkv, d, bs, group, scale, out, lse,
-                                       ws, wsb, None, ctypes.byref(opts), None)
+    return call(L, "clo_kv4_paged_decode_attn", kv4.AttnArgs, dict(
+        q=q, pool=pool, block_table=bt, ctx_len=cl, out=out, lse=lse, workspace=ws, ws_bytes=wsb,
+        opts=ctypes.addressof(opts), dtype=dt, scale=scale, B=B, n_q=n_q, Hq=Hq, Hkv=Hkv, d=d, num_blocks=nb,
+        block_size=bs, max_blocks=mb, group=group))
 
 
 def test_attention_rejects(L):
