@@ -9,14 +9,20 @@
 //
 // Both are streams: HBM bounds them, and next the issue slots (at HBM's rate an
 // SM has 110 warp instructions for a row pair of the append).  So a warp has the
-// rows of 4 (token, head)s in flight, the rows are loaded without waiting for
-// their slots, and fp32 work is done on pairs (the f32x2 instructions).
+// rows of 4 (token, head)s in flight: of one token where the heads divide by 4
+// (one slot and one address for all), else 2 heads of 2 tokens or 1 of 4.  The
+// rows are loaded without waiting for their slots, and fp32 work is done on
+// pairs (the f32x2 instructions).
 #include "clo_kv4.cuh"
 
 namespace clo {
 
 constexpr int CACHE_THREADS = 256;
-constexpr int CACHE_CTAS_PER_SM = 8;
+// CTAs an SM (registers: up to 42, and 42 or 32 a thread).  A warp
+// takes one group and ends: a grid of one wave whose warps loop measured 8%
+// slower on 128K tokens of 8 heads.
+constexpr int APPEND_CTAS = 6;
+constexpr int gather_ctas(int heads) { return heads == 4 ? 8 : 6; }
 constexpr int CACHE_UNROLL = 4;  // (token, head) pairs a warp has in flight
 
 struct CacheArgs {
@@ -61,8 +67,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// (min, -max) of this lane's 8 elements, as 16-bit values of the input's type;
-// NaN where there is a NaN.
+// Smaller and larger of pairs of 16-bit values of the input's type; NaN where
+// there is a NaN.
 template <bool BF16>
 __device__ __forceinline__ uint32_t least2(uint32_t a, uint32_t b) {
     if constexpr (BF16) {
@@ -75,6 +81,18 @@ __device__ __forceinline__ uint32_t least2(uint32_t a, uint32_t b) {
     }
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+        const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+}
+
 constexpr uint32_t SIGNS = 0x80008000u;  // of a pair of 16-bit values
 
 // The codes and the (scale, zero) pair of this lane's 8 channels; 16 / NG
@@ -83,25 +101,26 @@ template <bool BF16, int NG>
 __device__ __forceinline__ void quantise(const uint4 raw, uint32_t& codes, uint32_t& pair) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     const uint32_t lo = least2<BF16>(least2<BF16>(w[0], w[1]), least2<BF16>(w[2], w[3]));
-    const uint32_t up = least2<BF16>(least2<BF16>(w[0] ^ SIGNS, w[1] ^ SIGNS),
-                                     least2<BF16>(w[2] ^ SIGNS, w[3] ^ SIGNS));
+    const uint32_t up = SIGNS ^ most2<BF16>(most2<BF16>(w[0], w[1]), most2<BF16>(w[2], w[3]));
     uint32_t ends = least2<BF16>(__byte_perm(lo, up, 0x5410), __byte_perm(lo, up, 0x7632));
 #pragma unroll
     for (int o = 1; o < 16 / NG; o <<= 1) ends = least2<BF16>(ends, __shfl_xor_sync(FULL_MASK, ends, o));
     const float2 e = kv4_unpack2<BF16>(ends);
     float least = e.x, most = -e.y;
-    const bool finite = fabsf(least) < INFINITY && fabsf(most) < INFINITY;
-    bool clamp = false;
+    bool finite = true, clamp = false;
+    uint32_t zero_h = ends & 0xffffu;
     if (BF16) {
+        finite = fabsf(least) < INFINITY && fabsf(most) < INFINITY;
         clamp = least < -65504.f || most > 65504.f;
         least = fminf(fmaxf(least, -65504.f), 65504.f);
         most = fminf(fmaxf(most, -65504.f), 65504.f);
+        zero_h = __half_as_ushort(__float2half_rd(least));
     }
-    const __half zero_h = __float2half_rd(least);
-    const float zero = __half2float(zero_h);
+    const float zero = BF16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(zero_h))) : least;
     // Rounded up, so that below, where 15 times an fp16 value (exact in fp32)
     // is compared with it, the answer is the exact difference's.
     const float reach = __fsub_ru(most, zero);
+    if (!BF16) finite = reach < INFINITY;  // no: infinite or NaN
     // The fp16 value next to reach / 15, moved up if it is below it.
     __half scale_h = __float2half_rn(reach * (1.f / 15.f));
     if (15.f * __half2float(scale_h) < reach)
@@ -109,7 +128,7 @@ __device__ __forceinline__ void quantise(const uint4 raw, uint32_t& codes, uint3
     const float scale = __half2float(scale_h);
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
-    inv = scale > 0.f ? inv : 0.f;
+    inv = fminf(inv, 0x1p126f);  // scale 0: every element is the zero
     // Quotients by the reciprocal, put right by their remainder (Markstein's
     // correction): a quotient half way between two codes comes out exact, so
     // it is rounded to the even one.  Adding 1.5 * 2^23 leaves the code in the
@@ -135,59 +154,72 @@ __device__ __forceinline__ void quantise(const uint4 raw, uint32_t& codes, uint3
     }
     word -= MAGICS;
     codes = finite ? word : 0u;
-    pair = finite ? static_cast<uint32_t>(__half_as_ushort(scale_h)) | (static_cast<uint32_t>(__half_as_ushort(zero_h)) << 16)
-                  : 0x7fff7fffu;
+    pair = finite ? static_cast<uint32_t>(__half_as_ushort(scale_h)) | (zero_h << 16) : 0x7fff7fffu;
 }
 
-// (token, head) pairs u, u + 1, ..: the token and head of the first and a step
-// to the next without a division.
-struct Pair {
-    unsigned n, h;
-    __device__ __forceinline__ Pair(unsigned u, unsigned heads) : n(u / heads), h(u - n * heads) {}
-    __device__ __forceinline__ void next(unsigned heads) {
-        if (++h == heads) {
-            h = 0;
-            ++n;
-        }
-    }
+// Where a lane's word of codes and its group's pair lie in a record.
+struct LaneAt {
+    int word, flip, pair;
+    __device__ __forceinline__ LaneAt(int kv, int i, int ng)
+        : word(kv ? kv4_v_word(0, i) : kv4_k_word(0, i)), flip(kv ? 0x30 : 0), pair(kv4_param(0, kv, ng, i * ng / 16)) {}
+    // Token t's: the chunks of a V row change places with t, by an exclusive or.
+    __device__ __forceinline__ int word_of(int t) const { return t * KV4_ROW + (word ^ ((t << 3) & flip)); }
+    __device__ __forceinline__ int pair_of(int t, int ng) const { return t * 8 * ng + pair; }
 };
 
-template <bool BF16, int NG>
-__global__ void __launch_bounds__(CACHE_THREADS) kv4_append_kernel(const CacheArgs a) {
+// A warp's group of (token, head)s: T tokens from n on, H heads from h on.
+template <int H>
+struct Group {
+    static constexpr int T = CACHE_UNROLL / H;
+    unsigned n, h;
+    __device__ __forceinline__ Group(unsigned u, unsigned heads) {
+        const unsigned per_token = heads / H, q = u / per_token;
+        n = q * T;
+        h = (u - q * per_token) * H;
+    }
+    static __host__ __device__ long long count(long long N, int heads) { return (N + T - 1) / T * (heads / H); }
+};
+
+template <bool BF16, int NG, int H>
+__global__ void __launch_bounds__(CACHE_THREADS, APPEND_CTAS) kv4_append_kernel(const CacheArgs a) {
+    constexpr int T = Group<H>::T, R = kv4_record(NG);
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, kv = lane >> 4, i = lane & 15;
-    const unsigned warps = gridDim.x * (CACHE_THREADS / 32), heads = a.Hkv;
-    const unsigned pairs = static_cast<unsigned>(a.N) * heads;
+    const LaneAt lane_at(kv, i, NG);
+    const unsigned heads = a.Hkv, N = a.N;
+    const unsigned u = blockIdx.x * (CACHE_THREADS / 32) + (threadIdx.x >> 5);
+    if (u >= static_cast<unsigned>(Group<H>::count(N, heads))) return;
     const uint8_t* src = static_cast<const uint8_t*>(kv ? a.v : a.k) + 16 * i;
     const long long stride = 2 * (kv ? a.v_stride : a.k_stride);
+    const size_t block_bytes = static_cast<size_t>(heads) * R;
     bool bad = false;
-    for (unsigned u = (blockIdx.x * (CACHE_THREADS / 32) + (threadIdx.x >> 5)) * CACHE_UNROLL; u < pairs;
-         u += warps * CACHE_UNROLL) {
-        uint4 raw[CACHE_UNROLL];
-        int slot[CACHE_UNROLL];
-        unsigned head[CACHE_UNROLL];
-        Pair p(u, heads);
+    const Group<H> g(u, heads);
+    uint4 raw[T][H];
+    int slot[T];
 #pragma unroll
-        for (int x = 0; x < CACHE_UNROLL; ++x) {
-            slot[x] = -1;
-            head[x] = p.h;
-            if (u + x < pairs) {
-                slot[x] = __ldg(a.slots + p.n);
-                raw[x] = ld_stream(src + p.n * stride + p.h * (2 * KV4_D));
-            }
-            p.next(heads);
+    for (int t = 0; t < T; ++t) {
+        slot[t] = -1;
+        if (g.n + t < N) {
+            slot[t] = __ldg(a.slots + g.n + t);
+            const uint8_t* row = src + (g.n + t) * stride + g.h * (2 * KV4_D);
+#pragma unroll
+            for (int x = 0; x < H; ++x) raw[t][x] = ld_stream(row + x * (2 * KV4_D));
         }
+    }
 #pragma unroll
-        for (int x = 0; x < CACHE_UNROLL; ++x) {
-            const int s = checked_slot(slot[x], a.num_blocks, bad);
-            if (s < 0) continue;  // the whole warp
+    for (int t = 0; t < T; ++t) {
+        const int s = checked_slot(slot[t], a.num_blocks, bad);
+        if (s < 0) continue;  // the whole warp
+        uint8_t* rec = a.pool + (s / KV4_BLOCK) * block_bytes + g.h * R;
+        uint32_t* word = reinterpret_cast<uint32_t*>(rec + lane_at.word_of(s % KV4_BLOCK));
+        uint32_t* params = reinterpret_cast<uint32_t*>(rec + lane_at.pair_of(s % KV4_BLOCK, NG));
+#pragma unroll
+        for (int x = 0; x < H; ++x) {
             uint32_t codes, pair;
-            quantise<BF16, NG>(raw[x], codes, pair);
-            const int t = s % KV4_BLOCK;
-            uint8_t* rec = a.pool + (static_cast<size_t>(s / KV4_BLOCK) * heads + head[x]) * kv4_record(NG);
-            *reinterpret_cast<uint32_t*>(rec + (kv ? kv4_v_word(t, i) : kv4_k_word(t, i))) = codes;
-            if (i % (16 / NG) == 0) *reinterpret_cast<uint32_t*>(rec + kv4_param(t, kv, NG, i / (16 / NG))) = pair;
+            quantise<BF16, NG>(raw[t][x], codes, pair);
+            word[x * (R / 4)] = codes;
+            if (i % (16 / NG) == 0) params[x * (R / 4)] = pair;
         }
     }
     if (bad) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
@@ -236,55 +268,52 @@ __device__ __forceinline__ uint4 expand(uint32_t codes, uint32_t pair) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <bool BF16, int NG>
-__global__ void __launch_bounds__(CACHE_THREADS) kv4_gather_kernel(const CacheArgs a) {
+template <bool BF16, int NG, int H>
+__global__ void __launch_bounds__(CACHE_THREADS, gather_ctas(H)) kv4_gather_kernel(const CacheArgs a) {
+    constexpr int T = Group<H>::T, R = kv4_record(NG);
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, kv = lane >> 4, i = lane & 15;
-    const unsigned warps = gridDim.x * (CACHE_THREADS / 32), heads = a.Hkv;
-    const unsigned pairs = static_cast<unsigned>(a.N) * heads;
+    const LaneAt lane_at(kv, i, NG);
+    const unsigned heads = a.Hkv, N = a.N;
+    const unsigned u = blockIdx.x * (CACHE_THREADS / 32) + (threadIdx.x >> 5);
+    if (u >= static_cast<unsigned>(Group<H>::count(N, heads))) return;
     uint4* dst = static_cast<uint4*>(const_cast<void*>(kv ? a.v : a.k)) + i;
+    const size_t block_bytes = static_cast<size_t>(heads) * R;
     bool bad = false;
-    for (unsigned u = (blockIdx.x * (CACHE_THREADS / 32) + (threadIdx.x >> 5)) * CACHE_UNROLL; u < pairs;
-         u += warps * CACHE_UNROLL) {
-        uint32_t codes[CACHE_UNROLL], pair[CACHE_UNROLL];
-        int slot[CACHE_UNROLL];
-        Pair p(u, heads), q = p;
+    const Group<H> g(u, heads);
+    uint32_t codes[T][H], pair[T][H];
+    int slot[T];
 #pragma unroll
-        for (int x = 0; x < CACHE_UNROLL; ++x) {
-            slot[x] = u + x < pairs ? __ldg(a.slots + p.n) : -1;
-            p.next(heads);
-        }
+    for (int t = 0; t < T; ++t) slot[t] = g.n + t < N ? __ldg(a.slots + g.n + t) : -1;
 #pragma unroll
-        for (int x = 0; x < CACHE_UNROLL; ++x) {
-            const int s = checked_slot(slot[x], a.num_blocks, bad);
+    for (int t = 0; t < T; ++t) {
+        const int s = checked_slot(slot[t], a.num_blocks, bad);
+        const uint8_t* rec = a.pool + (max(s, 0) / KV4_BLOCK) * block_bytes + g.h * R;
+        const int tok = max(s, 0) % KV4_BLOCK;
+        const uint32_t* word = reinterpret_cast<const uint32_t*>(rec + lane_at.word_of(tok));
+        const uint32_t* params = reinterpret_cast<const uint32_t*>(rec + lane_at.pair_of(tok, NG));
+#pragma unroll
+        for (int x = 0; x < H; ++x) {
             // Code 0 of scale 0 and zero 0: a row of zeros.
-            codes[x] = pair[x] = 0u;
-            if (s >= 0) {
-                const int t = s % KV4_BLOCK;
-                const uint8_t* rec = a.pool + (static_cast<size_t>(s / KV4_BLOCK) * heads + q.h) * kv4_record(NG);
-                codes[x] = __ldg(reinterpret_cast<const uint32_t*>(rec + (kv ? kv4_v_word(t, i) : kv4_k_word(t, i))));
-                pair[x] = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_param(t, kv, NG, i / (16 / NG))));
-            }
-            q.next(heads);
+            codes[t][x] = s >= 0 ? __ldg(word + x * (R / 4)) : 0u;
+            pair[t][x] = s >= 0 ? __ldg(params + x * (R / 4)) : 0u;
         }
-#pragma unroll
-        for (int x = 0; x < CACHE_UNROLL; ++x)
-            if (u + x < pairs) dst[static_cast<size_t>(u + x) * 16] = expand<BF16>(codes[x], pair[x]);
     }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int x = 0; x < H; ++x)
+            if (g.n + t < N)
+                dst[(static_cast<size_t>(g.n + t) * heads + g.h + x) * 16] = expand<BF16>(codes[t][x], pair[t][x]);
     if (bad) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
 }
 
 using CacheKernel = void (*)(const CacheArgs);
 
-static clo_status launch_cache(CacheKernel kernel, const CacheArgs& a, cudaStream_t stream) {
-    const int sms = device_sm_count();
-    if (sms <= 0 || !prepare_kernel(reinterpret_cast<const void*>(kernel), 0)) return CLO_ERR_CUDA;
-    const long long units = static_cast<long long>(a.N) * a.Hkv;
-    constexpr int per_cta = CACHE_THREADS / 32 * CACHE_UNROLL;
-    long long grid = (units + per_cta - 1) / per_cta;
-    const long long most = static_cast<long long>(sms) * CACHE_CTAS_PER_SM;
-    if (grid > most) grid = most;
+static clo_status launch_cache(CacheKernel kernel, long long groups, const CacheArgs& a, cudaStream_t stream) {
+    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), 0)) return CLO_ERR_CUDA;
+    const long long grid = (groups + CACHE_THREADS / 32 - 1) / (CACHE_THREADS / 32);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(CACHE_THREADS), 0, stream, a) == cudaSuccess
                ? CLO_OK
                : CLO_ERR_CUDA;
@@ -306,13 +335,25 @@ static clo_status check_cache(const void* k, const void* v, clo_dtype dtype, con
     return CLO_OK;
 }
 
-template <bool BF16>
-static CacheKernel append_kernel(int ng) {
-    return ng == 1 ? kv4_append_kernel<BF16, 1> : ng == 2 ? kv4_append_kernel<BF16, 2> : kv4_append_kernel<BF16, 4>;
+template <bool BF16, int H>
+static CacheKernel cache_kernel(bool append, int ng) {
+    if (append)
+        return ng == 1 ? kv4_append_kernel<BF16, 1, H> : ng == 2 ? kv4_append_kernel<BF16, 2, H>
+                                                                 : kv4_append_kernel<BF16, 4, H>;
+    return ng == 1 ? kv4_gather_kernel<BF16, 1, H> : ng == 2 ? kv4_gather_kernel<BF16, 2, H>
+                                                             : kv4_gather_kernel<BF16, 4, H>;
 }
-template <bool BF16>
-static CacheKernel gather_kernel(int ng) {
-    return ng == 1 ? kv4_gather_kernel<BF16, 1> : ng == 2 ? kv4_gather_kernel<BF16, 2> : kv4_gather_kernel<BF16, 4>;
+
+template <int H>
+static clo_status run_cache_heads(bool append, clo_dtype dtype, int ng, const CacheArgs& a, cudaStream_t stream) {
+    return launch_cache(dtype == CLO_BF16 ? cache_kernel<true, H>(append, ng) : cache_kernel<false, H>(append, ng),
+                        Group<H>::count(a.N, a.Hkv), a, stream);
+}
+
+static clo_status run_cache(bool append, clo_dtype dtype, int ng, const CacheArgs& a, cudaStream_t stream) {
+    return a.Hkv % 4 == 0   ? run_cache_heads<4>(append, dtype, ng, a, stream)
+           : a.Hkv % 2 == 0 ? run_cache_heads<2>(append, dtype, ng, a, stream)
+                            : run_cache_heads<1>(append, dtype, ng, a, stream);
 }
 
 }  // namespace clo
@@ -336,8 +377,7 @@ extern "C" clo_status clo_kv4_append(const clo_kv4_append_args* args, cudaStream
         return CLO_ERR_INVALID_ARG;
     if (r.N == 0) return CLO_OK;
     CacheArgs a{r.k, r.v, r.k_stride, r.v_stride, r.pool, r.slot_map, r.err_flag, r.N, r.Hkv, r.num_blocks};
-    const int ng = kv4_groups(r.group);
-    return launch_cache(r.dtype == CLO_BF16 ? append_kernel<true>(ng) : append_kernel<false>(ng), a, stream);
+    return run_cache(true, r.dtype, kv4_groups(r.group), a, stream);
 }
 
 extern "C" clo_status clo_kv4_gather(const clo_kv4_gather_args* args, cudaStream_t stream) {
@@ -348,6 +388,5 @@ extern "C" clo_status clo_kv4_gather(const clo_kv4_gather_args* args, cudaStream
     if (st != CLO_OK) return st;
     if (r.N == 0) return CLO_OK;
     CacheArgs a{r.k, r.v, 0, 0, const_cast<uint8_t*>(r.pool), r.slot_map, r.err_flag, r.N, r.Hkv, r.num_blocks};
-    const int ng = kv4_groups(r.group);
-    return launch_cache(r.dtype == CLO_BF16 ? gather_kernel<true>(ng) : gather_kernel<false>(ng), a, stream);
+    return run_cache(false, r.dtype, kv4_groups(r.group), a, stream);
 }
