@@ -49,6 +49,8 @@ constexpr int KV4_WARPS = 4;
 constexpr int KV4_THREADS = KV4_WARPS * 32;
 constexpr int KV4_UNIT = 2 * KV4_BLOCK;  // tokens of a unit
 constexpr int KV4_MAX_ROWS = 32;   // query rows of a KV head: G * n_q
+constexpr int KV4_MERGE_THREADS = 512;
+constexpr int KV4_MERGE_UNROLL = 8;
 constexpr int KV4_PIECE_ROW = KV4_D + 4;  // floats of a row of a piece; the four behind: m, l
 constexpr int KV4_SMEM_PER_SM = 228 * 1024;
 constexpr int KV4_SMEM_RESERVED = 1024 + 256;  // of a CTA: the system's, and the static arrays
@@ -74,9 +76,10 @@ struct Kv4Args {
     float* ws_o;    // [2 * CTAs][rows][128] partial sums, head piece and tail piece of each CTA
     float* ws_first;  // [warps][rows][KV4_PIECE_ROW] piece of the set that ends in a warp but began before it
     float2* ws_ml;  // [2 * CTAs][rows] their (reference, denominator); denominator -1: bad data
-    int2* ws_tail;  // [CTAs] (token set, CTAs it covers) of the set that starts in this CTA and goes on, or covers 0
+    int2* ws_cut;   // what the merge finds its work by: see kv4_merge_kernel
     float scale_log2;
     int max_blocks, num_blocks, B, n_q, Hq, Hkv, G, rows;
+    bool by_set;    // ws_cut is by token set, else by CTA
 };
 
 __device__ __forceinline__ void mbar_init(uint32_t bar) {
@@ -137,7 +140,9 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     bool bad, any_bad = false;
     int mine = 0;
     for (int r = r0; r < r1; ++r) {
-        mine += kv4_steps(a, r, bad);
+        const int steps = kv4_steps(a, r, bad);
+        prefix[r + 1] = steps;
+        mine += steps;
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
@@ -153,7 +158,7 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     for (int w = 0; w < warp; ++w) run += wsum[w];
     if (threadIdx.x == 0) prefix[0] = 0;
     for (int r = r0; r < r1; ++r) {
-        run += kv4_steps(a, r, bad);
+        run += prefix[r + 1];
         prefix[r + 1] = run;
     }
     __syncthreads();
@@ -655,7 +660,6 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     if (lane < 2) piece_set[2 * warp + lane] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     pdl_wait();
-    pdl_launch_dependents();
     kv4_prefix(a, prefix, wsum);
 
     // Requests without a token (or with a bad length) get zeros.
@@ -666,6 +670,8 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             (reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row0 * KV4_D * 2))[i] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse != nullptr)
             for (int i = threadIdx.x; i < a.n_q * a.Hq; i += KV4_THREADS) a.lse[row0 + i] = -INFINITY;
+        if (a.by_set)
+            for (int h = threadIdx.x; h < a.Hkv; h += KV4_THREADS) a.ws_cut[r * a.Hkv + h] = make_int2(0, 0);
     }
 
     // Warp g of W takes the units of steps [N g / W, N (g + 1) / W).
@@ -803,12 +809,16 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             if (lane == 0) {
                 walk[1] = p;
                 if (!whole) piece_set[2 * warp + (last ? 1 : 0)] = set;
+                else if (a.by_set) a.ws_cut[set] = make_int2(0, 0);
             }
             __syncwarp();
             float* piece = whole ? nullptr : last ? reinterpret_cast<float*>(ring) : first_piece;
             end_set<BF16, NT, NG>(a, w, r, h, bad, piece, lane);
         }
     }
+    // Dependents start here, not earlier: blocks of the merge that wait on an SM
+    // would hold registers that CTAs of this grid or the next one need.
+    pdl_launch_dependents();
     __syncthreads();
 
     // The CTA's pieces, in the order of the stream; those of one token set are
@@ -841,6 +851,8 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
                 tail_ctas = static_cast<int>((static_cast<long long>(s1) * W - 1) / N / KV4_WARPS) -
                             static_cast<int>(blockIdx.x) + 1;
             }
+            if (a.by_set && s0 >= c0 && threadIdx.x == 0)  // it starts here
+                a.ws_cut[set] = make_int2(blockIdx.x, s1 > c1 ? tail_ctas : 0);
             for (int it = threadIdx.x; it < a.rows * (KV4_D / 4); it += KV4_THREADS) {
                 const int row = it / (KV4_D / 4), col = it % (KV4_D / 4);
                 float M = -INFINITY;
@@ -878,37 +890,42 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
         }
         i = end;
     }
-    if (threadIdx.x == 0) a.ws_tail[blockIdx.x] = make_int2(tail_set, tail_ctas);
+    if (!a.by_set && threadIdx.x == 0) a.ws_cut[blockIdx.x] = make_int2(tail_set, tail_ctas);
 }
 
-// Block (c, row) merges query row `row` of the token set that starts in CTA c
-// of the main kernel and goes on: its tail piece and the head pieces of the
-// CTAs behind it, in a fixed order.  A lane holds 4 channels; the warps take
-// the pieces in turn.
+// Merges the token sets that are cut by CTA boundaries, a query row of one an
+// item: the tail piece of the CTA it starts in and the head pieces of those
+// behind it, in a fixed order.  ws_cut, by token set: (CTA it starts in, CTAs
+// it covers, 0 if nothing is to merge); by CTA: (the set that starts in this one
+// and goes on, CTAs it covers).  An item has `share` warps (a power of 2), which
+// take its pieces in turn, KV4_MERGE_UNROLL loads in flight each; a lane holds 4
+// channels.
 template <bool BF16>
-__global__ void __launch_bounds__(KV4_THREADS) kv4_merge_kernel(const Kv4Args a) {
-    __shared__ float sm_m[KV4_WARPS], sm_l[KV4_WARPS];
-    __shared__ float4 sm_o[KV4_WARPS][32];
+__global__ void __launch_bounds__(KV4_MERGE_THREADS) kv4_merge_kernel(const Kv4Args a, int items, int share) {
+    constexpr int WARPS = KV4_MERGE_THREADS / 32, U = KV4_MERGE_UNROLL;
+    __shared__ float sm_m[WARPS], sm_l[WARPS];
+    __shared__ float4 sm_o[WARPS][32];
     pdl_launch_dependents();
     pdl_wait();
-    const int2 tail = a.ws_tail[blockIdx.x];
-    if (tail.y == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp & (share - 1);
+    const int item = blockIdx.x * (WARPS / share) + warp / share;
+    const int where = item / a.rows, row = item - where * a.rows;
+    const int2 cut = item < items ? a.ws_cut[where] : make_int2(0, 0);
+    const int set = a.by_set ? where : cut.x, cta = a.by_set ? cut.x : where, pieces = cut.y;
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool bad = false;
-    constexpr int U = 4;  // pieces a warp loads at a time
-    for (int p0 = warp; p0 < tail.y; p0 += KV4_WARPS * U) {
+    for (int p0 = part; p0 < pieces; p0 += share * U) {
         float2 ml[U];
         float4 v[U];
         float mx = M;
+        bool bad = L < 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int p = p0 + u * KV4_WARPS;
+            const int p = p0 + u * share;
             ml[u] = make_float2(-INFINITY, 0.f);
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p < tail.y) {
-                const size_t slot = 2 * (static_cast<size_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0);
+            if (p < pieces) {
+                const size_t slot = 2 * (static_cast<size_t>(cta) + p) + (p == 0 ? 1 : 0);
                 ml[u] = a.ws_ml[slot * a.rows + row];
                 v[u] = reinterpret_cast<const float4*>(a.ws_o + (slot * a.rows + row) * KV4_D)[lane];
             }
@@ -931,35 +948,41 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_merge_kernel(const Kv4Args a)
             O.w = fmaf(v[u].w, e, O.w);
         }
         M = mx;
+        if (bad) L = -1.f;
     }
-    if (lane == 0) {
-        sm_m[warp] = M;
-        sm_l[warp] = L;
+    if (share > 1) {
+        if (lane == 0) {
+            sm_m[warp] = M;
+            sm_l[warp] = L;
+        }
+        sm_o[warp][lane] = O;
+        __syncthreads();
+        if (part != 0) return;
+        float top = M;
+        for (int x = 1; x < share; ++x) top = fmaxf(top, sm_m[warp + x]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        bool bad = false;
+        L = 0.f;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < share; ++x) {
+            const float e = fast_exp2(sm_m[warp + x] - ref), l = sm_l[warp + x];
+            const float4 v = sm_o[warp + x][lane];
+            bad |= l == -1.f;
+            L = fmaf(l, e, L);
+            O.x = fmaf(v.x, e, O.x);
+            O.y = fmaf(v.y, e, O.y);
+            O.z = fmaf(v.z, e, O.z);
+            O.w = fmaf(v.w, e, O.w);
+        }
+        M = top;
+        if (bad) L = -1.f;
     }
-    sm_o[warp][lane] = O;
-    bad = __syncthreads_or(bad) != 0;
-    if (warp != 0) return;
-    float top = M;
-#pragma unroll
-    for (int x = 1; x < KV4_WARPS; ++x) top = fmaxf(top, sm_m[x]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    L = 0.f;
-    O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int x = 0; x < KV4_WARPS; ++x) {
-        const float e = fast_exp2(sm_m[x] - ref);
-        const float4 v = sm_o[x][lane];
-        L = fmaf(sm_l[x], e, L);
-        O.x = fmaf(v.x, e, O.x);
-        O.y = fmaf(v.y, e, O.y);
-        O.z = fmaf(v.z, e, O.z);
-        O.w = fmaf(v.w, e, O.w);
-    }
-    const bool none = bad || L == 0.f;
-    const int r = tail.x / a.Hkv, h = tail.x - r * a.Hkv;
+    if (pieces == 0) return;
+    const bool none = L == -1.f || L == 0.f;
+    const int r = set / a.Hkv, h = set - r * a.Hkv;
     const size_t orow = kv4_out_row(a, r, h, row);
     store4<BF16>(a, orow, lane, O, none ? 0.f : 1.f / L, none);
-    if (a.lse != nullptr && lane == 0) a.lse[orow] = kv4_lse(top, L, none);
+    if (a.lse != nullptr && lane == 0) a.lse[orow] = kv4_lse(M, L, none);
 }
 
 using Kv4Kernel = void (*)(const Kv4Args);
@@ -1051,12 +1074,21 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, c
         return CLO_ERR_WORKSPACE;
     if (ctas <= 0) return CLO_ERR_CUDA;
 
+    // Few sets are cut into many pieces each: the merge goes by set.  Many
+    // are cut into two or three: it goes by the cuts between CTAs.
+    const int sets = B * Hkv;
+    a.by_set = sets < ctas;
+    // Enough warps an item to load the pieces of an average set at once.
+    int share = 1;
+    while (share < KV4_MERGE_THREADS / 32 && share * KV4_MERGE_UNROLL < ctas / sets + 1) share *= 2;
+    const int items = (a.by_set ? sets : ctas - 1) * a.rows;
+    const int per_block = KV4_MERGE_THREADS / 32 / share;
     const size_t slots = 2 * static_cast<size_t>(ctas) * a.rows;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.ws_o = reinterpret_cast<float*>(ws);
     a.ws_ml = reinterpret_cast<float2*>(ws + round256(slots * KV4_D * sizeof(float)));
-    a.ws_tail = reinterpret_cast<int2*>(ws + round256(slots * KV4_D * sizeof(float)) + round256(slots * sizeof(float2)));
-    a.ws_first = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws_tail) +
+    a.ws_cut = reinterpret_cast<int2*>(ws + round256(slots * KV4_D * sizeof(float)) + round256(slots * sizeof(float2)));
+    a.ws_first = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws_cut) +
                                           round256(static_cast<size_t>(ctas) * sizeof(int2)));
     a.q = q;
     a.out = out;
@@ -1074,7 +1106,7 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, c
     a.Hkv = Hkv;
     a.G = Hq / Hkv;
     const Kv4Kernel kernel = dtype == CLO_BF16 ? attn_kernel<true>(nt, ng) : attn_kernel<false>(nt, ng);
-    const Kv4Kernel merge = dtype == CLO_BF16 ? kv4_merge_kernel<true> : kv4_merge_kernel<false>;
+    const auto merge = dtype == CLO_BF16 ? kv4_merge_kernel<true> : kv4_merge_kernel<false>;
     if (!prepare_kernel(reinterpret_cast<const void*>(kernel), kv4_layout(nt, ng, a.rows, KV4_MAX_B).total) ||
         !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
         return CLO_ERR_CUDA;
@@ -1082,7 +1114,8 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, c
     if (launch_pdl(kernel, dim3(ctas), dim3(KV4_THREADS), smem, stream, a) != cudaSuccess) return CLO_ERR_CUDA;
     if (opts != nullptr && opts->ev_end != nullptr && !record_event(opts->ev_end, stream)) return CLO_ERR_CUDA;
     if (ctas > 1 &&
-        launch_pdl(merge, dim3(ctas - 1, a.rows), dim3(KV4_THREADS), 0, stream, a) != cudaSuccess)
+        launch_pdl(merge, dim3((items + per_block - 1) / per_block), dim3(KV4_MERGE_THREADS), 0, stream, a, items, share) !=
+            cudaSuccess)
         return CLO_ERR_CUDA;
     return CLO_OK;
 }
