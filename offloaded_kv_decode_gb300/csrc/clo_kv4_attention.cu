@@ -49,6 +49,7 @@ constexpr int KV4_WARPS = 4;
 constexpr int KV4_THREADS = KV4_WARPS * 32;
 constexpr int KV4_UNIT = 2 * KV4_BLOCK;  // tokens of a unit
 constexpr int KV4_MAX_ROWS = 32;   // query rows of a KV head: G * n_q
+constexpr int KV4_MAX_CTAS = 16383;  // warps squared stay in 32 bits
 constexpr int KV4_MERGE_THREADS = 512;
 constexpr int KV4_MERGE_UNROLL = 8;
 constexpr int KV4_PIECE_ROW = KV4_D + 4;  // floats of a row of a piece; the four behind: m, l
@@ -163,6 +164,23 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     }
     __syncthreads();
 }
+
+// W warps share N steps: warp g from at(g) on, that is floor(N g / W), in 32 bits.
+struct Kv4Split {
+    unsigned N, W, each, rest;
+    __device__ __forceinline__ Kv4Split(int steps, unsigned warps) : N(steps), W(min(warps, N)) {
+        each = W > 0 ? N / W : 0u;
+        rest = N - each * W;
+    }
+    __device__ __forceinline__ int at(unsigned g) const { return g < W ? each * g + rest * g / W : N; }
+    // The warp that step t < N belongs to.
+    __device__ __forceinline__ unsigned owner(int t) const {
+        unsigned g = min(W - 1, static_cast<unsigned>(static_cast<float>(t) / static_cast<float>(N) * static_cast<float>(W)));
+        while (g > 0 && at(g) > t) --g;
+        while (g + 1 < W && at(g + 1) <= t) ++g;
+        return g;
+    }
+};
 
 // A unit: j of nt of request r's head h.
 struct Place {
@@ -648,7 +666,8 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int wsum[KV4_WARPS];
     __shared__ Place walks[KV4_WARPS][3];
-    __shared__ int piece_set[2 * KV4_WARPS];  // token set of each warp's first and last piece, or -1
+    __shared__ int4 piece_of[2 * KV4_WARPS];  // (token set, request, its units' first step, the step behind them) of
+                                              // each warp's first and last piece; set -1: none
     constexpr int R = kv4_record(NG), STAGES = kv4_stages(NG);
     const Kv4Layout y = kv4_layout(NT, NG, a.rows, a.B);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -657,7 +676,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     int* prefix = reinterpret_cast<int*>(smem + y.prefix);
 
     if (lane < STAGES) mbar_init(bars + lane * 8);
-    if (lane < 2) piece_set[2 * warp + lane] = -1;
+    if (lane < 2) piece_of[2 * warp + lane] = make_int4(-1, 0, 0, 0);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     pdl_wait();
     kv4_prefix(a, prefix, wsum);
@@ -674,49 +693,45 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             for (int h = threadIdx.x; h < a.Hkv; h += KV4_THREADS) a.ws_cut[r * a.Hkv + h] = make_int2(0, 0);
     }
 
-    // Warp g of W takes the units of steps [N g / W, N (g + 1) / W).
-    const long long N = prefix[a.B];
-    const long long W = min(static_cast<long long>(gridDim.x) * KV4_WARPS, N);
-    const long long g0 = static_cast<long long>(blockIdx.x) * KV4_WARPS;
-    const long long g = g0 + warp;
-    const int x0 = g < W ? static_cast<int>(N * g / W) : 0;
-    const int x1 = g < W ? static_cast<int>(N * (g + 1) / W) : 0;
+    // Warp g takes the units of steps [split.at(g), split.at(g + 1)).
+    const Kv4Split split(prefix[a.B], gridDim.x * KV4_WARPS);
+    const unsigned g0 = blockIdx.x * KV4_WARPS, g = g0 + warp;
+    const int x0 = split.at(g), x1 = split.at(g + 1);
     // Where this warp's range begins and ends, and where its loads and its
     // computation stand: read when one goes on to another token set.
     Place* const walk = walks[warp];
-    {
-        const Place begin = kv4_place(prefix, a.B, a.Hkv, x0), end = kv4_place(prefix, a.B, a.Hkv, x1);
+    float* first_piece = a.ws_first + static_cast<size_t>(g) * a.rows * KV4_PIECE_ROW;
+    const Place begin = kv4_place(prefix, a.B, a.Hkv, x0);
+    // ---- loads.  Lane i holds entry `at0` + i of the row of block ids; the next
+    // unit is entries at0 + at and the one behind it.
+    int ids = 0, at = 0, to_load = 0;     // to_load: units of this set that are still to load
+    const uint8_t* head_pool = nullptr;   // the pool from this KV head's record on
+    const int32_t* row = nullptr;         // the request's ids from at0 on, and how many there are
+    int row_left = 0;
+    auto load_ids = [&]() {
+        if (lane < row_left) ids = __ldg(row + lane);
+        if (lane == 0 && row_left > 32) prefetch_l1(row + 32);
+        at = 0;
+    };
+    auto start_row = [&](const Place& p) {
+        row = a.table + static_cast<size_t>(p.r) * a.max_blocks + 2 * p.j;
+        row_left = (__ldg(a.ctx_len + p.r) + KV4_BLOCK - 1) / KV4_BLOCK - 2 * p.j;
+        head_pool = a.pool + static_cast<size_t>(p.h) * R;
+        load_ids();
+    };
+    if (x0 < x1 && begin.r < a.B) {
+        start_row(begin);
+        const Place end = kv4_place(prefix, a.B, a.Hkv, x1);
+        const bool one_set = begin.r == end.r && begin.h == end.h;
+        to_load = (one_set ? end.j : begin.nt) - begin.j;
         if (lane == 0) {
             walk[0] = walk[1] = begin;
             walk[2] = end;
         }
+        __syncwarp();
     }
-    __syncwarp();
-    const bool any = x0 < x1 && (walk[0].r != walk[2].r || walk[0].h != walk[2].h || walk[0].j != walk[2].j);
-    float* first_piece = a.ws_first + static_cast<size_t>(g) * a.rows * KV4_PIECE_ROW;
-    if (any) {
+    if (to_load > 0) {
         const uint64_t policy = l2_evict_first_policy();
-        // ---- loads.  Lane i holds entry `at0` + i of the row of block ids (-1
-        // behind its last block, -2 for an id that is none); the next unit is
-        // entries at0 + at and the one behind it.
-        int ids, at, to_load;       // to_load: units of this set that are still to load
-        const uint8_t* head_pool;   // the pool from this KV head's record on
-        const int32_t* row;         // the request's ids from at0 on, and how many there are
-        int row_left;
-        auto load_ids = [&]() {
-            ids = lane < row_left ? __ldg(row + lane) : -1;
-            if (lane < row_left && (ids < 0 || ids >= a.num_blocks)) ids = -2;
-            if (lane == 0 && row_left > 32) prefetch_l1(row + 32);
-            at = 0;
-        };
-        auto start_loads = [&](const Place& p) {
-            row = a.table + static_cast<size_t>(p.r) * a.max_blocks + 2 * p.j;
-            row_left = (__ldg(a.ctx_len + p.r) + KV4_BLOCK - 1) / KV4_BLOCK - 2 * p.j;
-            head_pool = a.pool + static_cast<size_t>(p.h) * R;
-            to_load = (p.r == walk[2].r && p.h == walk[2].h ? walk[2].j : p.nt) - p.j;
-            load_ids();
-        };
-        start_loads(walk[0]);
         uint32_t bad_slots = 0;  // stages with a record that does not exist
         const size_t block_bytes = static_cast<size_t>(a.Hkv) * R;
         auto issue = [&](int stage) {
@@ -727,16 +742,18 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             }
             // Lanes 0 and 1 take the unit's two blocks; the second may be behind the last one.
             const int id = __shfl_sync(FULL_MASK, ids, at + (lane & 1));
-            const uint32_t have = __ballot_sync(FULL_MASK, id >= 0) & 3u;
+            const bool exists = at + (lane & 1) < row_left;
+            const bool ok = exists && static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks);
+            const uint32_t have = __ballot_sync(FULL_MASK, ok) & 3u;
             bad_slots &= ~(1u << stage);
-            if (__any_sync(FULL_MASK, id == -2)) bad_slots |= 1u << stage;
+            if (__any_sync(FULL_MASK, exists && !ok)) bad_slots |= 1u << stage;
             const uint32_t bar = bars + stage * 8;
             if (lane == 0) {
                 if (have != 0u) mbar_expect(bar, have == 3u ? 2 * R : R);
                 else mbar_arrive(bar);
             }
             __syncwarp();
-            if (lane < 2 && id >= 0)
+            if (lane < 2 && ok)
                 bulk_load(smem_u32(ring) + (2 * stage + lane) * R, head_pool + id * block_bytes, R, bar, policy);
             at += 2;
             if (--to_load == 0) {  // on to the next set, if its first unit is this warp's
@@ -748,7 +765,8 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
                 __syncwarp();
                 if (lane == 0) walk[0] = p;
                 __syncwarp();
-                start_loads(p);
+                start_row(p);
+                to_load = p.r == end.r && p.h == end.h ? end.j : p.nt;
                 prefetch_queries(a, p, lane);
             }
         };
@@ -798,7 +816,8 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             }
             Place p = walk[1];
             const Place end = walk[2];
-            const int set = p.r * a.Hkv + p.h, r = p.r, h = p.h;
+            const int set = p.r * a.Hkv + p.h, r = p.r, h = p.h, nt = p.nt;
+            const int s0 = prefix[r] + h * (nt + KV4_SET_COST) + KV4_SET_COST;  // the first unit's step
             const bool ends_here = !(p.r == end.r && p.h == end.h), whole = ends_here && p.j == 0;
             last = !ends_here;
             if (ends_here) {
@@ -808,7 +827,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
             __syncwarp();
             if (lane == 0) {
                 walk[1] = p;
-                if (!whole) piece_set[2 * warp + (last ? 1 : 0)] = set;
+                if (!whole) piece_of[2 * warp + (last ? 1 : 0)] = make_int4(set, r, s0, s0 + nt);
                 else if (a.by_set) a.ws_cut[set] = make_int2(0, 0);
             }
             __syncwarp();
@@ -821,74 +840,72 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     pdl_launch_dependents();
     __syncthreads();
 
-    // The CTA's pieces, in the order of the stream; those of one token set are
-    // next to each other.
-    const int c0 = g0 < W ? static_cast<int>(N * g0 / W) : 0;  // the CTA's steps
-    const int c1 = g0 < W ? static_cast<int>(N * min(g0 + KV4_WARPS, W) / W) : 0;
-    // Each warp's last piece is in shared memory, its first one (written in
-    // this CTA too) in the workspace.
-    auto piece_at = [&](int k) {
-        return (k & 1) ? reinterpret_cast<const float*>(smem + (k >> 1) * y.warp)
-                       : a.ws_first + static_cast<size_t>(g0 + (k >> 1)) * a.rows * KV4_PIECE_ROW;
-    };
+    // The CTA's pieces: each token set at its first one.  A warp's last piece is
+    // in shared memory, its first one (written in this CTA too) in the workspace.
+    const int c0 = split.at(g0), c1 = split.at(g0 + KV4_WARPS);  // the CTA's steps
+    int sets[2 * KV4_WARPS];
+#pragma unroll
+    for (int k = 0; k < 2 * KV4_WARPS; ++k) sets[k] = piece_of[k].x;
     int tail_set = 0, tail_ctas = 0;
-    for (int i = 0; i < 2 * KV4_WARPS;) {
-        const int set = piece_set[i];
-        int end = i + 1;
-        if (set >= 0) {
-            // -1 entries between two pieces of a set: a warp that has one piece only
-            for (int k = end; k < 2 * KV4_WARPS; ++k) {
-                if (piece_set[k] == set) end = k + 1;
-                else if (piece_set[k] >= 0) break;
-            }
-            const int r = set / a.Hkv, h = set - r * a.Hkv;
-            const int steps = (prefix[r + 1] - prefix[r]) / a.Hkv;
-            const int s0 = prefix[r] + h * steps + KV4_SET_COST, s1 = prefix[r] + (h + 1) * steps;  // its units' steps
-            const bool done = s0 >= c0 && s1 <= c1;
-            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s0 < c0 ? 0 : 1);
-            if (s0 >= c0 && s1 > c1) {
-                tail_set = set;
-                tail_ctas = static_cast<int>((static_cast<long long>(s1) * W - 1) / N / KV4_WARPS) -
-                            static_cast<int>(blockIdx.x) + 1;
-            }
-            if (a.by_set && s0 >= c0 && threadIdx.x == 0)  // it starts here
-                a.ws_cut[set] = make_int2(blockIdx.x, s1 > c1 ? tail_ctas : 0);
-            for (int it = threadIdx.x; it < a.rows * (KV4_D / 4); it += KV4_THREADS) {
-                const int row = it / (KV4_D / 4), col = it % (KV4_D / 4);
-                float M = -INFINITY;
-                bool bad = false;
-                for (int k = i; k < end; ++k)
-                    if (piece_set[k] == set) {
-                        const float* pc = piece_at(k);
-                        M = fmaxf(M, pc[row * KV4_PIECE_ROW + KV4_D]);
-                        bad |= pc[row * KV4_PIECE_ROW + KV4_D + 1] == -1.f;
-                    }
-                float L = 0.f;
-                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float ref = M == -INFINITY ? 0.f : M;
-                for (int k = i; k < end; ++k)
-                    if (piece_set[k] == set) {
-                        const float* pc = piece_at(k);
-                        const float e = fast_exp2(pc[row * KV4_PIECE_ROW + KV4_D] - ref);
-                        const float4 v = *reinterpret_cast<const float4*>(pc + row * KV4_PIECE_ROW + 4 * col);
-                        L = fmaf(pc[row * KV4_PIECE_ROW + KV4_D + 1], e, L);
-                        O.x = fmaf(v.x, e, O.x);
-                        O.y = fmaf(v.y, e, O.y);
-                        O.z = fmaf(v.z, e, O.z);
-                        O.w = fmaf(v.w, e, O.w);
-                    }
-                if (done) {
-                    const bool none = bad || L == 0.f;
-                    const size_t orow = kv4_out_row(a, r, h, row);
-                    store4<BF16>(a, orow, col, O, none ? 0.f : 1.f / L, none);
-                    if (a.lse != nullptr && col == 0) a.lse[orow] = kv4_lse(M, L, none);
-                } else {
-                    *reinterpret_cast<float4*>(a.ws_o + (slot * a.rows + row) * KV4_D + 4 * col) = O;
-                    if (col == 0) a.ws_ml[slot * a.rows + row] = make_float2(M, bad ? -1.f : L);
+#pragma unroll 1
+    for (int i = 0; i < 2 * KV4_WARPS; ++i) {
+        const int4 piece = piece_of[i];
+        const int set = piece.x;
+        bool again = set < 0;
+#pragma unroll
+        for (int k = 0; k < 2 * KV4_WARPS - 1; ++k) again |= k < i && sets[k] == set;
+        if (again) continue;
+        const int r = piece.y, s0 = piece.z, s1 = piece.w, h = set - r * a.Hkv;
+        const bool starts = s0 >= c0, goes_on = s1 > c1;
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0);
+        int covers = 0;
+        if (starts && goes_on) {
+            covers = static_cast<int>(split.owner(s1 - 1) / KV4_WARPS) - static_cast<int>(blockIdx.x) + 1;
+            tail_set = set;
+            tail_ctas = covers;
+        }
+        if (a.by_set && starts && threadIdx.x == 0) a.ws_cut[set] = make_int2(blockIdx.x, covers);
+        for (int it = threadIdx.x; it < a.rows * (KV4_D / 4); it += KV4_THREADS) {
+            const int row = it / (KV4_D / 4), col = it % (KV4_D / 4);
+            float2 ml[2 * KV4_WARPS];
+            float4 v[2 * KV4_WARPS];
+            float M = -INFINITY;
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 2 * KV4_WARPS; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (sets[k] == set) {
+                    const float* pc = (k & 1) ? reinterpret_cast<const float*>(smem + (k >> 1) * y.warp)
+                                              : a.ws_first + static_cast<size_t>(g0 + (k >> 1)) * a.rows * KV4_PIECE_ROW;
+                    ml[k] = *reinterpret_cast<const float2*>(pc + row * KV4_PIECE_ROW + KV4_D);
+                    v[k] = *reinterpret_cast<const float4*>(pc + row * KV4_PIECE_ROW + 4 * col);
                 }
+                M = fmaxf(M, ml[k].x);
+                bad |= ml[k].y == -1.f;
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 2 * KV4_WARPS; ++k) {
+                const float e = kv4_exp2(ml[k].x - ref);
+                L = fmaf(ml[k].y, e, L);
+                O.x = fmaf(v[k].x, e, O.x);
+                O.y = fmaf(v[k].y, e, O.y);
+                O.z = fmaf(v[k].z, e, O.z);
+                O.w = fmaf(v[k].w, e, O.w);
+            }
+            if (starts && !goes_on) {
+                const bool none = bad || L == 0.f;
+                const size_t orow = kv4_out_row(a, r, h, row);
+                store4<BF16>(a, orow, col, O, none ? 0.f : 1.f / L, none);
+                if (a.lse != nullptr && col == 0) a.lse[orow] = kv4_lse(M, L, none);
+            } else {
+                *reinterpret_cast<float4*>(a.ws_o + (slot * a.rows + row) * KV4_D + 4 * col) = O;
+                if (col == 0) a.ws_ml[slot * a.rows + row] = make_float2(M, bad ? -1.f : L);
             }
         }
-        i = end;
     }
     if (!a.by_set && threadIdx.x == 0) a.ws_cut[blockIdx.x] = make_int2(tail_set, tail_ctas);
 }
@@ -1057,7 +1074,7 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, c
     if (blocks >= (1ll << 31) || max_blocks > (1 << 26) ||
         units + static_cast<long long>(B) * Hkv * KV4_SET_COST >= (1ll << 31))
         return CLO_ERR_UNSUPPORTED;
-    if (opts != nullptr && opts->num_ctas > (1 << 20)) return CLO_ERR_UNSUPPORTED;
+    if (opts != nullptr && opts->num_ctas > KV4_MAX_CTAS) return CLO_ERR_UNSUPPORTED;
     if (B == 0) return CLO_OK;
 
     Kv4Args a;
