@@ -22,13 +22,21 @@ def inputs(ctx, n_q, Hq, Hkv, group, dt, seed, spread=1.0, mb=None):
     mb = mb or max(1, int(-(-ctx.max() // 16)))
     nb = B * mb + 2
     R = ref.record_bytes(group)
+    table = rng.permutation(nb - 2).reshape(B, mb) + 1
+    if mb > 1000:  # a wide table: only blocks in use are made
+        used = int(sum(-(-int(c) // 16) for c in ctx))
+        nb, at, wide = used + 2, 1, np.full((B, mb), -7)
+        for r in range(B):
+            n = -(-int(ctx[r]) // 16)
+            wide[r, :n] = np.arange(at, at + n)
+            at += n
+        table = wide
     pool = rng.integers(0, 256, (nb, Hkv, R), dtype=np.uint8)
     pool[:, :, :2048] = (pool[:, :, :2048] & 0x77) + (rng.integers(0, 256, (nb, Hkv, 2048), dtype=np.uint8) & 0x77)
     scale = rng.uniform(0.05, 0.4, (nb, Hkv, 16, 2, 128 // group))
     scale[:, :, :, 1] *= np.minimum(spread ** rng.standard_normal((nb, Hkv, 16, 1)), 2000.0)  # V; fp16 holds it
     zero = -scale * rng.normal(7.5, 1.0, scale.shape)
     par = np.stack([scale, zero], -1).astype(np.float16)
-    table = rng.permutation(nb - 2).reshape(B, mb) + 1
     live = np.zeros((nb, 16), bool)
     for r in range(B):
         for c in range(-(-int(ctx[r]) // 16)):
@@ -86,6 +94,21 @@ def test_head_layouts(n_q, Hq, Hkv, group, dtype):
 @pytest.mark.parametrize("ctx", [[1], [16], [2000], [0, 5, 0, 700, 1, 0], [31, 32, 33, 1, 1, 900, 2, 47]])
 def test_lengths_and_splits(ctx, num_ctas):
     check(ctx, 1, 8, 2, 64, "f16", 5, num_ctas)
+
+
+@pytest.mark.parametrize("n_q,group", [(1, 128), (1, 32), (3, 64), (8, 64)])
+def test_short_contexts_in_a_wide_table(n_q, group):
+    """The same requests with a table that just holds them and with one for far
+    longer contexts: the two take different ways, and both meet the tolerance."""
+    ctx = [0, 1, 16, 33, 500, 1023, 700, 2]
+    for mb in (None, 5000):
+        check(ctx, n_q, 8, 2, group, "f16", 31 + n_q, mb=mb)
+
+
+@pytest.mark.parametrize("ctx", [[64], [128, 100], [300, 256, 40], [1000, 10], [2048], [4000, 3000, 17]])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (16, 4), (64, 64)])
+def test_short_contexts_of_all_sizes(ctx, Hq, Hkv):
+    check(ctx, 1, Hq, Hkv, 64, "bf16", Hq + len(ctx))
 
 
 @pytest.mark.parametrize("num_ctas", [0, 3, 40])
