@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
                 const bool came = mbar_wait(bars + stage * 8, parity);
                 if (came && ((bad_slots >> stage) & 1u) == 0u) {
                     const uint8_t* rec = ring + 2 * stage * R;
-                    constexpr int NB = NT == 4 ? 1 : 2;  // registers
+                    constexpr int NB = NT >= 2 ? 1 : 2;  // registers
 #pragma unroll
                     for (int b = 0; b < 2; b += NB) {
                         const int from_here = left - b * KV4_BLOCK;

@@ -261,6 +261,29 @@ __device__ __forceinline__ uint32_t kv4_transpose(uint32_t a) {
     return d;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n" : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " mul.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n" : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n" : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 __device__ __forceinline__ __half2 kv4_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
 // The NG (scale, zero) pairs of one token's K (kv = 0) or V, as stored.
@@ -339,25 +362,35 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x[nt][b][k] = g == 0 ? f[k >> 1] * s[nt][k] : fmaf(f[k >> 1], s[nt][k], x[nt][b][k]);
+                for (int k = 0; k < 4; k += 2) {
+                    const float2 ff = make_float2(f[k >> 1], f[k >> 1]), ss = make_float2(s[nt][k], s[nt][k + 1]);
+                    const float2 y = g == 0 ? mul2(ff, ss) : fma2(ff, ss, make_float2(x[nt][b][k], x[nt][b][k + 1]));
+                    x[nt][b][k] = y.x;
+                    x[nt][b][k + 1] = y.y;
+                }
             }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float2 factor = qs.factor(nt, c);
-            float y[4];
+            float2 y[2];
+            const float2 ref = make_float2(-w.m[nt][0], -w.m[nt][1]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = fmaf(x[nt][b][k], (k & 1) ? factor.y : factor.x, -w.m[nt][k & 1]);
+            for (int t = 0; t < 2; ++t) y[t] = fma2(make_float2(x[nt][b][2 * t], x[nt][b][2 * t + 1]), factor, ref);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const float2 sum = qs.sum(nt, g, c);
-                const float z[2] = {__high2float(kv4_half2(kp[0][g])), __high2float(kv4_half2(kp[1][g]))};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = fmaf(z[k >> 1], (k & 1) ? sum.y : sum.x, y[k]);
+                for (int t = 0; t < 2; ++t) {
+                    const float z = __high2float(kv4_half2(kp[t][g]));
+                    y[t] = fma2(make_float2(z, z), sum, y[t]);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[nt][b][k] = y[k];
+            for (int t = 0; t < 2; ++t) {
+                x[nt][b][2 * t] = y[t].x;
+                x[nt][b][2 * t + 1] = y[t].y;
+            }
         }
     }
     bool hot = first;
@@ -365,13 +398,13 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
     for (int nt = 0; nt < NT; ++nt) {
         float over = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 2 * NB; ++t)
-#pragma unroll
-            for (int col = 0; col < 2; ++col) {
-                float& v = x[nt][t >> 1][2 * (t & 1) + col];
-                if (EDGE && !sees(nt, t, col)) v = -INFINITY;
-                over = fmaxf(over, v + big[t]);
-            }
+        for (int t = 0; t < 2 * NB; ++t) {
+            float* v = &x[nt][t >> 1][2 * (t & 1)];
+            if (EDGE && !sees(nt, t, 0)) v[0] = -INFINITY;
+            if (EDGE && !sees(nt, t, 1)) v[1] = -INFINITY;
+            const float2 y = add2(make_float2(v[0], v[1]), make_float2(big[t], big[t]));
+            over = fmaxf(over, fmaxf(y.x, y.y));
+        }
         hot |= over > KV4_SLACK;
     }
     if (__any_sync(FULL_MASK, hot)) {  // the reference moves
@@ -411,8 +444,10 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[nt][b][k] = kv4_exp2(x[nt][b][k]);
-            w.l[nt][0] += x[nt][b][0] + x[nt][b][2];
-            w.l[nt][1] += x[nt][b][1] + x[nt][b][3];
+            const float2 l = add2(make_float2(w.l[nt][0], w.l[nt][1]), add2(make_float2(x[nt][b][0], x[nt][b][1]),
+                                                                            make_float2(x[nt][b][2], x[nt][b][3])));
+            w.l[nt][0] = l.x;
+            w.l[nt][1] = l.y;
         }
         uint32_t vp[2][NG];
 #pragma unroll
@@ -428,13 +463,27 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float y[4];
+                    if constexpr (EDGE) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // A query that does not see a token takes nothing from it, not even a NaN.
-                        const bool in = sees(nt, 2 * b + (k >> 1), k & 1);
-                        float& z = w.z[nt][k & 1][g];
-                        y[k] = in ? x[nt][b][k] * f[k >> 1].x : 0.f;
-                        z = in ? fmaf(x[nt][b][k], f[k >> 1].y, z) : z;
+                        for (int k = 0; k < 4; ++k) {
+                            // A query that does not see a token takes nothing from it, not even a NaN.
+                            const bool in = sees(nt, 2 * b + (k >> 1), k & 1);
+                            float& z = w.z[nt][k & 1][g];
+                            y[k] = in ? x[nt][b][k] * f[k >> 1].x : 0.f;
+                            z = in ? fmaf(x[nt][b][k], f[k >> 1].y, z) : z;
+                        }
+                    } else {
+                        float2 z = make_float2(w.z[nt][0][g], w.z[nt][1][g]);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const float2 p = make_float2(x[nt][b][2 * t], x[nt][b][2 * t + 1]);
+                            const float2 v2 = mul2(p, make_float2(f[t].x, f[t].x));
+                            y[2 * t] = v2.x;
+                            y[2 * t + 1] = v2.y;
+                            z = fma2(p, make_float2(f[t].y, f[t].y), z);
+                        }
+                        w.z[nt][0][g] = z.x;
+                        w.z[nt][1][g] = z.y;
                     }
                     pb[nt][0] = kv4_transpose(pack_half2(y[0], y[1]));  // tokens 0-7
                     pb[nt][1] = kv4_transpose(pack_half2(y[2], y[3]));  // tokens 8-15

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
                 if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
             } else {
                 const uint8_t* rec = ring + 2 * stage * R;
-                constexpr int NB = NT == 4 ? 1 : 2;  // registers
+                constexpr int NB = NT >= 2 ? 1 : 2;  // registers
 #pragma unroll
                 for (int b = 0; b < 2; b += NB) {
                     const int from_here = left - b * KV4_BLOCK;
