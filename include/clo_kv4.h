@@ -210,7 +210,7 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  *              queries of that request and KV head, a bad length those of the
  *              request).
  * Requires d == 128, block_size == 16, (Hq / Hkv) * n_q <= 32, B <= 4096,
- * B * Hkv * max_blocks < 2^31, opts->num_ctas <= 16383.
+ * B * Hkv * max_blocks < 2^31, opts->num_ctas <= 4095.
  */
 typedef struct clo_kv4_attn_args {
     const void* q;

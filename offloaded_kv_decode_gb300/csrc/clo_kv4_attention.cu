@@ -19,7 +19,10 @@
 
 namespace clo {
 
-constexpr int KV4_MAX_CTAS = 16383;  // warps squared stay in 32 bits
+constexpr int KV4_MAX_CTAS = 4095;       // of 16 warps: warps squared stay in 32 bits
+constexpr int KV4_FLAT_WARPS = 16;       // of a CTA, at most
+constexpr int KV4_FLAT_SMEM = 225 * 1024;     // dynamic, at most
+constexpr int KV4_FLAT_RESERVED = 1024 + 1536;  // beside it: the system's, and the static arrays
 constexpr int KV4_MERGE_THREADS = 512;
 constexpr int KV4_MERGE_UNROLL = 8;
 constexpr int KV4_SET_COST = 2;  // what starting and ending a token set costs a warp, in units
@@ -40,7 +43,7 @@ __device__ __forceinline__ int kv4_steps(const Kv4Args& a, int r, bool& bad) {
 }
 
 __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* wsum) {
-    const int per = (a.B + KV4_THREADS - 1) / KV4_THREADS;
+    const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int r0 = min(a.B, static_cast<int>(threadIdx.x) * per), r1 = min(a.B, r0 + per);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad, any_bad = false;
@@ -70,7 +73,10 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Args& a, int* prefix, int* w
     __syncthreads();
 }
 
-// W warps share N steps: warp g from at(g) on, that is floor(N g / W), in 32 bits.
+// W warps share N steps equally: warp g from at(g) on, that is floor(N g / W), in
+// 32 bits.  (Equal shares although the warps of an SM do not advance alike: each
+// of its schedulers prefers the oldest of its warps, which ends a third earlier
+// than the youngest.  Weighing the shares by age measured 3 to 8% slower.)
 struct Kv4Split {
     unsigned N, W, each, rest;
     __device__ __forceinline__ Kv4Split(int steps, unsigned warps) : N(steps), W(min(warps, N)) {
@@ -138,27 +144,35 @@ struct Kv4Layout {
     int ring, warp, bars, prefix, total;  // ring, warp: bytes of a warp's ring, and with its queries
 };
 
-__host__ __device__ inline Kv4Layout kv4_layout(int nt, int ng, int rows, int B) {
+__host__ __device__ inline Kv4Layout kv4_layout(int warps, int nt, int ng, int rows, int B) {
     Kv4Layout y;
     y.ring = kv4_stages(ng) * 2 * kv4_record(ng);
     const int piece = rows * KV4_PIECE_ROW * static_cast<int>(sizeof(float));
     const int both = y.ring + kv4_query_bytes(nt, ng);
     y.warp = ((both > piece ? both : piece) + 127) / 128 * 128;  // the last piece takes their place
-    y.bars = KV4_WARPS * y.warp;
-    y.prefix = y.bars + KV4_WARPS * kv4_stages(ng) * 8;
+    y.bars = warps * y.warp;
+    y.prefix = y.bars + warps * kv4_stages(ng) * 8;
     y.total = y.prefix + (B + 1) * static_cast<int>(sizeof(int));
     return y;
 }
 
+// All warps of an SM in one CTA, so that their pieces meet in shared memory and
+// the prefix sums are made once an SM: 16 requests of 64K tokens 212 us against
+// 219 with CTAs of 4 warps.  With 4 n8 tiles of queries (8 warps an SM) two CTAs
+// of 4 are faster: 16 requests of 16K tokens and 32 query rows 127 us against 136.
+__host__ __device__ constexpr int kv4_flat_ctas(int nt) { return nt == 4 ? 2 : 1; }
+__host__ __device__ constexpr int kv4_flat_warps(int nt) { return 4 * kv4_ctas_per_sm(nt) / kv4_flat_ctas(nt); }
+
 template <bool BF16, int NT, int NG>
-__global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv4_attn_kernel(const Kv4Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int wsum[KV4_WARPS];
-    __shared__ Place walks[KV4_WARPS][3];
-    __shared__ int4 piece_of[2 * KV4_WARPS];  // (token set, request, its units' first step, the step behind them) of
+    __shared__ int wsum[KV4_FLAT_WARPS];
+    __shared__ Place walks[KV4_FLAT_WARPS][3];
+    __shared__ int4 piece_of[2 * KV4_FLAT_WARPS];  // (token set, request, its units' first step, the step behind them) of
                                               // each warp's first and last piece; set -1: none
     constexpr int R = kv4_record(NG), STAGES = kv4_stages(NG);
-    const Kv4Layout y = kv4_layout(NT, NG, a.rows, a.B);
+    const int warps = blockDim.x >> 5, threads = blockDim.x;
+    const Kv4Layout y = kv4_layout(warps, NT, NG, a.rows, a.B);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* ring = smem + warp * y.warp;
     const uint32_t bars = smem_u32(smem + y.bars) + warp * STAGES * 8;
@@ -174,17 +188,17 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     for (int r = blockIdx.x; r < a.B; r += gridDim.x) {
         if (prefix[r + 1] != prefix[r]) continue;
         const size_t row0 = static_cast<size_t>(r) * a.n_q * a.Hq;
-        for (int i = threadIdx.x; i < a.n_q * a.Hq * (KV4_D / 8); i += KV4_THREADS)
+        for (int i = threadIdx.x; i < a.n_q * a.Hq * (KV4_D / 8); i += threads)
             (reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row0 * KV4_D * 2))[i] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse != nullptr)
-            for (int i = threadIdx.x; i < a.n_q * a.Hq; i += KV4_THREADS) a.lse[row0 + i] = -INFINITY;
+            for (int i = threadIdx.x; i < a.n_q * a.Hq; i += threads) a.lse[row0 + i] = -INFINITY;
         if (a.by_set)
-            for (int h = threadIdx.x; h < a.Hkv; h += KV4_THREADS) a.ws_cut[r * a.Hkv + h] = make_int2(0, 0);
+            for (int h = threadIdx.x; h < a.Hkv; h += threads) a.ws_cut[r * a.Hkv + h] = make_int2(0, 0);
     }
 
     // Warp g takes the units of steps [split.at(g), split.at(g + 1)).
-    const Kv4Split split(prefix[a.B], gridDim.x * KV4_WARPS);
-    const unsigned g0 = blockIdx.x * KV4_WARPS, g = g0 + warp;
+    const Kv4Split split(prefix[a.B], gridDim.x * warps);
+    const unsigned g0 = blockIdx.x * warps, g = g0 + warp;
     const int x0 = split.at(g), x1 = split.at(g + 1);
     // Where this warp's range begins and ends, and where its loads and its
     // computation stand: read when one goes on to another token set.
@@ -329,70 +343,55 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
     pdl_launch_dependents();
     __syncthreads();
 
-    // The CTA's pieces: each token set at its first one.  A warp's last piece is
-    // in shared memory, its first one (written in this CTA too) in the workspace.
-    const int c0 = split.at(g0), c1 = split.at(g0 + KV4_WARPS);  // the CTA's steps
-    int sets[2 * KV4_WARPS];
-#pragma unroll
-    for (int k = 0; k < 2 * KV4_WARPS; ++k) sets[k] = piece_of[k].x;
+    // The CTA's pieces, a token set at a time.  A warp's last piece is in shared
+    // memory, its first one (written in this CTA too) in the workspace; lane k
+    // holds the set of piece k.
+    const int c0 = split.at(g0), c1 = split.at(g0 + warps);  // the CTA's steps
+    const int set_of = lane < 2 * warps ? piece_of[lane].x : -1;
+    uint32_t todo = __ballot_sync(FULL_MASK, set_of >= 0);
     int tail_set = 0, tail_ctas = 0;
 #pragma unroll 1
-    for (int i = 0; i < 2 * KV4_WARPS; ++i) {
-        const int4 piece = piece_of[i];
-        const int set = piece.x;
-        bool again = set < 0;
-#pragma unroll
-        for (int k = 0; k < 2 * KV4_WARPS - 1; ++k) again |= k < i && sets[k] == set;
-        if (again) continue;
-        const int r = piece.y, s0 = piece.z, s1 = piece.w, h = set - r * a.Hkv;
+    while (todo != 0u) {
+        const int4 piece = piece_of[__ffs(todo) - 1];
+        const uint32_t mine = __ballot_sync(FULL_MASK, set_of == piece.x);
+        todo &= ~mine;
+        const int set = piece.x, r = piece.y, s0 = piece.z, s1 = piece.w, h = set - r * a.Hkv;
         const bool starts = s0 >= c0, goes_on = s1 > c1;
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0);
         int covers = 0;
         if (starts && goes_on) {
-            covers = static_cast<int>(split.owner(s1 - 1) / KV4_WARPS) - static_cast<int>(blockIdx.x) + 1;
+            covers = static_cast<int>(split.owner(s1 - 1) / warps) - static_cast<int>(blockIdx.x) + 1;
             tail_set = set;
             tail_ctas = covers;
         }
         if (a.by_set && starts && threadIdx.x == 0) a.ws_cut[set] = make_int2(blockIdx.x, covers);
-        for (int it = threadIdx.x; it < a.rows * (KV4_D / 4); it += KV4_THREADS) {
+        for (int it = threadIdx.x; it < a.rows * (KV4_D / 4); it += threads) {
             const int row = it / (KV4_D / 4), col = it % (KV4_D / 4);
-            float2 ml[2 * KV4_WARPS];
-            float4 v[2 * KV4_WARPS];
-            float M = -INFINITY;
-            bool bad = false;
+            Sums sums;
+            for (uint32_t left = mine; left != 0u;) {
+                constexpr int P = 8;  // read at a time
+                float2 ml[P];
+                float4 v[P];
 #pragma unroll
-            for (int k = 0; k < 2 * KV4_WARPS; ++k) {
-                ml[k] = make_float2(-INFINITY, 0.f);
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (sets[k] == set) {
-                    const float* pc = (k & 1) ? reinterpret_cast<const float*>(smem + (k >> 1) * y.warp)
-                                              : a.ws_first + static_cast<size_t>(g0 + (k >> 1)) * a.rows * KV4_PIECE_ROW;
-                    ml[k] = *reinterpret_cast<const float2*>(pc + row * KV4_PIECE_ROW + KV4_D);
-                    v[k] = *reinterpret_cast<const float4*>(pc + row * KV4_PIECE_ROW + 4 * col);
+                for (int p = 0; p < P; ++p) {
+                    ml[p] = make_float2(-INFINITY, 0.f);
+                    v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (left != 0u) {
+                        const int k = __ffs(left) - 1;
+                        left &= left - 1;
+                        const float* pc = (k & 1) ? reinterpret_cast<const float*>(smem + (k >> 1) * y.warp)
+                                                  : a.ws_first + static_cast<size_t>(g0 + (k >> 1)) * a.rows * KV4_PIECE_ROW;
+                        ml[p] = *reinterpret_cast<const float2*>(pc + row * KV4_PIECE_ROW + KV4_D);
+                        v[p] = *reinterpret_cast<const float4*>(pc + row * KV4_PIECE_ROW + 4 * col);
+                    }
                 }
-                M = fmaxf(M, ml[k].x);
-                bad |= ml[k].y == -1.f;
-            }
-            const float ref = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < 2 * KV4_WARPS; ++k) {
-                const float e = kv4_exp2(ml[k].x - ref);
-                L = fmaf(ml[k].y, e, L);
-                O.x = fmaf(v[k].x, e, O.x);
-                O.y = fmaf(v[k].y, e, O.y);
-                O.z = fmaf(v[k].z, e, O.z);
-                O.w = fmaf(v[k].w, e, O.w);
+                sums.take<P>(ml, v);
             }
             if (starts && !goes_on) {
-                const bool none = bad || L == 0.f;
-                const size_t orow = kv4_out_row(a, r, h, row);
-                store4<BF16>(a, orow, col, O, none ? 0.f : 1.f / L, none);
-                if (a.lse != nullptr && col == 0) a.lse[orow] = kv4_lse(M, L, none);
+                sums.write<BF16>(a, r, h, row, col);
             } else {
-                *reinterpret_cast<float4*>(a.ws_o + (slot * a.rows + row) * KV4_D + 4 * col) = O;
-                if (col == 0) a.ws_ml[slot * a.rows + row] = make_float2(M, bad ? -1.f : L);
+                *reinterpret_cast<float4*>(a.ws_o + (slot * a.rows + row) * KV4_D + 4 * col) = sums.O;
+                if (col == 0) a.ws_ml[slot * a.rows + row] = make_float2(sums.M, sums.L);
             }
         }
     }
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_attn_ker
 template <bool BF16>
 __global__ void __launch_bounds__(KV4_MERGE_THREADS) kv4_merge_kernel(const Kv4Args a, int items, int share) {
     constexpr int WARPS = KV4_MERGE_THREADS / 32, U = KV4_MERGE_UNROLL;
-    __shared__ float sm_m[WARPS], sm_l[WARPS];
+    __shared__ float2 sm_ml[WARPS];
     __shared__ float4 sm_o[WARPS][32];
     pdl_launch_dependents();
     pdl_wait();
@@ -418,13 +417,10 @@ __global__ void __launch_bounds__(KV4_MERGE_THREADS) kv4_merge_kernel(const Kv4A
     const int where = item / a.rows, row = item - where * a.rows;
     const int2 cut = item < items ? a.ws_cut[where] : make_int2(0, 0);
     const int set = a.by_set ? where : cut.x, cta = a.by_set ? cut.x : where, pieces = cut.y;
-    float M = -INFINITY, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    Sums sums;
     for (int p0 = part; p0 < pieces; p0 += share * U) {
         float2 ml[U];
         float4 v[U];
-        float mx = M;
-        bool bad = L < 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int p = p0 + u * share;
@@ -436,59 +432,22 @@ __global__ void __launch_bounds__(KV4_MERGE_THREADS) kv4_merge_kernel(const Kv4A
                 v[u] = reinterpret_cast<const float4*>(a.ws_o + (slot * a.rows + row) * KV4_D)[lane];
             }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            mx = fmaxf(mx, ml[u].x);
-            bad |= ml[u].y == -1.f;
-        }
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float e = fast_exp2(M - ref);
-        L *= e, O.x *= e, O.y *= e, O.z *= e, O.w *= e;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            e = fast_exp2(ml[u].x - ref);
-            L = fmaf(ml[u].y, e, L);
-            O.x = fmaf(v[u].x, e, O.x);
-            O.y = fmaf(v[u].y, e, O.y);
-            O.z = fmaf(v[u].z, e, O.z);
-            O.w = fmaf(v[u].w, e, O.w);
-        }
-        M = mx;
-        if (bad) L = -1.f;
+        sums.take<U>(ml, v);
     }
     if (share > 1) {
-        if (lane == 0) {
-            sm_m[warp] = M;
-            sm_l[warp] = L;
-        }
-        sm_o[warp][lane] = O;
+        if (lane == 0) sm_ml[warp] = make_float2(sums.M, sums.L);
+        sm_o[warp][lane] = sums.O;
         __syncthreads();
         if (part != 0) return;
-        float top = M;
-        for (int x = 1; x < share; ++x) top = fmaxf(top, sm_m[warp + x]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        bool bad = false;
-        L = 0.f;
-        O = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = 0; x < share; ++x) {
-            const float e = fast_exp2(sm_m[warp + x] - ref), l = sm_l[warp + x];
-            const float4 v = sm_o[warp + x][lane];
-            bad |= l == -1.f;
-            L = fmaf(l, e, L);
-            O.x = fmaf(v.x, e, O.x);
-            O.y = fmaf(v.y, e, O.y);
-            O.z = fmaf(v.z, e, O.z);
-            O.w = fmaf(v.w, e, O.w);
+        for (int x = 1; x < share; ++x) {
+            const float2 ml[1] = {sm_ml[warp + x]};
+            const float4 v[1] = {sm_o[warp + x][lane]};
+            sums.take<1>(ml, v);
         }
-        M = top;
-        if (bad) L = -1.f;
     }
     if (pieces == 0) return;
-    const bool none = L == -1.f || L == 0.f;
     const int r = set / a.Hkv, h = set - r * a.Hkv;
-    const size_t orow = kv4_out_row(a, r, h, row);
-    store4<BF16>(a, orow, lane, O, none ? 0.f : 1.f / L, none);
-    if (a.lse != nullptr && lane == 0) a.lse[orow] = kv4_lse(M, L, none);
+    sums.write<BF16>(a, r, h, row, lane);
 }
 
 using Kv4Kernel = void (*)(const Kv4Args);
@@ -502,16 +461,13 @@ static Kv4Kernel attn_kernel(int nt, int ng) {
     return nt == 1 ? attn_kernel_ng<BF16, 1>(ng) : nt == 2 ? attn_kernel_ng<BF16, 2>(ng) : attn_kernel_ng<BF16, 4>(ng);
 }
 
-// One wave at the most: what the workspace is sized for.
-static int kv4_most_ctas(int rows) { return device_sm_count() * kv4_ctas_per_sm(kv4_row_tiles(rows)); }
-
 static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 static size_t kv4_workspace(int ctas, int rows) {
     const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
     return round256(slots * KV4_D * sizeof(float)) + round256(slots * sizeof(float2)) +
            round256(static_cast<size_t>(ctas) * sizeof(int2)) +
-           static_cast<size_t>(ctas) * KV4_WARPS * rows * KV4_PIECE_ROW * sizeof(float);
+           static_cast<size_t>(ctas) * kv4_flat_warps(kv4_row_tiles(rows)) * rows * KV4_PIECE_ROW * sizeof(float);
 }
 
 }  // namespace clo
@@ -522,7 +478,7 @@ extern "C" size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, 
     if (B < 0 || n_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d != KV4_D || num_ctas < 0) return 0;
     if (static_cast<long long>(Hq / Hkv) * n_q > KV4_MAX_ROWS) return 0;
     const int rows = Hq / Hkv * n_q;
-    const int ctas = num_ctas > 0 ? num_ctas : kv4_most_ctas(rows);
+    const int ctas = num_ctas > 0 ? num_ctas : device_sm_count() * kv4_flat_ctas(kv4_row_tiles(rows));
     return ctas > 0 ? kv4_workspace(ctas, rows) : 0;
 }
 
@@ -566,11 +522,13 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, c
     Kv4Args a;
     a.rows = Hq / Hkv * n_q;
     const int nt = kv4_row_tiles(a.rows);
-    const int smem = kv4_layout(nt, ng, a.rows, B).total;
-    // One wave: as many CTAs an SM as registers and shared memory allow.
-    const int per_sm = std::min(kv4_ctas_per_sm(nt), KV4_SMEM_PER_SM / (smem + KV4_SMEM_RESERVED));
-    int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count() * per_sm;
-    const long long most = (units + KV4_WARPS - 1) / KV4_WARPS;  // a unit a warp
+    // As many warps as shared memory allows, in one wave.
+    int warps = kv4_flat_warps(nt);
+    while (warps > 4 && kv4_layout(warps, nt, ng, a.rows, B).total > KV4_FLAT_SMEM) warps -= 4;
+    const int smem = kv4_layout(warps, nt, ng, a.rows, B).total;
+    const int per_sm = std::min(kv4_flat_ctas(nt), KV4_SMEM_PER_SM / (smem + KV4_FLAT_RESERVED));
+    int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count() * std::max(per_sm, 1);
+    const long long most = (units + warps - 1) / warps;  // a unit a warp
     if (ctas > most) ctas = static_cast<int>(most);
     if (workspace == nullptr || !kv4_aligned(workspace, 16) ||
         ws_bytes < clo_kv4_paged_workspace_size(B, n_q, Hq, Hkv, d, opts != nullptr ? opts->num_ctas : 0))
@@ -617,11 +575,11 @@ extern "C" clo_status clo_kv4_paged_decode_attn(const clo_kv4_attn_args* args, c
     }
     const Kv4Kernel kernel = dtype == CLO_BF16 ? attn_kernel<true>(nt, ng) : attn_kernel<false>(nt, ng);
     const auto merge = dtype == CLO_BF16 ? kv4_merge_kernel<true> : kv4_merge_kernel<false>;
-    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), kv4_layout(nt, ng, a.rows, KV4_MAX_B).total) ||
+    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), KV4_FLAT_SMEM) ||
         !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
         return CLO_ERR_CUDA;
     if (opts != nullptr && opts->ev_begin != nullptr && !record_event(opts->ev_begin, stream)) return CLO_ERR_CUDA;
-    if (launch_pdl(kernel, dim3(ctas), dim3(KV4_THREADS), smem, stream, a) != cudaSuccess) return CLO_ERR_CUDA;
+    if (launch_pdl(kernel, dim3(ctas), dim3(warps * 32), smem, stream, a) != cudaSuccess) return CLO_ERR_CUDA;
     if (opts != nullptr && opts->ev_end != nullptr && !record_event(opts->ev_end, stream)) return CLO_ERR_CUDA;
     if (ctas > 1 &&
         launch_pdl(merge, dim3((items + per_block - 1) / per_block), dim3(KV4_MERGE_THREADS), 0, stream, a, items, share) !=

@@ -46,7 +46,8 @@ constexpr long long KV4_WAIT_CLOCKS = 1ll << 32;  // about 2 s
 constexpr float KV4_SLACK = 8.f;  // how far x + log2(V scale) may pass the reference, log2
 constexpr uint32_t LOW_CODES = 0x000f000fu, HIGH_CODES = 0x00f000f0u;
 
-// CTAs an SM for NT tiles of 8 query rows (registers: 128, 168, 255 a thread).
+// CTAs of 4 warps that an SM's registers hold for NT tiles of 8 query rows (128,
+// 168, 255 a thread).
 __host__ __device__ constexpr int kv4_ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
 // Units a warp's ring has room for: what fits beside the others' at 4 CTAs an SM.
@@ -569,6 +570,43 @@ __device__ __forceinline__ void end_set(const Kv4Args& a, const Softmax<NT, NG>&
             }
         }
 }
+
+// Sums of pieces of one query row's 4 channels, in order; l = -1 marks
+// bad data, and l = 0 with m = -inf a piece without a token.
+struct Sums {
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    template <int P>
+    __device__ __forceinline__ void take(const float2 (&ml)[P], const float4 (&v)[P]) {
+        bool bad = L == -1.f;
+        float top = M;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            top = fmaxf(top, ml[p].x);
+            bad |= ml[p].y == -1.f;
+        }
+        const float ref = top == -INFINITY ? 0.f : top, keep = kv4_exp2(M - ref);
+        M = top;
+        L *= keep, O.x *= keep, O.y *= keep, O.z *= keep, O.w *= keep;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float e = kv4_exp2(ml[p].x - ref);
+            L = fmaf(ml[p].y, e, L);
+            O.x = fmaf(v[p].x, e, O.x);
+            O.y = fmaf(v[p].y, e, O.y);
+            O.z = fmaf(v[p].z, e, O.z);
+            O.w = fmaf(v[p].w, e, O.w);
+        }
+        if (bad) L = -1.f;
+    }
+    template <bool BF16>
+    __device__ __forceinline__ void write(const Kv4Args& a, int r, int h, int row, int col) const {
+        const bool none = L == -1.f || L == 0.f;
+        const size_t orow = kv4_out_row(a, r, h, row);
+        store4<BF16>(a, orow, col, O, none ? 0.f : 1.f / L, none);
+        if (a.lse != nullptr && col == 0) a.lse[orow] = kv4_lse(M, L, none);
+    }
+};
 
 // The kernel that gives each token set a cluster (clo_kv4_sets.cu): the CTAs of
 // one, 0 where the even split is the faster way; and its launch.

@@ -79,40 +79,6 @@ __host__ __device__ inline SetLayout set_layout(int nt, int ng, int rows, int cl
     return y;
 }
 
-// Sums of up to 8 pieces of one query row's 4 channels, in order; l = -1 marks
-// bad data, and l = 0 with m = -inf a piece without a token.
-struct Sums {
-    float M = -INFINITY, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    template <int P>
-    __device__ __forceinline__ void take(const float2 (&ml)[P], const float4 (&v)[P]) {
-        bool bad = false;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            M = fmaxf(M, ml[p].x);
-            bad |= ml[p].y == -1.f;
-        }
-        const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const float e = kv4_exp2(ml[p].x - ref);
-            L = fmaf(ml[p].y, e, L);
-            O.x = fmaf(v[p].x, e, O.x);
-            O.y = fmaf(v[p].y, e, O.y);
-            O.z = fmaf(v[p].z, e, O.z);
-            O.w = fmaf(v[p].w, e, O.w);
-        }
-        if (bad) L = -1.f;
-    }
-    template <bool BF16>
-    __device__ __forceinline__ void write(const Kv4Args& a, int r, int h, int row, int col) const {
-        const bool none = L == -1.f || L == 0.f;
-        const size_t orow = kv4_out_row(a, r, h, row);
-        store4<BF16>(a, orow, col, O, none ? 0.f : 1.f / L, none);
-        if (a.lse != nullptr && col == 0) a.lse[orow] = kv4_lse(M, L, none);
-    }
-};
-
 template <bool BF16, int NT, int NG>
 __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kernel(const Kv4Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
