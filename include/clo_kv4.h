@@ -204,9 +204,13 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  * q:           [B][n_q][Hq][d] of type `dtype`.
  * pool:        the cache; block_table: [B][max_blocks] int32 entries in
  *              [0, num_blocks); ctx_len: [B] int32 in [0, max_blocks * 16].
- * out:         [B][n_q][Hq][d] of type `dtype`.   lse: [B][n_q][Hq] fp32 or NULL.
+ * out:         [B][n_q][Hq][d] of type `dtype`; may be q.
+ * lse:         [B][n_q][Hq] fp32 or NULL.
  * workspace:   >= clo_kv4_paged_workspace_size(...) bytes, 16-byte aligned.
- * err_flag, opts: as for clo_paged_decode_attn (a bad block zeroes the
+ * err_flag, opts: as for clo_paged_decode_attn; opts->num_ctas > 0 also picks
+ *              the kernel that shares all tokens out evenly, where for short
+ *              contexts a cluster for each request and KV head is the default;
+ *              the events bracket whichever runs (a bad block zeroes the
  *              queries of that request and KV head, a bad length those of the
  *              request).
  * Requires d == 128, block_size == 16, (Hq / Hkv) * n_q <= 32, B <= 4096,

@@ -22,8 +22,8 @@ def inputs(ctx, n_q, Hq, Hkv, group, dt, seed, spread=1.0, mb=None):
     mb = mb or max(1, int(-(-ctx.max() // 16)))
     nb = B * mb + 2
     R = ref.record_bytes(group)
-    table = rng.permutation(nb - 2).reshape(B, mb) + 1
-    if mb > 1000:  # a wide table: only blocks in use are made
+    table = rng.permutation(nb - 2).reshape(B, mb) + 1 if B * mb <= 20000 else None
+    if B * mb > 20000:  # a wide table: only blocks in use are made
         used = int(sum(-(-int(c) // 16) for c in ctx))
         nb, at, wide = used + 2, 1, np.full((B, mb), -7)
         for r in range(B):
@@ -87,7 +87,9 @@ def check(ctx, n_q, Hq, Hkv, group, dtype, seed, num_ctas=0, **kw):
 @pytest.mark.parametrize("n_q,Hq,Hkv", [(1, 1, 1), (1, 8, 8), (1, 32, 8), (1, 10, 2), (1, 16, 2), (4, 8, 2), (3, 7, 1),
                                         (2, 32, 2), (1, 24, 1), (8, 4, 1), (32, 1, 1)])
 def test_head_layouts(n_q, Hq, Hkv, group, dtype):
-    check([1, 15, 16, 17, 200, 333], n_q, Hq, Hkv, group, dtype, n_q * 100 + Hq + group)
+    """Both ways: a number of CTAs asks for the one that shares all units out."""
+    for num_ctas in (0, 5):
+        check([1, 15, 16, 17, 200, 333], n_q, Hq, Hkv, group, dtype, n_q * 100 + Hq + group, num_ctas)
 
 
 @pytest.mark.parametrize("num_ctas", [0, 1, 2, 7, 64])
@@ -181,6 +183,64 @@ def test_bfloat16_queries_beyond_half_range():
         want = ref.attention(q.double().numpy(), pool, table, ctx, 128, scale, torch.bfloat16)
         assert err == 0
         assert_matches(got, lse, want)
+
+
+@pytest.mark.parametrize("group", [64, 128])
+def test_as_many_requests_as_there_may_be(group):
+    """4096 requests, most of them empty, in a wide table and in a narrow one."""
+    ctx = np.zeros(4096, int)
+    ctx[[0, 1, 7, 2048, 4095]] = [3, 40, 700, 33, 1000]
+    for mb in (None, 1100):
+        check(ctx, 1, 8, 2, group, "f16", 41, mb=mb)
+    with pytest.raises(clo.CloError):
+        run(*inputs(np.ones(4097, int), 1, 1, 1, 128, torch.float16, 1))
+
+
+def test_events_bracket_the_kernel():
+    q, pool, table, ctx = inputs([900, 40], 1, 16, 4, 64, torch.float16, 19)
+    i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).to(dev())  # noqa: E731
+    q, pool = q.to(dev()), torch.as_tensor(pool).to(dev())
+    for num_ctas in (0, 30):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        for e in ev:
+            e.record()  # creates it
+        out = torch.empty_like(q)
+        ws = torch.empty(clo.clo_kv4_paged_workspace_size(2, 1, 16, 4, 128, num_ctas), dtype=torch.uint8, device=dev())
+        clo.clo_kv4_paged_decode_attn(q, pool, i32(table), i32(ctx), out, ws, num_ctas=num_ctas, events=ev)
+        torch.cuda.synchronize()
+        assert 0 < ev[0].elapsed_time(ev[1]) < 1000
+
+
+def test_output_in_place_of_the_queries():
+    """out may be q."""
+    for mb, ctx in ((None, [900, 40, 0, 5]), (1500, [3000, 40, 0, 5])):
+        q, pool, table, ctx = inputs(ctx, 2, 16, 4, 64, torch.float16, 23, mb=mb)
+        want, _, _ = run(q, pool, table, ctx)
+        i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).to(dev())  # noqa: E731
+        both = q.to(dev())
+        ws = torch.empty(clo.clo_kv4_paged_workspace_size(4, 2, 16, 4), dtype=torch.uint8, device=dev())
+        clo.clo_kv4_paged_decode_attn(both, torch.as_tensor(pool).to(dev()), i32(table), i32(ctx), both, ws)
+        assert np.array_equal(both.double().cpu().numpy(), want)
+
+
+def test_two_calls_at_once_on_two_streams():
+    a, b = (inputs([1500, 700], 1, 16, 4, 64, torch.float16, s, mb=1200) for s in (24, 25))
+    i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).to(dev())  # noqa: E731
+    jobs = []
+    for q, pool, table, ctx in (a, b):
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev())
+        ws = torch.empty(clo.clo_kv4_paged_workspace_size(2, 1, 16, 4), dtype=torch.uint8, device=dev())
+        st = torch.cuda.Stream()
+        call = clo.prepare_kv4_paged_decode_attn(q.to(dev()), torch.as_tensor(pool).to(dev()), i32(table), i32(ctx),
+                                                 out, ws, stream=st)
+        jobs.append((call, out, run(q, pool, table, ctx)[0]))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, _, _ in jobs:
+            call()
+    torch.cuda.synchronize()
+    for _, out, want in jobs:
+        assert np.array_equal(out.double().cpu().numpy(), want)
 
 
 def test_a_non_finite_token_is_seen_only_by_queries_that_see_it():

@@ -4,6 +4,7 @@ layout and quantiser."""
 import ctypes
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -34,6 +35,28 @@ def test_header_and_library_agree(L):
         assert hasattr(L, n) and hasattr(clo, n)
     assert int(re.search(r"CLO_FLAG_NO_ROOM (0x[0-9a-f]+)", text).group(1), 16) == clo.FLAG_NO_ROOM == ref.NO_ROOM
     assert clo.check_error_flag(clo.FLAG_NO_ROOM) == clo.CLO_ERR_BAD_INDEX
+
+
+def test_structs_match_the_header(tmp_path):
+    """Sizes and offsets of the argument structs as a C compiler lays them out."""
+    structs = {"clo_paged_plan_args": kv4.PlanArgs, "clo_kv4_append_args": kv4.AppendArgs,
+               "clo_kv4_gather_args": kv4.GatherArgs, "clo_kv4_attn_args": kv4.AttnArgs}
+    lines = []
+    for name, t in structs.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f[0]}));' for f in t._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "clo_kv4.h"\nint main(void) {\n' +
+                   "\n".join(lines) + "\nreturn 0; }\n")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(libbuild.nvcc_path())), "include")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), "-I", cuda, str(src),
+                    "-o", str(tmp_path / "layout")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "layout")], capture_output=True, check=True).stdout.split()]
+    want = []
+    for t in structs.values():
+        want.append(ctypes.sizeof(t))
+        want += [getattr(t, f[0]).offset for f in t._fields_]
+    assert got == want
 
 
 def test_record_sizes(L):
