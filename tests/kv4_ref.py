@@ -42,7 +42,8 @@ def unpack(rec, group):
     rec = np.asarray(rec)
     k = (rec[..., KB] >> SH) & 15
     v = (rec[..., VB] >> SH) & 15
-    par = np.ascontiguousarray(rec[..., 2048:]).view(np.float16).astype(np.float64)
+    with np.errstate(invalid="ignore"):  # what nothing has been written to may be a NaN
+        par = np.ascontiguousarray(rec[..., 2048:]).view(np.float16).astype(np.float64)
     return k, v, par.reshape(*rec.shape[:-1], BLOCK, 2, D // group, 2)
 
 

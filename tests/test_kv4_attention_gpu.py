@@ -70,7 +70,7 @@ def assert_matches(got, lse, want, what=""):
     assert over.max() <= 0, f"{what}: {over.max():.3e} over a tolerance of {tol.flat[over.argmax()]:.3e}"
     seen = np.isfinite(l)
     assert np.array_equal(np.isneginf(lse), ~seen), what
-    assert np.all(np.abs(lse - l)[seen] <= ltol[seen]), what
+    assert np.all(np.abs(lse[seen] - l[seen]) <= ltol[seen]), what
 
 
 def check(ctx, n_q, Hq, Hkv, group, dtype, seed, num_ctas=0, **kw):

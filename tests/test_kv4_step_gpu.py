@@ -86,7 +86,7 @@ def test_decode_loop(group, dt, captured):
             got, gl = out[i].double().cpu().numpy(), lse[i].double().cpu().numpy()
             assert np.all(np.abs(got - o) <= tol)
             seen = np.isfinite(l)
-            assert np.array_equal(np.isneginf(gl), ~seen) and np.all(np.abs(gl - l)[seen] <= ltol[seen])
+            assert np.array_equal(np.isneginf(gl), ~seen) and np.all(np.abs(gl[seen] - l[seen]) <= ltol[seen])
         # The last layer's new rows read back; the padding is zeros.
         n = off[-1]
         got = ko.double().cpu().numpy()
