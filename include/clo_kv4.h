@@ -212,7 +212,9 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  *              contexts a cluster for each request and KV head is the default;
  *              the events bracket whichever runs (a bad block zeroes the
  *              queries of that request and KV head, a bad length those of the
- *              request).
+ *              request; a record that does not arrive within about 2 s, which
+ *              says that the GPU is in trouble, sets CLO_FLAG_TIMEOUT and
+ *              zeroes what needed it).
  * Requires d == 128, block_size == 16, (Hq / Hkv) * n_q <= 32, B <= 4096,
  * B * Hkv * max_blocks < 2^31, opts->num_ctas <= 4095.
  */

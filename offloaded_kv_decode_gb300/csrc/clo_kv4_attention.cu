@@ -25,7 +25,10 @@ constexpr int KV4_FLAT_SMEM = 225 * 1024;     // dynamic, at most
 constexpr int KV4_FLAT_RESERVED = 1024 + 1536;  // beside it: the system's, and the static arrays
 constexpr int KV4_MERGE_THREADS = 512;
 constexpr int KV4_MERGE_UNROLL = 8;
-constexpr int KV4_SET_COST = 2;  // what starting and ending a token set costs a warp, in units
+// What starting and ending a token set costs a warp, in units: 128 requests of
+// 128 to 4096 tokens and 32 KV heads take 314 us with 0, 278 with 1, 228 with 2
+// and 231 with 3.
+constexpr int KV4_SET_COST = 2;
 
 // Units of request r of one KV head; 0 if it is empty or its length is bad.
 __device__ __forceinline__ int kv4_units(const Kv4Args& a, int r, bool& bad) {
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
         Softmax<NT, NG> w;
         int stage = 0;
         uint32_t parity = 0;
+        bool lost = false;  // a record did not come: no more loads, and no more waits
         for (bool last = false; !last;) {  // a token set, or the part of it in this range
             load_queries<BF16, NT, NG>(a, walk[1].r, walk[1].h, lane, qs);
             reset(w);
@@ -293,7 +297,8 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
                 left = __ldg(a.ctx_len + p.r) - p.j * KV4_UNIT;
             }
             for (; units > 0; --units, left -= KV4_UNIT) {
-                const bool came = mbar_wait(bars + stage * 8, parity);
+                const bool came = !lost && mbar_wait(bars + stage * 8, parity);
+                lost = !came;
                 if (came && ((bad_slots >> stage) & 1u) == 0u) {
                     const uint8_t* rec = ring + 2 * stage * R;
                     constexpr int NB = NT >= 2 ? 1 : 2;  // registers
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
                     if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
                 }
                 __syncwarp();
-                if (to_load > 0) issue(stage);
+                if (to_load > 0 && !lost) issue(stage);
                 if (++stage == STAGES) {
                     stage = 0;
                     parity ^= 1;

@@ -8,15 +8,15 @@
 // shared memory), where each then finishes a part of the outputs: one launch,
 // no workspace, no prefix sums and searches, and a fixed order of the sums.  It
 // is the faster one in two cases.
-//   * Short contexts, where the time is latency.  One request of 1024 tokens
-//     (8 KV heads, 4 query heads each): 5.0 us against 9.8; 8 requests of 2048:
-//     10.2 against 14.7; 32 of 1024: 12.7 against 19.4.
+//   * Short contexts, where the time is latency.  One request of 1024 tokens (8
+//     KV heads, 4 query heads each): 5.0 us against 11.3; 8 requests of 4096:
+//     15.5 against 18.4; 64 of 1024: 19.9 against 27.7.
 //   * Many sets, several for each place a CTA has, where the hardware's order of
 //     CTAs levels the load better than an equal split does (the warps of an SM
-//     do not advance alike).  2048 sets of 4096 tokens: 198 us against 213; 4096
-//     of 128 to 4096: 215 against 218.
+//     do not advance alike).  4096 sets of 2048 tokens: 188 us against 204; of
+//     128 to 4096 tokens: 206 and 206.
 // With a place or two for each long set the even split wins: 128 sets of 64K
-// tokens 236 us against 269, 1024 of 1 to 8192 tokens 125 against 150.
+// tokens 211 us against 249, 1024 of 1 to 8192 tokens 119 against 143.
 #include <algorithm>
 
 #include "clo_kv4_math.cuh"
@@ -145,11 +145,12 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
         load_queries<BF16, NT, NG>(a, r, h, lane, qs);
         Softmax<NT, NG> w;
         reset(w);
-        bool bad = false, first = true;
+        bool bad = false, first = true, lost = false;  // lost: a record did not come, no more loads and waits
 #pragma unroll 1
         for (int k = 0; k < mine; ++k) {
             const int stage = k % STAGES, left = n - (u0 + k) * KV4_UNIT;
-            const bool came = mbar_wait(bars + stage * 8, (k / STAGES) & 1);
+            const bool came = !lost && mbar_wait(bars + stage * 8, (k / STAGES) & 1);
+            lost = !came;
             if (!came || ((bad_slots >> stage) & 1u) != 0u) {
                 bad = true;
                 if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
                 first = false;
             }
             __syncwarp();
-            if (k + STAGES < mine) issue(k + STAGES);
+            if (k + STAGES < mine && !lost) issue(k + STAGES);
         }
         __syncwarp();
         end_set<BF16, NT, NG>(a, w, r, h, bad, reinterpret_cast<float*>(ring), lane);

@@ -220,3 +220,16 @@ def test_refused_tensors():
     clo.clo_kv4_append(empty, empty, s[:0], pool)
     clo.clo_kv4_gather(pool, s[:0], empty.clone(), empty.clone())
     torch.cuda.synchronize()
+
+
+def test_refused_while_another_device_is_current(monkeypatch):
+    """The call's kernels would start on the other device."""
+    k, v = rows(4, 2, torch.float16, 1)
+    pool = torch.zeros(2, 2, 2304, dtype=torch.uint8, device=dev())
+    s = torch.arange(4, dtype=torch.int32, device=dev())
+    call = clo.prepare_kv4_append(k, v, s, pool)
+    call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for again in (call, lambda: clo.clo_kv4_append(k, v, s, pool), lambda: clo.prepare_kv4_gather(pool, s, k, v)):
+        with pytest.raises(clo.CloError, match="current device"):
+            again()
