@@ -25,10 +25,12 @@ constexpr int KV4_FLAT_SMEM = 225 * 1024;     // dynamic, at most
 constexpr int KV4_FLAT_RESERVED = 1024 + 1536;  // beside it: the system's, and the static arrays
 constexpr int KV4_MERGE_THREADS = 512;
 constexpr int KV4_MERGE_UNROLL = 8;
-// What starting and ending a token set costs a warp, in units: 128 requests of
-// 128 to 4096 tokens and 32 KV heads take 314 us with 0, 278 with 1, 228 with 2
-// and 231 with 3.
-constexpr int KV4_SET_COST = 2;
+// What starting and ending a token set costs a warp, in units.  With 2, 4, 6 and
+// 8: 32 requests of 1 to 4096 tokens (8 KV heads, 16 query rows each) 43.2, 41.2,
+// 39.6 and 39.2 us; 24 of 1 to 16384 (32 rows) 118, 113, 109 and 109; 128 of 1 to
+// 8192 (4 rows) 119.4, 118.9, 118.9 and 119.7.  Without it, 128 requests of 128
+// to 4096 tokens took a third longer.
+constexpr int KV4_SET_COST = 6;
 
 // Units of request r of one KV head; 0 if it is empty or its length is bad.
 __device__ __forceinline__ int kv4_units(const Kv4Args& a, int r, bool& bad) {
