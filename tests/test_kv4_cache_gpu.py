@@ -229,7 +229,9 @@ def test_refused_while_another_device_is_current(monkeypatch):
     s = torch.arange(4, dtype=torch.int32, device=dev())
     call = clo.prepare_kv4_append(k, v, s, pool)
     call()
+    kc, vc = k.contiguous(), v.contiguous()
+    clo.prepare_kv4_gather(pool, s, kc, vc)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    for again in (call, lambda: clo.clo_kv4_append(k, v, s, pool), lambda: clo.prepare_kv4_gather(pool, s, k, v)):
+    for again in (call, lambda: clo.clo_kv4_append(k, v, s, pool), lambda: clo.prepare_kv4_gather(pool, s, kc, vc)):
         with pytest.raises(clo.CloError, match="current device"):
             again()
