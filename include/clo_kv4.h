@@ -201,7 +201,8 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  *     o = sum_t softmax_t(scale * q . K_t) V_t,  lse = log sum_t exp(scale * q . K_t),
  * zeros and -inf for a query that sees no token.  Nothing behind the last
  * token a query sees enters its result, whatever it holds.
- * q:           [B][n_q][Hq][d] of type `dtype`.
+ * q:           [B][n_q][Hq][d] of type `dtype`; bf16 elements beyond +-2^112
+ *              may overflow to NaN.
  * pool:        the cache; block_table: [B][max_blocks] int32 entries in
  *              [0, num_blocks); ctx_len: [B] int32 in [0, max_blocks * 16].
  * out:         [B][n_q][Hq][d] of type `dtype`; may be q.

@@ -217,13 +217,13 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
     const int32_t* row = nullptr;         // the request's ids from at0 on, and how many there are
     int row_left = 0;
     auto load_ids = [&]() {
-        if (lane < row_left) ids = __ldg(row + lane);
+        if (lane < row_left) ids = row[lane];
         if (lane == 0 && row_left > 32) prefetch_l1(row + 32);
         at = 0;
     };
     auto start_row = [&](const Place& p) {
         row = a.table + static_cast<size_t>(p.r) * a.max_blocks + 2 * p.j;
-        row_left = (__ldg(a.ctx_len + p.r) + KV4_BLOCK - 1) / KV4_BLOCK - 2 * p.j;
+        row_left = (a.ctx_len[p.r] + KV4_BLOCK - 1) / KV4_BLOCK - 2 * p.j;
         head_pool = a.pool + static_cast<size_t>(p.h) * R;
         load_ids();
     };
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
         Softmax<NT, NG> w;
         int stage = 0;
         uint32_t parity = 0;
-        bool lost = false;  // a record did not come: no more loads, and no more waits
+        bool lost = false;  // a record did not come: no more loads, and all that follows is bad
         for (bool last = false; !last;) {  // a token set, or the part of it in this range
             load_queries<BF16, NT, NG>(a, walk[1].r, walk[1].h, lane, qs);
             reset(w);
@@ -296,12 +296,14 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
             {
                 const Place p = walk[1], end = walk[2];
                 units = (p.r == end.r && p.h == end.h ? end.j : p.nt) - p.j;
-                left = __ldg(a.ctx_len + p.r) - p.j * KV4_UNIT;
+                left = a.ctx_len[p.r] - p.j * KV4_UNIT;
             }
-            for (; units > 0; --units, left -= KV4_UNIT) {
-                const bool came = !lost && mbar_wait(bars + stage * 8, parity);
-                lost = !came;
-                if (came && ((bad_slots >> stage) & 1u) == 0u) {
+            for (; units > 0 && !lost; --units, left -= KV4_UNIT) {
+                if (!warp_wait(bars + stage * 8, parity)) {
+                    lost = true;
+                    break;
+                }
+                if (((bad_slots >> stage) & 1u) == 0u) {
                     const uint8_t* rec = ring + 2 * stage * R;
                     constexpr int NB = NT >= 2 ? 1 : 2;  // registers
 #pragma unroll
@@ -315,15 +317,16 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
                     first = false;
                 } else {
                     bad = true;
-                    if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
+                    if (lane == 0) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
                 }
                 __syncwarp();
-                if (to_load > 0 && !lost) issue(stage);
+                if (to_load > 0) issue(stage);
                 if (++stage == STAGES) {
                     stage = 0;
                     parity ^= 1;
                 }
             }
+            bad |= lost;
             Place p = walk[1];
             const Place end = walk[2];
             const int set = p.r * a.Hkv + p.h, r = p.r, h = p.h, nt = p.nt;
@@ -341,6 +344,7 @@ __global__ void __launch_bounds__(kv4_flat_warps(NT) * 32, kv4_flat_ctas(NT)) kv
                 else if (a.by_set) a.ws_cut[set] = make_int2(0, 0);
             }
             __syncwarp();
+            if (lost && last) give_up<STAGES>(a.err_flag, bars, stage, parity, lane);
             float* piece = whole ? nullptr : last ? reinterpret_cast<float*>(ring) : first_piece;
             end_set<BF16, NT, NG>(a, w, r, h, bad, piece, lane);
         }

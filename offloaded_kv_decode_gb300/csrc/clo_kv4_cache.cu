@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(CACHE_THREADS, APPEND_CTAS) kv4_append_kernel(
     for (int t = 0; t < T; ++t) {
         slot[t] = -1;
         if (g.n + t < N) {
-            slot[t] = __ldg(a.slots + g.n + t);
+            slot[t] = a.slots[g.n + t];
             const uint8_t* row = src + (g.n + t) * stride + g.h * (2 * KV4_D);
 #pragma unroll
             for (int x = 0; x < H; ++x) raw[t][x] = ld_stream(row + x * (2 * KV4_D));
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(CACHE_THREADS, gather_ctas(H)) kv4_gather_kern
     uint32_t codes[T][H], pair[T][H];
     int slot[T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) slot[t] = g.n + t < N ? __ldg(a.slots + g.n + t) : -1;
+    for (int t = 0; t < T; ++t) slot[t] = g.n + t < N ? a.slots[g.n + t] : -1;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         const int s = checked_slot(slot[t], a.num_blocks, bad);
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(CACHE_THREADS, gather_ctas(H)) kv4_gather_kern
 #pragma unroll
         for (int x = 0; x < H; ++x) {
             // Code 0 of scale 0 and zero 0: a row of zeros.
-            codes[t][x] = s >= 0 ? __ldg(word + x * (R / 4)) : 0u;
-            pair[t][x] = s >= 0 ? __ldg(params + x * (R / 4)) : 0u;
+            codes[t][x] = s >= 0 ? word[x * (R / 4)] : 0u;
+            pair[t][x] = s >= 0 ? params[x * (R / 4)] : 0u;
         }
     }
 #pragma unroll

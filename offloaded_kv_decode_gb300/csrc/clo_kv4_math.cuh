@@ -102,6 +102,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     } while (clock64() - t0 < KV4_WAIT_CLOCKS);
     return false;
 }
+// For a whole warp: all of it goes on, or none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(FULL_MASK, mbar_wait(bar, parity));
+}
+// After a wait that ran out: waits, with the same limit, for the other stages'
+// copies, so that none lands in memory that is used for something else by then.
+template <int STAGES>
+__device__ __noinline__ void give_up(int32_t* err_flag, uint32_t bars, int stage, uint32_t parity, int lane) {
+    if (lane == 0) report_error(err_flag, CLO_FLAG_TIMEOUT);
+    for (int s = 0; s < STAGES; ++s)
+        if (s != stage) mbar_wait(bars + s * 8, s > stage ? parity : parity ^ 1u);
+    __syncwarp();
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
                                           uint64_t policy) {
     asm volatile(
@@ -160,7 +173,7 @@ __device__ __forceinline__ void load_queries(const Kv4Args& a, int r, int h, int
         // This lane's channels: 32j + 8c .. + 7 for j = 0 .. 3.
         uint4 raw[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) raw[j] = has ? __ldg(src + 4 * j + c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 4; ++j) raw[j] = has ? src[4 * j + c] : make_uint4(0u, 0u, 0u, 0u);
         float top = 0.f;
         float part[4];
 #pragma unroll

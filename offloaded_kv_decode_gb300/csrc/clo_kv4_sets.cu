@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
     __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
-    int n = __ldg(a.ctx_len + r);
+    int n = a.ctx_len[r];
     if (n < 0 || n > a.max_blocks * KV4_BLOCK) {
         if (threadIdx.x == 0 && rank == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
         n = 0;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
         auto load_ids = [&](int u) {
             const int entry = 2 * u + lane;
             exists = entry < blocks;
-            id = exists ? __ldg(row + entry) : -1;
+            id = exists ? row[entry] : -1;
             ok = exists && id >= 0 && id < a.num_blocks;
         };
         load_ids(u0);
@@ -145,15 +145,15 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
         load_queries<BF16, NT, NG>(a, r, h, lane, qs);
         Softmax<NT, NG> w;
         reset(w);
-        bool bad = false, first = true, lost = false;  // lost: a record did not come, no more loads and waits
+        bool bad = false, first = true;
+        int k = 0;
 #pragma unroll 1
-        for (int k = 0; k < mine; ++k) {
+        for (; k < mine; ++k) {
             const int stage = k % STAGES, left = n - (u0 + k) * KV4_UNIT;
-            const bool came = !lost && mbar_wait(bars + stage * 8, (k / STAGES) & 1);
-            lost = !came;
-            if (!came || ((bad_slots >> stage) & 1u) != 0u) {
+            if (!warp_wait(bars + stage * 8, (k / STAGES) & 1)) break;
+            if (((bad_slots >> stage) & 1u) != 0u) {
                 bad = true;
-                if (lane == 0) report_error(a.err_flag, came ? CLO_FLAG_BAD_INDEX : CLO_FLAG_TIMEOUT);
+                if (lane == 0) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
             } else {
                 const uint8_t* rec = ring + 2 * stage * R;
                 constexpr int NB = NT >= 2 ? 1 : 2;  // registers
@@ -168,7 +168,11 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
                 first = false;
             }
             __syncwarp();
-            if (k + STAGES < mine && !lost) issue(k + STAGES);
+            if (k + STAGES < mine) issue(k + STAGES);
+        }
+        if (k < mine) {  // a record did not come
+            bad = true;
+            give_up<STAGES>(a.err_flag, bars, k % STAGES, (k / STAGES) & 1, lane);
         }
         __syncwarp();
         end_set<BF16, NT, NG>(a, w, r, h, bad, reinterpret_cast<float*>(ring), lane);

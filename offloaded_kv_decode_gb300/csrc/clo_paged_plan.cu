@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(SLOTS_THREADS) paged_slots_kernel(const clo_pa
                         const int pos = first[r] + i - off[r];
                         if (pos / KV4_BLOCK != col) {
                             col = pos / KV4_BLOCK;
-                            id = __ldg(a.block_table + static_cast<long long>(r) * a.max_blocks + col);
+                            id = a.block_table[static_cast<long long>(r) * a.max_blocks + col];
                         }
                         slot[k] = plan_slot(id, pos, bad);
                     }
