@@ -21,11 +21,14 @@
 //     2^9 and never all small, whatever the V scales are, most units need no
 //     reduction over lanes, and the sums are hardly ever rescaled.  l = sum p_t
 //     stays in fp32 (p_t < 2^33 as an fp16 scale is at least 2^-24).
-//   * That rounding is the one that costs accuracy: fp16 outputs are 3.4e-4 off
-//     the 64-bit ones in the 2-norm, 2.1e-4 of which is their own rounding.
-//     Taking V's codes from the middle of their range (code - 8, and the sum of
-//     the rounded weights by one more instruction a group) gives 2.7e-4, but
-//     measured 5 to 11% slower: the registers for it are not there.
+//   * That rounding is the one that costs accuracy.  For fp16 outputs the sums
+//     are arranged so that it meets V's codes from the middle of their range,
+//         sum_t (p_t s_tg)~ (code_td - 7.5) + sum_t p_t (z_tg + 7.5 s_tg),
+//     ~ the rounding: the first product and z take the 7.5 (p s)~ away again.
+//     Outputs are then 2.4e-4 off the 64-bit ones in the 2-norm, 2.1e-4 of which
+//     is their own rounding, against 3.4e-4, for 2 to 5% of the time (128 ragged
+//     multi-head requests: 217 us against 207).  Beside a bf16 output's own
+//     rounding, 1.7e-3, neither shows, and it is left out.
 //
 // Shape.  mma.sync m16n8k16 with 16 tokens on M and 8 query rows (of the
 // G * n_q of a KV head) on N for the scores, then channels on M for the second
@@ -230,7 +233,7 @@ template <int NT, int NG>
 struct Softmax {
     float m[NT][2];        // reference (log2 units) of columns 2c, 2c + 1
     float l[NT][2];        // this lane's share of sum p
-    float z[NT][2][NG];    // this lane's share of sum p z_g
+    float z[NT][2][NG];    // this lane's share of sum p z_g (fp16 outputs: p (z_g + 7.5 s_g) - 7.5 (p s_g)~)
     float o[NT][4][2][4];  // sum p s code: [n8 tile][chunk][low, high codes][register]
 };
 
@@ -327,7 +330,7 @@ __device__ __forceinline__ void load_params(const uint8_t* rec, int t, int kv, b
 // query rows 2c and 2c + 1 of each n8 tile.  first: nothing has been taken in
 // yet.  EDGE: there are tokens that some query does not see; `left` counts the
 // tokens from the first record's first one on.
-template <int NT, int NG, int NB, bool EDGE>
+template <bool BF16, int NT, int NG, int NB, bool EDGE>
 __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool first, const Kv4Args& a,
                                              const Queries<NT, NG>& qs, Softmax<NT, NG>& w, int lane) {
     constexpr int R = kv4_record(NG);
@@ -478,7 +481,11 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
         for (int ch = 0; ch < 4; ++ch) {  // channels 32 ch + 4 gid + 0..3
             if (ch % (4 / NG) == 0) {
                 const int g = ch * NG / 4;
-                const float2 f[2] = {__half22float2(kv4_half2(vp[0][g])), __half22float2(kv4_half2(vp[1][g]))};
+                float2 f[2] = {__half22float2(kv4_half2(vp[0][g])), __half22float2(kv4_half2(vp[1][g]))};
+                if constexpr (!BF16) {
+                    const float2 mid = fma2(make_float2(f[0].x, f[1].x), make_float2(7.5f, 7.5f), make_float2(f[0].y, f[1].y));
+                    f[0].y = mid.x, f[1].y = mid.y;
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float y[4];
@@ -504,8 +511,17 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
                         w.z[nt][0][g] = z.x;
                         w.z[nt][1][g] = z.y;
                     }
-                    pb[nt][0] = kv4_transpose(pack_half2(y[0], y[1]));  // tokens 0-7
-                    pb[nt][1] = kv4_transpose(pack_half2(y[2], y[3]));  // tokens 8-15
+                    const uint32_t yr[2] = {pack_half2(y[0], y[1]), pack_half2(y[2], y[3])};
+                    if constexpr (!BF16) {  // a code counts from 7.5
+                        float2 z = make_float2(w.z[nt][0][g], w.z[nt][1][g]);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            z = fma2(__half22float2(kv4_half2(yr[t])), make_float2(-7.5f, -7.5f), z);
+                        w.z[nt][0][g] = z.x;
+                        w.z[nt][1][g] = z.y;
+                    }
+                    pb[nt][0] = kv4_transpose(yr[0]);  // tokens 0-7
+                    pb[nt][1] = kv4_transpose(yr[1]);  // tokens 8-15
                 }
             }
             if ((ch & 1) == 0) ldmatrix_x4_trans(v, vbase + (((ch + half) ^ ((tok >> 1) & 3)) << 4));

@@ -161,9 +161,9 @@ __global__ void __launch_bounds__(KV4_THREADS, kv4_ctas_per_sm(NT)) kv4_set_kern
                 for (int b = 0; b < 2; b += NB) {
                     const int from_here = left - b * KV4_BLOCK;
                     if (from_here >= NB * KV4_BLOCK + a.n_q - 1)
-                        take_records<NT, NG, NB, false>(rec + b * R, from_here, first && b == 0, a, qs, w, lane);
+                        take_records<BF16, NT, NG, NB, false>(rec + b * R, from_here, first && b == 0, a, qs, w, lane);
                     else if (from_here > 0)
-                        take_records<NT, NG, NB, true>(rec + b * R, from_here, first && b == 0, a, qs, w, lane);
+                        take_records<BF16, NT, NG, NB, true>(rec + b * R, from_here, first && b == 0, a, qs, w, lane);
                 }
                 first = false;
             }
