@@ -7,16 +7,21 @@
 // CTA's warps meet in shared memory, the CTAs in the cluster's (distributed
 // shared memory), where each then finishes a part of the outputs: one launch,
 // no workspace, no prefix sums and searches, and a fixed order of the sums.  It
-// is the faster one in two cases.
+// is the faster one in three cases.
 //   * Short contexts, where the time is latency.  One request of 1024 tokens (8
-//     KV heads, 4 query heads each): 5.0 us against 11.3; 8 requests of 4096:
-//     15.5 against 18.4; 64 of 1024: 19.9 against 27.7.
+//     KV heads, 4 query heads each): 5.0 us against 11.5; 8 requests of 4096:
+//     16.1 against 19.4; 64 of 1024: 20.6 against 28.4.
 //   * Many sets, several for each place a CTA has, where the hardware's order of
 //     CTAs levels the load better than an equal split does (the warps of an SM
-//     do not advance alike).  4096 sets of 2048 tokens: 188 us against 204; of
-//     128 to 4096 tokens: 206 and 206.
+//     do not advance alike).  4096 sets of 2048 tokens: 197 us against 212; of
+//     128 to 4096 tokens: 217 and 218.
+//   * Sets that nearly fill the places, up to about 2048 tokens: 64 requests of
+//     2048 tokens 34.5 us against 41.1, of 1 to 2048 29.4 against 30.1; with 16
+//     query rows 48 requests 39.0 against 47.8 and 35.4 against 35.5, with 32
+//     rows 36 of 1 to 2048 43 against 62.
 // With a place or two for each long set the even split wins: 128 sets of 64K
-// tokens 211 us against 249, 1024 of 1 to 8192 tokens 119 against 143.
+// tokens 211 us against 249, 1024 of 1 to 8192 tokens 123 against 150, 512 of 1
+// to 4096 tokens 43 against 54, 384 of 1 to 2048 24.5 against 27.5.
 #include <algorithm>
 
 #include "clo_kv4_math.cuh"
@@ -26,7 +31,7 @@ namespace clo {
 constexpr int SET_MAX_CLUSTER = 8;
 // Where the even split wins, by measurement.
 constexpr int SET_WARP_UNITS = 12;       // more units a warp, the sets all at once
-constexpr int SET_WARP_UNITS_MANY = 16;  // the same with 1.25 to 4 sets a place
+constexpr int SET_WARP_UNITS_MANY = 16;  // the same with 0.75 to 1 and 1.25 to 4 sets a place
 constexpr int SET_FEW_UNITS = 8;         // fewer units a set, with over 2 sets a place
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -258,7 +263,9 @@ int kv4_set_cluster(const Kv4Args& a, int ng) {
            sets * cluster * 2 <= places(2))
         cluster *= 2;
     const long long a_warp = (units + cluster * KV4_WARPS - 1) / (cluster * KV4_WARPS), room = places(cluster);
-    if (sets * cluster * 4 <= room * 5) return a_warp <= SET_WARP_UNITS ? cluster : 0;
+    const bool filled = sets * cluster <= room && sets * cluster * 4 >= room * 3;
+    if (sets * cluster * 4 <= room * 5)
+        return a_warp <= (filled ? SET_WARP_UNITS_MANY : SET_WARP_UNITS) ? cluster : 0;
     if (sets > 2 * room && units < SET_FEW_UNITS) return 0;
     return sets >= 4 * room || a_warp <= SET_WARP_UNITS_MANY ? cluster : 0;
 }
