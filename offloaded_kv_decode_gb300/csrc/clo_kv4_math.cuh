@@ -26,7 +26,7 @@
 //         sum_t (p_t s_tg)~ (code_td - 7.5) + sum_t p_t (z_tg + 7.5 s_tg),
 //     ~ the rounding: the first product and z take the 7.5 (p s)~ away again.
 //     Outputs are then 2.4e-4 off the 64-bit ones in the 2-norm, 2.1e-4 of which
-//     is their own rounding, against 3.4e-4, for 2 to 5% of the time (128 ragged
+//     is their own rounding, against 3.4e-4, for 2 to 6% of the time (128 ragged
 //     multi-head requests: 217 us against 207).  Beside a bf16 output's own
 //     rounding, 1.7e-3, neither shows, and it is left out.
 //
