@@ -234,7 +234,7 @@ struct Softmax {
     float m[NT][2];        // reference (log2 units) of columns 2c, 2c + 1
     float l[NT][2];        // this lane's share of sum p
     float z[NT][2][NG];    // this lane's share of sum p z_g (fp16 outputs: p (z_g + 7.5 s_g) - 7.5 (p s_g)~)
-    float o[NT][4][2][4];  // sum p s code: [n8 tile][chunk][low, high codes][register]
+    float o[NT][4][2][4];  // sum p s code, but for what is in z: [n8 tile][chunk][low, high codes][register]
 };
 
 template <int NT, int NG>
@@ -535,6 +535,49 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
             }
         }
     }
+}
+
+// Takes out of a warp's sums of p s code what the channels of a group have in
+// common (the mean of the first lanes' channels) and adds it to sum p z.  The
+// codes are not negative, so the sums grow with every token, and the matrix
+// instructions cut each addition to the accumulator off, toward zero: over many
+// tokens the loss is as large as the output, in which the sums of codes and
+// zeros all but cancel (50000 tokens a warp, V of mean 0: 5 to 30%).  What is
+// left in the accumulators after this is of the outputs' own size.  The kernel
+// that gives a token set a cluster has at most 32 units a warp and goes without.
+template <int NT, int NG>
+__device__ __forceinline__ void level_sums(Softmax<NT, NG>& w, int lane) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float2 mean = make_float2(0.f, 0.f);  // of columns 2c and 2c + 1
+#pragma unroll
+            for (int ch = g * 4 / NG; ch < (g + 1) * 4 / NG; ++ch)
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl) {
+                    const float* o = w.o[nt][ch][hl];
+                    const float unit = (hl == 0 ? 0x1p24f : 0x1p20f) * NG / 16.f;
+                    mean = fma2(add2(make_float2(o[0], o[1]), make_float2(o[2], o[3])), make_float2(unit, unit), mean);
+                }
+            mean.x = __shfl_sync(FULL_MASK, mean.x, lane & 3);
+            mean.y = __shfl_sync(FULL_MASK, mean.y, lane & 3);
+            w.z[nt][0][g] += lane < 4 ? mean.x : 0.f;
+            w.z[nt][1][g] += lane < 4 ? mean.y : 0.f;
+#pragma unroll
+            for (int ch = g * 4 / NG; ch < (g + 1) * 4 / NG; ++ch)
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl) {
+                    float* o = w.o[nt][ch][hl];
+                    const float unit = hl == 0 ? -0x1p-24f : -0x1p-20f;
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 x = fma2(mean, make_float2(unit, unit), make_float2(o[k], o[k + 1]));
+                        o[k] = x.x;
+                        o[k + 1] = x.y;
+                    }
+                }
+        }
 }
 
 // Row of the outputs and of lse for query row `row` of request r's KV head h.
