@@ -13,8 +13,11 @@
 //     16.1 against 19.4; 64 of 1024: 20.6 against 28.4.
 //   * Many sets, several for each place a CTA has, where the hardware's order of
 //     CTAs levels the load better than an equal split does (the warps of an SM
-//     do not advance alike).  4096 sets of 2048 tokens: 197 us against 212; of
-//     128 to 4096 tokens: 217 and 218.
+//     do not advance alike).  4096 sets of 2048 tokens: 197 us against 209; of
+//     4096: 374 and 389; of 128 to 4096: 217 and 220.  No order of CTAs levels
+//     sets of any length: with one request of 128K tokens among 79 of up to 2048
+//     (32 KV heads) 1115 us against 170.  So there is a limit here too, by the
+//     table's width.
 //   * Sets that nearly fill the places, up to about 2048 tokens: 64 requests of
 //     2048 tokens 34.5 us against 41.1, of 1 to 2048 29.4 against 30.1; with 16
 //     query rows 48 requests 39.0 against 47.8 and 35.4 against 35.5, with 32
@@ -32,6 +35,10 @@ constexpr int SET_MAX_CLUSTER = 8;
 // Where the even split wins, by measurement.
 constexpr int SET_WARP_UNITS = 12;       // more units a warp, the sets all at once
 constexpr int SET_WARP_UNITS_MANY = 16;  // the same with 0.75 to 1 and 1.25 to 4 sets a place
+// The same from 4 sets a place on.  2560 sets of 1 to 4096 tokens (4 query rows
+// each, up to 32 units a warp) 154 us against 150, of 1 to 8192 tokens 290
+// against 268; with one row and 3200 sets 191 against 192, and 363 against 350.
+constexpr int SET_WARP_UNITS_MOST = 32;
 constexpr int SET_FEW_UNITS = 8;         // fewer units a set, with over 2 sets a place
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -267,7 +274,7 @@ int kv4_set_cluster(const Kv4Args& a, int ng) {
     if (sets * cluster * 4 <= room * 5)
         return a_warp <= (filled ? SET_WARP_UNITS_MANY : SET_WARP_UNITS) ? cluster : 0;
     if (sets > 2 * room && units < SET_FEW_UNITS) return 0;
-    return sets >= 4 * room || a_warp <= SET_WARP_UNITS_MANY ? cluster : 0;
+    return a_warp <= (sets >= 4 * room ? SET_WARP_UNITS_MOST : SET_WARP_UNITS_MANY) ? cluster : 0;
 }
 
 cudaError_t kv4_launch_sets(const Kv4Args& a, int ng, bool bf16, int cluster, cudaStream_t stream) {

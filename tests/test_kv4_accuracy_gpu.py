@@ -54,12 +54,9 @@ def head_rows(pool, blocks, h, group):
 
 
 def measure(q, pool, table, n, group, num_ctas=0):
-    """Outputs of one request of n tokens, and the sums of the model over them:
-    dict of the error's, the output's, and the expected errors' mean squares, the
-    mean error, and the mean of sum_t p s code."""
+    """The call for one request of n tokens, and how far its outputs are off."""
     _, n_q, Hq, _ = q.shape
     Hkv = pool.shape[1]
-    G = Hq // Hkv
     out = torch.empty_like(q)
     ws = torch.empty(clo.clo_kv4_paged_workspace_size(1, n_q, Hq, Hkv, 128, num_ctas), dtype=torch.uint8, device=dev())
     err = torch.zeros(1, dtype=torch.int32, device=dev())
@@ -67,16 +64,25 @@ def measure(q, pool, table, n, group, num_ctas=0):
                                   err_flag=err, num_ctas=num_ctas)
     torch.cuda.synchronize()
     assert int(err.item()) == 0
+    return compare(out[0], q[0], pool, table[0], n, group, range(Hkv))
+
+
+def compare(out, q, pool, blocks, n, group, heads):
+    """The sums of the model over one request's outputs [n_q][Hq][128] of some KV
+    heads: dict of the error's, the output's, and the expected errors' mean
+    squares, the mean error, and the mean of sum_t p s code; and their number."""
+    n_q, Hq, _ = q.shape
+    G = Hq // pool.shape[1]
     sums = {x: 0.0 for x in ("err2", "out2", "weights2", "plain2", "mean", "mass")}
-    for h in range(Hkv):
-        K, code, s, z = head_rows(pool, table[0, :-(-n // 16)], h, group)
+    for h in heads:
+        K, code, s, z = head_rows(pool, blocks[:-(-n // 16)], h, group)
         for i in range(n_q):
             m = n - (n_q - 1 - i)
-            x = q[0, i, h * G:(h + 1) * G].double() @ K[:m].T * ref.scale_for()
+            x = q[i, h * G:(h + 1) * G].double() @ K[:m].T * ref.scale_for()
             p = torch.softmax(x, -1)
             sc, cd = s[:m], code[:m]
             o = p @ (cd * sc + z[:m])
-            d = out[0, i, h * G:(h + 1) * G].double() - o
+            d = out[i, h * G:(h + 1) * G].double() - o
             p2 = p * p
             sums["err2"] += float((d * d).sum())
             sums["out2"] += float((o * o).sum())
@@ -84,7 +90,7 @@ def measure(q, pool, table, n, group, num_ctas=0):
             sums["plain2"] += float((p2 @ (sc * cd) ** 2).sum())
             sums["mean"] += float(d.sum())
             sums["mass"] += float((p @ (sc * cd)).sum())
-    N = n_q * Hq * 128
+    N = n_q * G * len(heads) * 128
     return {k: v / N for k, v in sums.items()}, N
 
 
@@ -147,4 +153,28 @@ def test_many_light_tokens_beside_a_heavy_one(nats, dtype):
     par[first, :, 0, 0, :, 1] = K0.half()[:, None]
     for num_ctas in (0, 20):
         m, N = measure(q, pool, table, T, group, num_ctas)
+        check(m, N, dt)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_long_request_among_many_short_ones(dtype):
+    """More than four (request, KV head)s for each place a CTA has, one request of
+    131072 tokens among them: its sums are not left to a few warps each."""
+    dt, T, Hkv, group = DT[dtype], 131072, 32, 64
+    places = 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    B = 4 * places // Hkv + 2
+    g = torch.Generator(device=dev()).manual_seed(3)
+    pool = make_pool(T // 16 + 8, Hkv, group, g)
+    table = torch.randint(0, pool.shape[0], (B, T // 16), dtype=torch.int32, device=dev(), generator=g)
+    table[B // 2] = torch.randperm(pool.shape[0], device=dev(), generator=g)[:T // 16]
+    ctx = torch.randint(1, 200, (B,), dtype=torch.int32, device=dev(), generator=g)
+    ctx[B // 2] = T
+    q = torch.randn(B, 1, Hkv, 128, device=dev(), generator=g).to(dt)
+    out = torch.empty_like(q)
+    ws = torch.empty(clo.clo_kv4_paged_workspace_size(B, 1, Hkv, Hkv), dtype=torch.uint8, device=dev())
+    clo.clo_kv4_paged_decode_attn(q, pool, table, ctx, out, ws)
+    m, N = compare(out[B // 2], q[B // 2], pool, table[B // 2], T, group, range(0, Hkv, 4))
+    check(m, N, dt)
+    for r in (0, B - 1):
+        m, N = compare(out[r], q[r], pool, table[r], int(ctx[r]), group, range(Hkv))
         check(m, N, dt)
