@@ -39,7 +39,14 @@ constexpr int SET_WARP_UNITS_MANY = 16;  // the same with 0.75 to 1 and 1.25 to 
 // each, up to 32 units a warp) 154 us against 150, of 1 to 8192 tokens 290
 // against 268; with one row and 3200 sets 191 against 192, and 363 against 350.
 constexpr int SET_WARP_UNITS_MOST = 32;
-constexpr int SET_FEW_UNITS = 8;         // fewer units a set, with over 2 sets a place
+// Sets for each place and unit (by the table's width), with over 2 sets a place: a
+// CTA's start and end cost as much as some units.  8 KV heads, 4 query rows each:
+// 256 requests of 1 to 32 tokens 14.8 us against 10.5, of 1 to 96 17.1 against
+// 18.1, of 1 to 224 19.7 against 25.5; 600 of 1 to 160 39.2 against 36.1, of 1 to
+// 224 42.8 and 42.5.  16 rows, 200 requests: of 1 to 96 tokens 26.7 against 23.2,
+// of 1 to 128 27 and 27.5; 32 rows: of 1 to 32 62 against 35, of 1 to 160 79
+// against 109.
+constexpr float SET_MOST_A_UNIT = 1.15f;
 
 __device__ __forceinline__ unsigned cluster_size() {
     unsigned n;
@@ -273,7 +280,7 @@ int kv4_set_cluster(const Kv4Args& a, int ng) {
     const bool filled = sets * cluster <= room && sets * cluster * 4 >= room * 3;
     if (sets * cluster * 4 <= room * 5)
         return a_warp <= (filled ? SET_WARP_UNITS_MANY : SET_WARP_UNITS) ? cluster : 0;
-    if (sets > 2 * room && units < SET_FEW_UNITS) return 0;
+    if (sets > 2 * room && sets > SET_MOST_A_UNIT * room * units) return 0;
     return a_warp <= (sets >= 4 * room ? SET_WARP_UNITS_MOST : SET_WARP_UNITS_MANY) ? cluster : 0;
 }
 
