@@ -165,7 +165,9 @@ clo_status clo_kv4_append(const clo_kv4_append_args* args, cudaStream_t stream);
 /*
  * clo_kv4_gather -- reads the rows of N slots back in 16 bits: what the
  * attention takes as their K and V, code * scale + zero rounded to the nearest
- * value of `dtype` (for bf16 by way of fp32).
+ * value of `dtype` (for bf16 by way of fp32).  In fp16 a value beyond +-65504 is
+ * read as +-65504: the scale is rounded up, so the code of a group's largest
+ * element may stand for up to 64 more.
  * slot_map: [N] int32; a slot may repeat.  -1 gives a row of zeros, any other
  *           slot outside [0, num_blocks * 16) too (and CLO_FLAG_BAD_INDEX).
  * k, v:     [N][Hkv][d] of type `dtype`, contiguous, 16-byte aligned.
@@ -199,8 +201,9 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  * the last n_q among them: query i of request r sees the tokens
  * t < ctx_len[r] - (n_q - 1 - i), and
  *     o = sum_t softmax_t(scale * q . K_t) V_t,  lse = log sum_t exp(scale * q . K_t),
- * zeros and -inf for a query that sees no token.  Nothing behind the last
- * token a query sees enters its result, whatever it holds.
+ * zeros and -inf for a query that sees no token.  fp16 outputs beyond +-65504
+ * are +-65504.  Nothing behind the last token a query sees enters its result,
+ * whatever it holds.
  * q:           [B][n_q][Hq][d] of type `dtype`; bf16 elements beyond +-2^112
  *              may overflow to NaN.
  * pool:        the cache; block_table: [B][max_blocks] int32 entries in

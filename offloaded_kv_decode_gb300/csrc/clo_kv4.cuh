@@ -54,4 +54,18 @@ __device__ __forceinline__ uint32_t kv4_pack2(float lo, float hi) {
     }
 }
 
+// The same, but fp16 has its largest value where the rounding would pass it: a
+// scale is rounded up, so code 15 of a group that reaches 65504 may lie up to 64
+// above.  A NaN stays one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t kv4_pack2_finite(float lo, float hi) {
+    if constexpr (BF16) {
+        return kv4_pack2<true>(lo, hi);
+    } else {
+        uint32_t d;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
+}
+
 }  // namespace clo

@@ -253,11 +253,14 @@ __device__ __forceinline__ uint4 expand(uint32_t codes, uint32_t pair) {
         o[2] = kv4_pack2<true>(v[0].y, v[1].y);
         o[3] = kv4_pack2<true>(v[2].y, v[3].y);
     } else {
-        // One rounding: code * scale + zero is a single fp16 multiply-add.
+        // One rounding: code * scale + zero is a single fp16 multiply-add.  Then
+        // the values past fp16's largest (the scale is rounded up) are that.
+        const __half2 top = __float2half2_rn(65504.f);
         uint32_t v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const __half2 y = __hfma2(r[k], __low2half2(sz), __high2half2(sz));
+            __half2 y = __hfma2(r[k], __low2half2(sz), __high2half2(sz));
+            y = __hmax2_nan(__hmin2_nan(y, top), __hneg2(top));
             v[k] = *reinterpret_cast<const uint32_t*>(&y);
         }
         o[0] = __byte_perm(v[0], v[1], 0x5410);

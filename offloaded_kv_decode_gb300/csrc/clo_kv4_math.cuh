@@ -590,8 +590,8 @@ template <bool BF16>
 __device__ __forceinline__ void store4(const Kv4Args& a, size_t row, int ch4, float4 v, float inv, bool none) {
     uint2 pk = make_uint2(0u, 0u);
     if (!none) {
-        pk.x = kv4_pack2<BF16>(v.x * inv, v.y * inv);
-        pk.y = kv4_pack2<BF16>(v.z * inv, v.w * inv);
+        pk.x = kv4_pack2_finite<BF16>(v.x * inv, v.y * inv);
+        pk.y = kv4_pack2_finite<BF16>(v.z * inv, v.w * inv);
     }
     reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * KV4_D * 2)[ch4] = pk;
 }
