@@ -28,6 +28,7 @@
  * groups (group = 32, 64 or 128 channels); each token has, for K and for V,
  * one pair (scale, zero) of fp16 a group, and one code 0..15 a channel:
  *     value = code * scale + zero.
+ * (clo_kv4_append writes no negative scale, but a record may hold one.)
  * A record is
  *   bytes    0..1023  K codes, 64 bytes a token: 32-bit word 4c + j of a row
  *                     holds channels 32j + 8c .. 32j + 8c + 7;

@@ -16,7 +16,7 @@
 //     the largest.
 //   * Online softmax with one reference m a query row, p_t = 2^(x_t - m), x the
 //     score in log2 units.  m follows the maximum of x_t + log2(largest V scale
-//     of t), and only when a unit passes it by more than 2^8: the weights
+//     of t, in size), and only when a unit passes it by more than 2^8: the weights
 //     p_t s_tg that are rounded to fp16 for the second product are then below
 //     2^9 and never all small, whatever the V scales are, most units need no
 //     reduction over lanes, and the sums are hardly ever rescaled.  l = sum p_t
@@ -354,10 +354,11 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
             uint32_t vp[NG];
             load_params<NG>(rec + b * R, gid + 8 * t, 0, there(2 * b + t), kp[t]);
             load_params<NG>(rec + b * R, gid + 8 * t, 1, there(2 * b + t), vp);
-            __half2 most = kv4_half2(vp[0]);
+            // Scales of either sign.
+            __half2 most = NG == 1 ? kv4_half2(vp[0]) : __habs2(kv4_half2(vp[0]));
 #pragma unroll
-            for (int g = 1; g < NG; ++g) most = __hmax2(most, kv4_half2(vp[g]));
-            big[2 * b + t] = fmaxf(kv4_log2(__low2float(most)), -24.f);
+            for (int g = 1; g < NG; ++g) most = __hmax2(most, __habs2(kv4_half2(vp[g])));
+            big[2 * b + t] = fmaxf(kv4_log2(fabsf(__low2float(most))), -24.f);
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {

@@ -1,5 +1,5 @@
 """The ends of the value range of the 4-bit cache on the GPU: groups that reach
-fp16's largest values."""
+fp16's largest values, and scales of either sign."""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +7,7 @@ import torch
 import kv4_ref as ref
 import offloaded_kv_decode_gb300 as clo
 from gpu_util import dev
+from test_kv4_attention_gpu import inputs, run
 
 pytestmark = pytest.mark.gpu
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -75,3 +76,44 @@ def test_attention_over_rows_at_the_ends_of_the_range_is_finite(group, dtype):
         # The weight's rounding (2^-11 of code * scale) and the output's.
         mag = np.abs(val) + 15 * 8736.0
         assert np.all(np.abs(got - want) <= (2.0 ** -11 + 2.0 ** -20) * mag + ref.U16[dt] * (np.abs(want) + 2.0 ** -11 * mag))
+
+
+@pytest.mark.parametrize("num_ctas", [0, 7])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_scales_of_either_sign(group, dtype, num_ctas):
+    """code * scale + zero is defined for a negative scale too: the same values
+    with some groups' codes counted down from the top instead of up."""
+    dt = DT[dtype]
+    q, pool, table, ctx = inputs([700, 33, 5], 2, 8, 2, group, dt, 77)
+    rng = np.random.Generator(np.random.PCG64(78))
+    par = pool[:, :, 2048:].copy().view(np.float16).reshape(*pool.shape[:2], 16, 2, -1, 2)
+    flip = rng.random(par.shape[:-1]) < 0.5
+    flip[table[2]] = True  # all of a request's
+    with np.errstate(invalid="ignore"):
+        par[..., 1] = np.where(flip, par[..., 1] + np.float16(15) * par[..., 0], par[..., 1])
+        par[..., 0] = np.where(flip, -par[..., 0], par[..., 0])
+    pool[:, :, 2048:] = par.reshape(*pool.shape[:2], -1).view(np.uint8)
+    got, lse, err = run(q, pool, table, ctx, num_ctas)
+    assert err == 0
+    # The reference's tolerance counts magnitudes as code * scale + |zero|: here
+    # those of the pairs turned round again, which are the larger of the two ways.
+    o, l, _, _ = ref.attention(q.double().numpy(), pool, table, ctx, group, ref.scale_for(), dt)
+    turned = par.copy()
+    with np.errstate(invalid="ignore"):
+        turned[..., 0] = np.abs(par[..., 0])
+        turned[..., 1] = np.abs(par[..., 1]) + np.float16(15) * np.abs(par[..., 0])
+    high = pool.copy()
+    high[:, :, :2048] = 0xff
+    high[:, :, 2048:] = turned.reshape(*pool.shape[:2], -1).view(np.uint8)
+    K = ref.values(high, group)
+    for r in range(3):
+        n = int(ctx[r])
+        Kmag, Vmag = (x[table[r, :-(-n // 16)]].transpose(1, 0, 2, 3).reshape(2, -1, 128)[:, :n] for x in K)
+        for h in range(2):
+            qq = np.abs(q.double().numpy()[r, :, 4 * h:4 * h + 4])
+            dx = 20 * 2.0 ** -24 * (qq @ Kmag[h].max(0)) * ref.scale_for() + 2.0 ** -22
+            inner = (2.0 ** -11 + 2 * dx[..., None]) * Vmag[h].max(0) + n * 2.0 ** -25 * 15 * 0.4
+            g, w = got[r, :, 4 * h:4 * h + 4], o[r, :, 4 * h:4 * h + 4]
+            assert np.all(np.isfinite(g)) and np.all(np.abs(g - w) <= inner + ref.U16[dt] * (np.abs(w) + inner) + 2.0 ** -25)
+            assert np.all(np.abs(lse - l)[r, :, 4 * h:4 * h + 4] <= dx + 2.0 ** -22 * (1 + np.abs(l[r, :, 4 * h:4 * h + 4])))
