@@ -15,12 +15,15 @@
 //     element is near 2^13: exact, for bf16 too, but for elements some 2^-27 of
 //     the largest.
 //   * Online softmax with one reference m a query row, p_t = 2^(x_t - m), x the
-//     score in log2 units.  m follows the maximum of x_t + log2(largest V scale
-//     of t, in size), and only when a unit passes it by more than 2^8: the weights
+//     score in log2 units.  m follows 2^6 below the maximum of x_t + log2(largest
+//     V scale of t, in size), and only when a unit gets 2^14 above it: the weights
 //     p_t s_tg that are rounded to fp16 for the second product are then below
-//     2^9 and never all small, whatever the V scales are, most units need no
-//     reduction over lanes, and the sums are hardly ever rescaled.  l = sum p_t
-//     stays in fp32 (p_t < 2^33 as an fp16 scale is at least 2^-24).
+//     2^15 and the largest of them not below 2^6, whatever the V scales are, most
+//     units need no reduction over lanes, and the sums are hardly ever rescaled.
+//     l = sum p_t stays in fp32 (p_t < 2^39 as an fp16 scale is at least 2^-24).
+//     (With the maximum itself for m, weights 2^-25 of the largest were lost:
+//     1e-3 of bf16 outputs, V scales 0.2, with 128K tokens in a warp beside one
+//     of ten times their scale and a score 16 above theirs; now under 1e-4.)
 //   * That rounding is the one that costs accuracy.  For fp16 outputs the sums
 //     are arranged so that it meets V's codes from the middle of their range,
 //         sum_t (p_t s_tg)~ (code_td - 7.5) + sum_t p_t (z_tg + 7.5 s_tg),
@@ -51,7 +54,10 @@ constexpr int KV4_PIECE_ROW = KV4_D + 4;  // floats of a row of a piece; the fou
 constexpr int KV4_SMEM_PER_SM = 228 * 1024;
 constexpr int KV4_SMEM_RESERVED = 1024 + 256;  // of a CTA: the system's, and the static arrays
 constexpr long long KV4_WAIT_CLOCKS = 1ll << 32;  // about 2 s
-constexpr float KV4_SLACK = 8.f;  // how far x + log2(V scale) may pass the reference, log2
+// How far x + log2(V scale) lies above the reference when this moves, and how far
+// it may get: weights up to 2^14 of fp16's 2^16, and down to its least steps of
+// 2^-24 for those 2^-30 of the largest.
+constexpr float KV4_LIFT = 6.f, KV4_SLACK = 14.f;
 constexpr uint32_t LOW_CODES = 0x000f000fu, HIGH_CODES = 0x00f000f0u;
 
 // CTAs of 4 warps that an SM's registers hold for NT tiles of 8 query rows (128,
@@ -440,8 +446,8 @@ __device__ __forceinline__ void take_records(const uint8_t* rec, int left, bool 
                 for (int t = 0; t < 2 * NB; ++t) top = fmaxf(top, x[nt][t >> 1][2 * (t & 1) + col] + big[t]);
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
-                // At the first records to their maximum (0 where a column sees nothing), later only up.
-                const float by = first ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
+                // At the first records to below their maximum (0 where a column sees nothing), later only up.
+                const float by = first ? (top == -INFINITY ? 0.f : top - KV4_LIFT) : fmaxf(top - KV4_LIFT, 0.f);
                 const float al = first ? 0.f : kv4_exp2(-by);
                 w.m[nt][col] += by;
                 w.l[nt][col] *= al;

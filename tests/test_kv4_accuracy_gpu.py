@@ -23,10 +23,12 @@ from gpu_util import dev
 
 pytestmark = pytest.mark.gpu
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
-# 32 additions in a row from zero, each off by up to 2 units of 2^-23 of the sum
-# so far: 2 * 2^-23 * 33 / 2 = 66 * 2^-24 of their sum; the same again for what
-# the sums hold of the outputs themselves.
-MASS = 132
+# An addition sums 16 products and the accumulator, each cut off at the last place
+# of the largest, 2^-23 of it: 17 / 2 of those on average.  After 32 additions
+# what the sums have in common is taken out of the accumulators.  So as much as
+# 32 * 17 / 2 * 2^-23 of an accumulator that has its size from the start, as it has
+# behind one heavy token.
+MASS = 544
 
 
 def make_pool(nb, Hkv, group, g):
@@ -139,9 +141,12 @@ def test_sums_over_many_tokens_do_not_drift(group, Hq, n_q, dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("nats", [10.0, 14.0, 16.0, 18.0])
-def test_many_light_tokens_beside_a_heavy_one(nats, dtype):
-    """The first token's score is `nats` above the middle of 131071 others',
-    which have 1 to 85% of the weight between them."""
+@pytest.mark.parametrize("heavy", [0.2, 2.0])
+def test_many_light_tokens_beside_a_heavy_one(heavy, nats, dtype):
+    """The first token's score is `nats` above the middle of 131071 others', which
+    have 0.2 to 85% of the weight between them.  Its V is 0 (code 7, zero -7
+    scales; the scale is like the others' or ten times as large), so what is lost
+    of the light weights shows: by the end one warp has them all."""
     dt, T, Hkv, group = DT[dtype], 131072, 16, 128
     q, pool, table = one_request(T, 1, Hkv, Hkv, group, dt, 7)
     par = pool[:, :, 2048:].view(torch.float16).view(pool.shape[0], Hkv, 16, 2, 1, 2)
@@ -151,7 +156,10 @@ def test_many_light_tokens_beside_a_heavy_one(nats, dtype):
     K0 = torch.where(total.abs() < 2, 0.0, nats / ref.scale_for() / total)
     par[first, :, 0, 0, :, 0] = 0
     par[first, :, 0, 0, :, 1] = K0.half()[:, None]
-    for num_ctas in (0, 20):
+    s = torch.tensor(heavy).half()
+    par[first, :, 0, 1, :, 0], par[first, :, 0, 1, :, 1] = s.item(), (-7 * s.float()).item()
+    pool[first, :, 1024:1024 + 64] = 0x77
+    for num_ctas in (0, 20, 1):
         m, N = measure(q, pool, table, T, group, num_ctas)
         check(m, N, dt)
 
