@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "clo.h"
+#include "clo_prepared.cuh"
 
 namespace clo {
 
@@ -222,17 +223,12 @@ inline unsigned long long current_context_id() {
 // again; with no context id they are set on every call.
 inline bool prepare_kernel(const void* func, int dyn_smem) {
     static std::mutex mu;
-    static const void* done_func[64];
-    static unsigned long long done_ctx[64];
-    static int done_smem[64];
-    static int n_done = 0;
+    static PreparedKernels done;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(mu);
-    if (ctx != 0)
-        for (int i = 0; i < n_done; ++i)
-            if (done_func[i] == func && done_ctx[i] == ctx && done_smem[i] >= dyn_smem) return true;
+    if (ctx != 0 && done.has(func, ctx, dyn_smem)) return true;
     if (cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return false;
@@ -240,15 +236,7 @@ inline bool prepare_kernel(const void* func, int dyn_smem) {
         cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn_smem) !=
             cudaSuccess)
         return false;
-    if (ctx == 0) return true;
-    int slot = -1;
-    for (int i = 0; i < n_done && slot < 0; ++i)
-        if (done_func[i] == func && done_ctx[i] == ctx) slot = i;
-    if (slot < 0 && n_done < 64) slot = n_done++;
-    if (slot < 0) slot = static_cast<int>(reinterpret_cast<uintptr_t>(func) % 64);  // full: reuse
-    done_func[slot] = func;
-    done_ctx[slot] = ctx;
-    done_smem[slot] = dyn_smem;
+    if (ctx != 0) done.add(func, ctx, dyn_smem);
     return true;
 }
 
