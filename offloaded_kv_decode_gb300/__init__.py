@@ -168,7 +168,9 @@ def _opts(num_ctas: int, events) -> Optional[AttnOpts]:
     if not num_ctas and events is None:
         return None
     eb, ee = _events(events)
-    return AttnOpts(int(num_ctas), eb or None, ee or None)
+    opts = AttnOpts(int(num_ctas), eb or None, ee or None)
+    opts.events = events  # the struct holds their handles
+    return opts
 
 
 _BYREF = type(ctypes.byref(ctypes.c_int()))
@@ -180,7 +182,7 @@ class PreparedCall:
     Calling it issues the same C call again (same buffers; their contents may
     change between calls) without redoing the Python-side checks, for loops
     that re-run a decode step on fixed buffers.  It holds references to its
-    tensors, so they stay alive as long as the object does.  The stream is
+    tensors and events, so they stay alive as long as the object does.  The stream is
     the one given to the ``prepare_*`` function, else the current stream at
     each call.
     """
