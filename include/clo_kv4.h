@@ -7,8 +7,8 @@
  * new tokens of each request get (clo_paged_plan), their K and V written
  * there (clo_kv4_append), the attention of the new queries over every cached
  * token (clo_kv4_paged_decode_attn), and, for a prompt computed in chunks
- * with a 16-bit attention, the tokens before the chunk read back
- * (clo_kv4_gather).  The paged cache and its block table are those of
+ * with a 16-bit attention of the caller's own, the tokens before the chunk read
+ * back (clo_kv4_gather).  The paged cache and its block table are those of
  * clo_paged_decode_attn (clo.h); a token's slot is
  *     block * block_size + (position % block_size).
  * In 4 bits a cached token takes 136 to 160 bytes a KV head instead of 512,
@@ -220,6 +220,14 @@ size_t clo_kv4_paged_workspace_size(int B, int n_q, int Hq, int Hkv, int d, int 
  *              request; a record that does not arrive within about 2 s, which
  *              says that the GPU is in trouble, sets CLO_FLAG_TIMEOUT and
  *              zeroes what needed it).
+ * Sums are in fp32.  The weights are rounded to fp16 once, times V's scale; the
+ * largest lie between 2^6 and 2^15 there, and what is 2^-31 of them counts as 0.
+ * The same call on the same kind of GPU gives the same bits each time.  The order
+ * of the sums, and with it the last bits, depends on every request's length, on
+ * max_blocks, num_ctas and the number of SMs.
+ * More than 32 query rows a KV head take several calls: the queries 0 .. i of
+ * each request with ctx_len less n_q - 1 - i (0 if that is negative), then the
+ * rest with ctx_len.
  * Requires d == 128, block_size == 16, (Hq / Hkv) * n_q <= 32, B <= 4096,
  * B * Hkv * max_blocks < 2^31, opts->num_ctas <= 4095.
  */

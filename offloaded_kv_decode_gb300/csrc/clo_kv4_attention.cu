@@ -11,8 +11,8 @@
 // in flight.  A (request, KV head) that lies in one warp's range is finished by
 // that warp alone.  What crosses ranges is merged once a CTA at its end, and
 // what crosses CTAs leaves one fp32 partial a CTA, merged by a second kernel.
-// The split depends on the lengths alone, so the bits of a result do not
-// depend on timing.
+// The split depends on the lengths, the table's width and the grid alone, so the
+// bits of a result do not depend on timing.
 #include <algorithm>
 
 #include "clo_kv4_math.cuh"

@@ -27,7 +27,8 @@ DT = {"f16": torch.float16, "bf16": torch.bfloat16}
 # of the largest, 2^-23 of it: 17 / 2 of those on average.  After 32 additions
 # what the sums have in common is taken out of the accumulators.  So as much as
 # 32 * 17 / 2 * 2^-23 of an accumulator that has its size from the start, as it has
-# behind one heavy token.
+# behind one heavy token; and of one that grows, in the 64 additions at most of the
+# kernel for short contexts.
 MASS = 544
 
 
