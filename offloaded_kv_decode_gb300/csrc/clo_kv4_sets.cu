@@ -10,18 +10,18 @@
 // is the faster one in three cases.
 //   * Short contexts, where the time is latency.  One request of 1024 tokens (8
 //     KV heads, 4 query heads each): 5.0 us against 11.5; 8 requests of 4096:
-//     16.1 against 19.4; 64 of 1024: 20.6 against 28.4.
+//     16.1 against 19.2; 64 of 1024: 20.5 against 28.4.
 //   * Many sets, several for each place a CTA has, where the hardware's order of
 //     CTAs levels the load better than an equal split does (the warps of an SM
 //     do not advance alike).  4096 sets of 2048 tokens: 197 us against 209; of
-//     4096: 374 and 389; of 128 to 4096: 217 and 220.  No order of CTAs levels
+//     4096: 374 and 389; of 128 to 4096: 217 both.  No order of CTAs levels
 //     sets of any length: with one request of 128K tokens among 79 of up to 2048
 //     (32 KV heads) 1115 us against 170.  So there is a limit here too, by the
 //     table's width.
 //   * Sets that nearly fill the places, up to about 2048 tokens: 64 requests of
-//     2048 tokens 34.5 us against 41.1, of 1 to 2048 29.4 against 30.1; with 16
-//     query rows 48 requests 39.0 against 47.8 and 35.4 against 35.5, with 32
-//     rows 36 of 1 to 2048 43 against 62.
+//     2048 tokens 34.5 us against 40.9, of 1 to 2048 29.5 against 30.3; with 16
+//     query rows 48 requests 39.0 against 46.7 and 35.6 against 34.5, with 32
+//     rows 36 of 1 to 2048 43 against 63.
 // With a place or two for each long set the even split wins: 128 sets of 64K
 // tokens 211 us against 249, 1024 of 1 to 8192 tokens 123 against 150, 512 of 1
 // to 4096 tokens 43 against 54, 384 of 1 to 2048 24.5 against 27.5.
