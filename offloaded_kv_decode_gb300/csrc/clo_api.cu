@@ -14,7 +14,7 @@ extern "C" const char* clo_status_string(clo_status s) {
     return "CLO_ERR_UNKNOWN";
 }
 
-extern "C" int clo_version(void) { return 10400; }  // 1.4.0
+extern "C" int clo_version(void) { return 10401; }  // 1.4.1
 
 extern "C" clo_status clo_check_error_flag(int32_t host_err_flag) {
     if (host_err_flag == 0) return CLO_OK;
