@@ -252,7 +252,7 @@ def _prepare_calls(s):
                                                    err_flag=err)]
     else:
         sws = work(clo.clo_paged_select_workspace_size(c["B"], c["Hkv"], s["table"].shape[1]))
-        ws = work(clo.clo_paged_workspace_size(c["B"], c["Hq"], c["Hkv"]))
+        ws = work(clo.clo_paged_chunk_workspace_size(c["Hq"], c["Hkv"]))
         s["calls"] = [clo.prepare_paged_block_select(s["q"], s["bounds"], s["table"], s["ctx"], s["sel"], sws, n_first=c["first"], n_last=c["last"],
                                                      err_flag=err),
                       clo.prepare_paged_sparse_decode_attn(s["q"], s["kc"], s["vc"], s["table"], s["ctx"], s["sel"], s["out"], ws, lse=s["lse"],
