@@ -778,3 +778,12 @@ from .kv4 import (FLAG_NO_ROOM, KV4_BLOCK_SIZE, KV4_GROUPS, clo_kv4_append,  # n
                   clo_kv4_block_bytes, clo_kv4_gather, clo_kv4_paged_decode_attn,
                   clo_kv4_paged_workspace_size, clo_paged_plan, prepare_kv4_append,
                   prepare_kv4_gather, prepare_kv4_paged_decode_attn, prepare_paged_plan)
+
+
+# ---------------------------------------------------------------- paged KV cache in 16 bits
+
+from .paged import (PAGED_BLOCK_SIZE, clo_paged_block_bounds, clo_paged_block_select,  # noqa: E402,F401
+                    clo_paged_bounds_bytes, clo_paged_chunk_attn, clo_paged_chunk_workspace_size,
+                    clo_paged_rope_append, clo_paged_select_workspace_size, clo_paged_sparse_decode_attn,
+                    clo_rope_pairs, prepare_paged_block_bounds, prepare_paged_block_select,
+                    prepare_paged_chunk_attn, prepare_paged_rope_append, prepare_paged_sparse_decode_attn)

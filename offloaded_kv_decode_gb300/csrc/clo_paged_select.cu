@@ -1,0 +1,407 @@
+// clo_paged_select.cu -- the range of each block's keys in 8-bit codes, and the
+// blocks that a decode step selects by a score from those ranges.
+//
+// Mathematics.  For a query s and keys k_t of a block, s . k_t is at most the sum
+// over channels of max(s_c * max_t k_tc, s_c * min_t k_tc).  With the ranges and
+// the query as whole numbers of at most 127 in size the sum is a whole number
+// below 2^24, the same in any order, and one product with the block's scale (a
+// single rounding) makes the score.  So a selection depends on its inputs alone,
+// not on the split of the work, and equal scores are exactly equal.  A positive
+// code meets the largest keys, a negative one the smallest: with the query's
+// positive and negative codes apart, each a word of four bytes, the sum is two
+// dp4a for every four channels.
+#include <math.h>
+
+#include "clo_paged.cuh"
+
+namespace clo {
+
+// ---------------------------------------------------------------- bounds
+
+constexpr int BOUNDS_THREADS = 128;
+
+struct BoundsArgs {
+    const uint8_t* kc;
+    const int32_t* slots;
+    uint8_t* bounds;
+    int32_t* err_flag;
+    int N, Hkv, num_blocks, tokens;  // tokens a warp looks at
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (BF16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ int code_of(float x, float div, bool up) {
+    const float c = __fdiv_rn(x, div);
+    return static_cast<int>(fminf(fmaxf(up ? ceilf(c) : floorf(c), -127.f), 127.f));
+}
+
+// The record of one block and head, of its first `count` rows, by a warp: lanes i
+// and i + 16 take 16-byte chunk i of the even and of the odd rows.
+template <bool BF16>
+__device__ __forceinline__ void block_record(const uint8_t* rows, int count, uint8_t* rec, int lane) {
+    const int i = lane & 15, odd = lane >> 4;
+    uint4 r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // Rows past the end repeat the first one, which is always there.
+        const int row = 2 * j + odd < count ? 2 * j + odd : 0;
+        r[j] = *reinterpret_cast<const uint4*>(rows + row * PG_ROW + 16 * i);
+    }
+    uint32_t hi[4] = {r[0].x, r[0].y, r[0].z, r[0].w}, lo[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+        const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            hi[c] = max2_nan<BF16>(hi[c], w[c]);
+            lo[c] = min2_nan<BF16>(lo[c], w[c]);
+        }
+    }
+    float2 top[4], low[4];
+    float m = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        hi[c] = max2_nan<BF16>(hi[c], __shfl_xor_sync(FULL_MASK, hi[c], 16));
+        lo[c] = min2_nan<BF16>(lo[c], __shfl_xor_sync(FULL_MASK, lo[c], 16));
+        top[c] = pg_unpack<BF16>(hi[c]);
+        low[c] = pg_unpack<BF16>(lo[c]);
+        finite &= pg_finite(top[c].x) && pg_finite(top[c].y) && pg_finite(low[c].x) && pg_finite(low[c].y);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(top[c].x), fabsf(top[c].y)), fmaxf(fabsf(low[c].x), fabsf(low[c].y))));
+    }
+    finite = __all_sync(FULL_MASK, finite);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, off));
+    const float scale = finite ? __fdiv_rn(m, 127.f) : INFINITY;
+    const float div = scale > 0.f ? scale : 1.f;
+    uint32_t w[4];  // largest of channels 8i .. 8i + 3, smallest of them, largest of the next four, smallest
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const bool up = (x & 1) == 0;
+        const float2 a = up ? top[x & 2] : low[x & 2], b = up ? top[(x & 2) + 1] : low[(x & 2) + 1];
+        w[x] = finite ? (code_of(a.x, div, up) & 0xff) | (code_of(a.y, div, up) & 0xff) << 8 |
+                            (code_of(b.x, div, up) & 0xff) << 16 | static_cast<uint32_t>(code_of(b.y, div, up) & 0xff) << 24
+                      : 0u;
+    }
+    if (odd == 0) *reinterpret_cast<uint4*>(rec + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane == 16) *reinterpret_cast<uint4*>(rec + 256) = make_uint4(__float_as_uint(scale), 0u, 0u, 0u);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(BOUNDS_THREADS) block_bounds_kernel(const BoundsArgs a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long first = (blockIdx.x * static_cast<long long>(BOUNDS_THREADS / 32) + (threadIdx.x >> 5)) * a.tokens;
+    const int h = blockIdx.y;
+    // Lane l looks at token first + l: is it the last of its block?
+    const long long n = first + lane;
+    int slot = -1;
+    bool last = false, bad = false;
+    if (lane < a.tokens && n < a.N) {
+        slot = a.slots[n];
+        const int next = n + 1 < a.N ? a.slots[n + 1] : -1;
+        bad = slot >= 0 && slot >= a.num_blocks * PG_BLOCK;
+        last = slot >= 0 && !bad && (slot % PG_BLOCK == PG_BLOCK - 1 || next != slot + 1);
+    }
+    unsigned todo = __ballot_sync(FULL_MASK, last);
+    while (todo != 0) {
+        const int s = __shfl_sync(FULL_MASK, slot, __ffs(todo) - 1);
+        todo &= todo - 1;
+        const size_t at = static_cast<size_t>(s / PG_BLOCK) * a.Hkv + h;
+        block_record<BF16>(a.kc + at * PG_BLOCK_BYTES, s % PG_BLOCK + 1, a.bounds + at * PG_RECORD, lane);
+    }
+    if (bad && h == 0) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
+}
+
+// ---------------------------------------------------------------- scores
+
+constexpr int SCORE_THREADS = 128;
+constexpr int SCORE_AHEAD = 4;                                   // records an 8-lane group keeps in flight
+constexpr int SCORE_BLOCKS = SCORE_THREADS / 8 * SCORE_AHEAD;    // columns a CTA scores
+constexpr uint32_t KEY_ALWAYS = 0xffffffffu;                     // above every score's key
+
+struct SelectArgs {
+    const void* q;
+    const uint8_t* bounds;
+    const int32_t* table;
+    const int32_t* ctx_len;
+    uint32_t* keys;  // [B * Hkv][max_blocks]
+    int32_t* sel;
+    int32_t* err_flag;
+    int Hq, Hkv, G, num_blocks, max_blocks, n_sel, n_first, n_last;
+};
+
+// The blocks of a request, or -1 for a bad length.
+__device__ __forceinline__ int select_blocks(const SelectArgs& a, int r) {
+    const int ctx = a.ctx_len[r];
+    return ctx < 0 || ctx > a.max_blocks * PG_BLOCK ? -1 : (ctx + PG_BLOCK - 1) / PG_BLOCK;
+}
+
+// Unsigned keys in the order of finite floats (-0 as 0); +inf gives KEY_ALWAYS.
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (x == INFINITY) return KEY_ALWAYS;
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(SCORE_THREADS) block_score_kernel(const SelectArgs a) {
+    __shared__ float warp_max[SCORE_THREADS / 32];
+    __shared__ uint32_t pos_codes[PG_D / 4], neg_codes[PG_D / 4];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int r = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+    const int nb = select_blocks(a, r);
+    const int first = blockIdx.x * SCORE_BLOCKS;
+    if (nb < 0 && blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
+    if (nb <= a.n_sel || first >= nb) return;  // all blocks are selected: no scores
+
+    const int u = threadIdx.x & 7, grp = threadIdx.x >> 3;  // an 8-lane group a record
+    uint4 rec[SCORE_AHEAD][2];
+    float scale[SCORE_AHEAD];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < SCORE_AHEAD; ++j) {
+        const int col = first + j * (SCORE_THREADS / 8) + grp;
+        rec[j][0] = rec[j][1] = make_uint4(0u, 0u, 0u, 0u);
+        scale[j] = 0.f;
+        if (col < nb) {
+            const int id = a.table[static_cast<size_t>(r) * a.max_blocks + col];
+            if (id < 0 || id >= a.num_blocks) {
+                bad = true;
+                scale[j] = INFINITY;
+            } else {
+                const uint8_t* p = a.bounds + (static_cast<size_t>(id) * a.Hkv + g) * PG_RECORD;
+                rec[j][0] = *reinterpret_cast<const uint4*>(p + 32 * u);
+                rec[j][1] = *reinterpret_cast<const uint4*>(p + 32 * u + 16);
+                scale[j] = *reinterpret_cast<const float*>(p + 256);
+            }
+        }
+    }
+    // The query's codes: thread c sums channel c over the group's heads, in order.
+    float s = 0.f;
+    {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                            (static_cast<size_t>(r) * a.Hq + static_cast<size_t>(g) * a.G) * PG_D + threadIdx.x;
+        for (int h = 0; h < a.G; ++h) {
+            const float x = pg_unpack<BF16>(q[h * PG_D]).x;
+            s = h == 0 ? x : s + x;
+        }
+    }
+    float m = fabsf(s);
+    const bool finite = __syncthreads_and(pg_finite(s)) != 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, off));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(warp_max[0], warp_max[1]), fmaxf(warp_max[2], warp_max[3]));
+    const float step = __fdiv_rn(m, 127.f);
+    const int code = finite && step > 0.f
+                         ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(s, step)), -127.f), 127.f)) : 0;
+    reinterpret_cast<int8_t*>(pos_codes)[threadIdx.x] = static_cast<int8_t>(max(code, 0));
+    reinterpret_cast<int8_t*>(neg_codes)[threadIdx.x] = static_cast<int8_t>(min(code, 0));
+    __syncthreads();
+    const uint4 qp = *reinterpret_cast<const uint4*>(pos_codes + 4 * u), qn = *reinterpret_cast<const uint4*>(neg_codes + 4 * u);
+#pragma unroll
+    for (int j = 0; j < SCORE_AHEAD; ++j) {
+        int sum = __dp4a(static_cast<int>(rec[j][0].x), static_cast<int>(qp.x), 0);
+        sum = __dp4a(static_cast<int>(rec[j][0].y), static_cast<int>(qn.x), sum);
+        sum = __dp4a(static_cast<int>(rec[j][0].z), static_cast<int>(qp.y), sum);
+        sum = __dp4a(static_cast<int>(rec[j][0].w), static_cast<int>(qn.y), sum);
+        sum = __dp4a(static_cast<int>(rec[j][1].x), static_cast<int>(qp.z), sum);
+        sum = __dp4a(static_cast<int>(rec[j][1].y), static_cast<int>(qn.z), sum);
+        sum = __dp4a(static_cast<int>(rec[j][1].z), static_cast<int>(qp.w), sum);
+        sum = __dp4a(static_cast<int>(rec[j][1].w), static_cast<int>(qn.w), sum);
+        sum += __shfl_xor_sync(FULL_MASK, sum, 4);
+        sum += __shfl_xor_sync(FULL_MASK, sum, 2);
+        sum += __shfl_xor_sync(FULL_MASK, sum, 1);
+        const int col = first + j * (SCORE_THREADS / 8) + grp;
+        if (u == 0 && col < nb) {
+            const bool always = col < a.n_first || col >= nb - a.n_last || !pg_finite(scale[j]);
+            a.keys[static_cast<size_t>(blockIdx.y) * a.max_blocks + col] =
+                always ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale[j]);
+        }
+    }
+    if (bad && u == 0) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
+}
+
+// ---------------------------------------------------------------- selection
+
+constexpr int PICK_THREADS = 512;
+constexpr int PICK_WARPS = PICK_THREADS / 32;
+constexpr int PICK_HELD = 16;  // keys a thread holds in registers; further ones are read again
+
+// One CTA a (request, KV head).  The n_sel-th largest key is found digit by digit
+// (four of 8 bits): each pass counts the keys that agree with the digits found so
+// far by their next digit.  Then one pass in the order of the columns writes those
+// above it, and of the equal ones the first.
+__global__ void __launch_bounds__(PICK_THREADS) block_pick_kernel(const SelectArgs a) {
+    __shared__ int hist[256];
+    __shared__ int found[2];           // digit, keys above it
+    __shared__ int2 warp_count[PICK_WARPS];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int r = blockIdx.x / a.Hkv;
+    const int nb = max(select_blocks(a, r), 0);
+    int32_t* sel = a.sel + static_cast<size_t>(blockIdx.x) * a.n_sel;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (nb <= a.n_sel) {
+        for (int i = tid; i < a.n_sel; i += PICK_THREADS) sel[i] = i < nb ? i : -1;
+        return;
+    }
+    const uint32_t* keys = a.keys + static_cast<size_t>(blockIdx.x) * a.max_blocks;
+    uint32_t held[PICK_HELD];
+#pragma unroll
+    for (int j = 0; j < PICK_HELD; ++j) held[j] = tid + j * PICK_THREADS < nb ? keys[tid + j * PICK_THREADS] : 0u;
+    uint32_t prefix = 0u;
+    int want = a.n_sel;  // how many of the keys that agree with the prefix are selected
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        const auto count = [&](uint32_t key) {
+            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
+        };
+#pragma unroll
+        for (int j = 0; j < PICK_HELD; ++j)
+            if (tid + j * PICK_THREADS < nb) count(held[j]);
+        for (int i = tid + PICK_HELD * PICK_THREADS; i < nb; i += PICK_THREADS) count(keys[i]);
+        __syncthreads();
+        if (warp == 0) {
+            // Lane l holds digits 255 - 8l .. 248 - 8l; a scan gives the keys above.
+            int c[8], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
+            int above = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(FULL_MASK, above, off);
+                if (lane >= off) above += v;
+            }
+            above -= sum;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (above < want && above + c[j] >= want) {
+                    found[0] = 255 - 8 * lane - j;
+                    found[1] = above;
+                }
+                above += c[j];
+            }
+        }
+        __syncthreads();
+        prefix |= static_cast<uint32_t>(found[0]) << shift;
+        want -= found[1];
+    }
+    // Column order: thread t takes columns base + t of one round after another.
+    int above = 0, equal = 0;  // selected above, and equal keys, in earlier rounds
+    for (int base = 0; base < nb; base += PICK_THREADS) {
+        const int i = base + tid;
+        const uint32_t key = i < nb ? keys[i] : 0u;
+        const bool gt = i < nb && key > prefix, eq = i < nb && key == prefix;
+        const unsigned mg = __ballot_sync(FULL_MASK, gt), me = __ballot_sync(FULL_MASK, eq);
+        if (lane == 0) warp_count[warp] = make_int2(__popc(mg), __popc(me));
+        __syncthreads();
+        int g0 = above, e0 = equal, gt_all = 0, eq_all = 0;
+#pragma unroll
+        for (int w = 0; w < PICK_WARPS; ++w) {
+            const int2 c = warp_count[w];
+            if (w < warp) {
+                g0 += c.x;
+                e0 += c.y;
+            }
+            gt_all += c.x;
+            eq_all += c.y;
+        }
+        const unsigned before = (1u << lane) - 1u;
+        g0 += __popc(mg & before);
+        e0 += __popc(me & before);
+        if (gt || (eq && e0 < want)) sel[g0 + min(e0, want)] = i;
+        above += gt_all;
+        equal += eq_all;
+        __syncthreads();
+    }
+}
+
+}  // namespace clo
+
+using namespace clo;
+
+extern "C" size_t clo_paged_bounds_bytes(int block_size, int d) {
+    return block_size == PG_BLOCK && d == PG_D ? PG_RECORD : 0;
+}
+
+extern "C" clo_status clo_paged_block_bounds(const clo_paged_block_bounds_args* args, cudaStream_t stream) {
+    if (args == nullptr) return CLO_ERR_INVALID_ARG;
+    const clo_paged_block_bounds_args& r = *args;
+    if (r.N < 0 || r.Hkv < 1 || r.num_blocks < 1 || !pg_dtype_ok(r.dtype)) return CLO_ERR_INVALID_ARG;
+    if (r.N > 0 && (r.kc == nullptr || r.slot_map == nullptr || r.bounds == nullptr)) return CLO_ERR_INVALID_ARG;
+    if (!pg_aligned(r.kc, 16) || !pg_aligned(r.bounds, 16) || !pg_aligned(r.slot_map, 4) || !pg_aligned(r.err_flag, 4))
+        return CLO_ERR_INVALID_ARG;
+    if (r.d != PG_D || r.block_size != PG_BLOCK || r.Hkv > 65535 || r.num_blocks > (1 << 26)) return CLO_ERR_UNSUPPORTED;
+    if (r.N == 0) return CLO_OK;
+    BoundsArgs a{static_cast<const uint8_t*>(r.kc), r.slot_map, r.bounds, r.err_flag, r.N, r.Hkv, r.num_blocks, 0};
+    // A warp looks at 16 tokens, about one block of a prompt; at one where that
+    // leaves few warps (a decode step: each token ends a block).
+    a.tokens = static_cast<long long>(r.N) * r.Hkv <= 32768 ? 1 : 16;
+    const long long warps = (static_cast<long long>(r.N) + a.tokens - 1) / a.tokens;
+    const unsigned grid = static_cast<unsigned>((warps + BOUNDS_THREADS / 32 - 1) / (BOUNDS_THREADS / 32));
+    const auto kernel = r.dtype == CLO_BF16 ? block_bounds_kernel<true> : block_bounds_kernel<false>;
+    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), 0)) return CLO_ERR_CUDA;
+    return launch_pdl(kernel, dim3(grid, r.Hkv), dim3(BOUNDS_THREADS), 0, stream, a) == cudaSuccess ? CLO_OK
+                                                                                                   : CLO_ERR_CUDA;
+}
+
+static bool select_sizes_ok(int B, int Hkv, int max_blocks) {
+    return B >= 0 && B <= PG_MAX_B && Hkv >= 1 && max_blocks >= 1 && max_blocks <= (1 << 20) &&
+           static_cast<long long>(B) * Hkv <= 65535 && static_cast<long long>(B) * Hkv * max_blocks < (1ll << 31);
+}
+
+extern "C" size_t clo_paged_select_workspace_size(int B, int Hkv, int max_blocks) {
+    if (!select_sizes_ok(B, Hkv, max_blocks)) return 0;
+    const size_t n = static_cast<size_t>(B) * Hkv * max_blocks * sizeof(uint32_t);
+    return n < 16 ? 16 : n;
+}
+
+extern "C" clo_status clo_paged_block_select(const clo_paged_block_select_args* args, cudaStream_t stream) {
+    if (args == nullptr) return CLO_ERR_INVALID_ARG;
+    const clo_paged_block_select_args& r = *args;
+    if (r.B < 0 || r.Hq < 1 || r.Hkv < 1 || r.Hq % r.Hkv != 0 || r.num_blocks < 1 || r.max_blocks < 1 || r.n_sel < 1 ||
+        r.n_first < 0 || r.n_last < 0 || r.n_first > r.n_sel - r.n_last || !pg_dtype_ok(r.dtype))
+        return CLO_ERR_INVALID_ARG;
+    if (r.B > 0 && (r.q == nullptr || r.bounds == nullptr || r.block_table == nullptr || r.ctx_len == nullptr || r.sel == nullptr))
+        return CLO_ERR_INVALID_ARG;
+    if (!pg_aligned(r.q, 16) || !pg_aligned(r.bounds, 16) || !pg_aligned(r.block_table, 4) || !pg_aligned(r.ctx_len, 4) ||
+        !pg_aligned(r.sel, 4) || !pg_aligned(r.err_flag, 4))
+        return CLO_ERR_INVALID_ARG;
+    if (r.d != PG_D || r.block_size != PG_BLOCK || r.Hq / r.Hkv > PG_MAX_G || r.num_blocks > (1 << 26) || r.n_sel > (1 << 20) ||
+        !select_sizes_ok(r.B, r.Hkv, r.max_blocks))
+        return CLO_ERR_UNSUPPORTED;
+    if (r.B == 0) return CLO_OK;
+    if (r.workspace == nullptr || r.ws_bytes < clo_paged_select_workspace_size(r.B, r.Hkv, r.max_blocks) ||
+        !pg_aligned(r.workspace, 16))
+        return CLO_ERR_WORKSPACE;
+    const SelectArgs a{r.q, r.bounds, r.block_table, r.ctx_len, static_cast<uint32_t*>(r.workspace), r.sel, r.err_flag,
+                       r.Hq, r.Hkv, r.Hq / r.Hkv, r.num_blocks, r.max_blocks, r.n_sel, r.n_first, r.n_last};
+    const auto score = r.dtype == CLO_BF16 ? block_score_kernel<true> : block_score_kernel<false>;
+    if (!prepare_kernel(reinterpret_cast<const void*>(score), 0) ||
+        !prepare_kernel(reinterpret_cast<const void*>(block_pick_kernel), 0))
+        return CLO_ERR_CUDA;
+    const unsigned sets = static_cast<unsigned>(r.B) * r.Hkv;
+    if (launch_pdl(score, dim3((r.max_blocks + SCORE_BLOCKS - 1) / SCORE_BLOCKS, sets), dim3(SCORE_THREADS), 0, stream, a) !=
+        cudaSuccess)
+        return CLO_ERR_CUDA;
+    return launch_pdl(block_pick_kernel, dim3(sets), dim3(PICK_THREADS), 0, stream, a) == cudaSuccess ? CLO_OK : CLO_ERR_CUDA;
+}
