@@ -135,8 +135,8 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  * ctx_len:     [B] int32 in [0, max_blocks * 16].
  * offsets:     [B + 1] int32, not descending, in [0, N], as clo_paged_plan writes
  *              them.  Rows of no request are left as they were.
- * out:         [N][Hq][d] of type `dtype`, contiguous; may be q if that is
- *              contiguous.   lse: [N][Hq] fp32 or NULL.
+ * out:         [N][Hq][d] of type `dtype`, contiguous, apart from q.
+ *              lse: [N][Hq] fp32 or NULL.
  * workspace:   >= clo_paged_chunk_workspace_size(...) bytes, 16-byte aligned.
  * err_flag:    a length out of range or offsets that descend or leave [0, N] set
  *              CLO_FLAG_BAD_CTX: a bad length zeroes the request's rows, and
@@ -236,7 +236,8 @@ size_t clo_paged_select_workspace_size(int B, int Hkv, int max_blocks);
  * the whole numbers exact and the product in fp32.  In exact numbers this is an
  * upper bound of the summed score s . K_t that clo_topk_retrieve ranks tokens by.
  * The first n_first blocks of a request and the last n_last, the one being
- * filled among them, are always selected; of the others those with the highest
+ * filled among them, are always selected (as
+ * long as there is room); of the others those with the highest
  * scores, equal ones going to the lower block, until there are n_sel.  A request
  * with no more than n_sel blocks has them all.
  * q:           [B][Hq][d] of type `dtype`, contiguous.
@@ -285,7 +286,8 @@ clo_status clo_paged_block_select(const clo_paged_block_select_args* args, cudaS
  * and bad blocks set CLO_FLAG_BAD_INDEX and zero the outputs of that request and KV
  * head, as do bad lengths (CLO_FLAG_BAD_CTX) those of the request.  With every
  * column in sel the result is that of the dense attention.
- * q, out:    [B][Hq][d] of type `dtype`, contiguous.   lse: [B][Hq] fp32 or NULL.
+ * q, out:    [B][Hq][d] of type `dtype`, contiguous, apart from one another.
+ *            lse: [B][Hq] fp32 or NULL.
  * workspace: >= clo_paged_chunk_workspace_size(Hq, Hkv, d, num_ctas) bytes,
  *            16-byte aligned.
  * Sums are in fp32; the weights are rounded to `dtype` for the product with V.

@@ -1,44 +1,1031 @@
 // clo_paged_attention.cu -- attention of chunks of new tokens over the 16-bit
 // paged cache, and decode attention over selected blocks of it.
+//
+// Work.  A request's rows of one KV head (its new tokens times the G heads of the
+// group) are cut into items of 256 rows, two tiles of 128.  An item goes over the
+// tokens that its last row sees, 128 at a time.  All items of a call, weighed by
+// their tokens, are shared out evenly, one contiguous range a CTA and one CTA an
+// SM; each CTA works its range out by itself from the lengths.  An item that a
+// border cuts leaves a partial result for each piece (sums, reference, denominator), which
+// paged_merge_kernel joins.  So few rows over a long context occupy every SM, and a
+// long prompt costs each SM the same.
+//
+// A CTA has two streams, each a warpgroup with its own scores and sums in tensor memory (4
+// x 128 columns: all of it).  An item of more than 128 rows gives a tile of rows to
+// each stream, and both go over every tile of tokens, so the tensor cores work on
+// one stream's products while the other's weights are made.  An item of up to 128
+// rows gives the streams alternate tiles of tokens, and their sums are added up at its
+// end.  A row belongs to one thread: no shuffles.  Besides:
+//   warp 8   brings K and V tiles into a ring of five (16 tokens a copy, whatever the
+//            cache's strides), in the order in which the products take them;
+//   warp 9   issues the products: S = Q K^T, both from shared memory, and O += P V with
+//            P from tensor memory, where it takes the place of S;
+//   warps 10, 11 bring the rows of q.
+// Softmax: with a reference that lies 2^6 below a maximum seen so far and moves only when
+// a score passes it by 2^14, weights up to 2^14 fit fp16 and those down to 2^-31 of
+// the largest still count, and sums in tensor memory are seldom rescaled.
+//
+// What a row does not see.  Scores are replaced before anything is made of them.  A
+// weight of 0 does not hide a V that is not finite: rows of V behind the item's
+// last token are zeroed as they are brought in; one between a row's last token and
+// the item's can only make the row's result not finite, so such results are looked at
+// again at the end and made anew by paged_row where a V that they do not see is
+// not finite (nothing of this runs on finite data).
+//
+// Every wait has a limit (about 2 s); one that runs out ends the CTA's work in order.
 #include <math.h>
 
+#include "clo_kv4_math.cuh"  // barriers, fp32 pairs
 #include "clo_paged_attention.cuh"
+#include "clo_tcgen05.cuh"
 
 namespace clo {
 
-constexpr int ROWS_THREADS = 256;
+constexpr int CH_TILE = 128;                      // tokens of a K or V tile; rows of a Q tile
+constexpr int CH_PLACES = CH_TILE / PG_BLOCK;     // blocks of a tile
+constexpr int CH_HALF = CH_TILE * 128;            // bytes of 64 channels of a tile
+constexpr int CH_TILE_BYTES = 2 * CH_HALF;
+constexpr int CH_STAGES = 5;
+constexpr int CHUNK_ROWS = 2 * CH_TILE;           // rows of an item
+constexpr int CH_THREADS = 384;
+constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
+constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
+static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
+constexpr int CH_FIXED = 128;                     // what an item costs beside its tokens, in tokens
+constexpr int CH_LEAST = 256;                     // tokens that are worth a CTA of their own
+constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
+constexpr int CH_SMALL = 2048;                    // shared memory beside the tiles
+constexpr int CH_SMEM = CHUNK_ROWS * PG_ROW + CH_STAGES * CH_TILE_BYTES + CH_SMALL + 1024;
+constexpr int MERGE_THREADS = 256;
 
-// A warp a (query row, head).
+// Where a range starts or ends: tile `cut` of item (request, KV head, item).
+struct ChunkPos {
+    int r, h, j, cut;
+};
+
+struct ChunkWs {
+    float* o;     // [CTA][head piece, tail piece][256 rows][128]
+    float2* ml;   // [CTA][2][256] reference and denominator; denominator -1: bad data
+    int4* desc;   // [CTA][8]: see CH_DESC
+};
+enum { DESC_START, DESC_END, DESC_FLAGS };  // flags: x head piece, y that piece ends its item, z tail piece, w look again
+
+struct alignas(16) ChunkSmall {
+    unsigned long long full[CH_STAGES], empty[CH_STAGES], q_full, q_empty, s_full[2], p_ready[2], o_full[2], x_full, x_empty, drain;
+    ChunkPos start, end;
+    uint32_t tmem;
+    int dead;      // a wait ran out
+    int again;     // a complete item has a result that is not finite
+    int bad[8];    // by item: a place that could not be read
+    float2 ml1[CH_TILE];  // stream 1's reference and denominator, for items with one tile of rows
+};
+static_assert(sizeof(ChunkSmall) <= CH_SMALL, "");
+
+// ---------------------------------------------------------------- shares
+
+// Tokens that the last row of item j sees (sparse: the selected places' length).
+template <bool SPARSE>
+__device__ __forceinline__ int item_sees(const PagedAttnArgs& a, const PagedReq& q, int j) {
+    if constexpr (SPARSE) {
+        return paged_places<true>(a, q.ctx) * PG_BLOCK;
+    } else {
+        const unsigned upto = (static_cast<unsigned>(j + 1) * CHUNK_ROWS + a.G - 1) / static_cast<unsigned>(a.G);
+        return max(q.ctx - q.n + static_cast<int>(min(static_cast<unsigned>(q.n), upto)), 0);
+    }
+}
+__device__ __forceinline__ int items_of(const PagedAttnArgs& a, const PagedReq& q) {
+    return static_cast<int>((static_cast<long long>(q.n) * a.G + CHUNK_ROWS - 1) / CHUNK_ROWS);
+}
+
+// The weights of a request's items of one KV head, in units of 1 / G token: item j
+// weighs G (tokens before the new ones + CH_FIXED) + 256 (j + 1), the last one
+// by the request's length.
+struct Weights {
+    long long each, last;  // each = without the part that rises
+    int items;
+    __device__ long long before(int j) const {  // items 0 .. j - 1
+        return j < items ? j * each + (CHUNK_ROWS / 2) * static_cast<long long>(j) * (j + 1) : all();
+    }
+    __device__ long long all() const {
+        const long long m = items - 1;
+        return items == 0 ? 0 : m * each + (CHUNK_ROWS / 2) * m * (m + 1) + last;
+    }
+};
+template <bool SPARSE>
+__device__ __forceinline__ Weights weights_of(const PagedAttnArgs& a, const PagedReq& q) {
+    Weights w;
+    w.items = items_of(a, q);
+    const long long G = a.G, base = SPARSE ? 0 : max(q.ctx - q.n, 0);
+    w.each = G * (base + CH_FIXED);
+    w.last = G * ((SPARSE ? item_sees<true>(a, q, 0) : base + q.n) + CH_FIXED);
+    return w;
+}
+
+// The place of weight x; prefix[r] = weight of the requests before r.
+template <bool SPARSE>
+__device__ ChunkPos locate(const PagedAttnArgs& a, const long long* prefix, long long x) {
+    if (x >= prefix[a.B]) return ChunkPos{a.B, 0, 0, 0};
+    int lo = 0, hi = a.B - 1;  // the first r with prefix[r + 1] > x
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid + 1] > x) hi = mid;
+        else lo = mid + 1;
+    }
+    const int r = lo;
+    const PagedReq q = paged_request<SPARSE>(a, r);
+    const Weights w = weights_of<SPARSE>(a, q);
+    const long long head = w.all();
+    long long rest = x - prefix[r];
+    const int h = static_cast<int>(rest / head);
+    rest -= h * head;
+    lo = 0, hi = w.items - 1;  // the last j with before(j) <= rest
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (w.before(mid) <= rest) lo = mid;
+        else hi = mid - 1;
+    }
+    const int tiles = (item_sees<SPARSE>(a, q, lo) + CH_TILE - 1) / CH_TILE;
+    const long long off = rest - w.before(lo), size = w.before(lo + 1) - w.before(lo);
+    return ChunkPos{r, h, lo, static_cast<int>(off * tiles / size)};
+}
+
+// One piece of work: tiles lo .. hi - 1 of an item of `tiles`.
+struct Piece {
+    PagedReq q;
+    int r, h, j, lo, hi, tiles;
+    int rows;  // of the item
+    int sees;  // tokens of the item's last row
+    __device__ bool whole() const { return lo == 0 && hi == tiles; }
+};
+
+// The pieces from `start` to `end`, in order.
+template <bool SPARSE>
+struct Walk {
+    PagedReq q;
+    ChunkPos at, end;
+    int items;
+    bool loaded;
+    __device__ Walk(const ChunkPos& s, const ChunkPos& e) : at(s), end(e), items(0), loaded(false) {}
+    __device__ bool next(const PagedAttnArgs& a, Piece& p) {
+        while (at.r < a.B) {
+            if (at.r > end.r) return false;
+            if (!loaded) {
+                q = paged_request<SPARSE>(a, at.r);
+                items = items_of(a, q);
+                loaded = true;
+            }
+            if (items > 0 && at.h < a.Hkv) break;
+            at = ChunkPos{at.r + 1, 0, 0, 0};
+            loaded = false;
+        }
+        if (at.r >= a.B) return false;
+        if (at.r == end.r && (at.h > end.h || (at.h == end.h && at.j > end.j))) return false;
+        const bool at_end = at.r == end.r && at.h == end.h && at.j == end.j;
+        if (at_end && end.cut <= at.cut) return false;
+        p.q = q;
+        p.r = at.r;
+        p.h = at.h;
+        p.j = at.j;
+        p.sees = item_sees<SPARSE>(a, q, at.j);
+        p.tiles = (p.sees + CH_TILE - 1) / CH_TILE;
+        p.rows = static_cast<int>(min(static_cast<long long>(CHUNK_ROWS),
+                                      static_cast<long long>(q.n) * a.G - static_cast<long long>(at.j) * CHUNK_ROWS));
+        p.lo = at.cut;
+        p.hi = at_end ? min(end.cut, p.tiles) : p.tiles;
+        at.cut = 0;
+        if (++at.j == items) {
+            at.j = 0;
+            ++at.h;
+        }
+        return true;
+    }
+};
+
+// Row (of the item) -> its token among the request's new ones and its head in the group.
+__device__ __forceinline__ void row_of(const PagedAttnArgs& a, int j, int row, int& token, int& g) {
+    const unsigned x = static_cast<unsigned>(j) * CHUNK_ROWS + row;
+    token = x / static_cast<unsigned>(a.G);
+    g = x - token * a.G;
+}
+
+// ---------------------------------------------------------------- small parts
+
+__device__ __forceinline__ void mbar_init_n(uint32_t bar, int n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(n) : "memory");
+}
+// False if the wait ran out, here or in another warp.
+__device__ __forceinline__ bool ch_wait(unsigned long long& bar, uint32_t parity, ChunkSmall* sm) {
+    const uint32_t b = smem_u32(&bar);
+    if (mbar_try(b, parity)) return true;
+    const long long t0 = clock64();
+    do {
+        if (mbar_try(b, parity)) return true;
+        if (*reinterpret_cast<volatile int*>(&sm->dead) != 0) return false;
+    } while (clock64() - t0 < KV4_WAIT_CLOCKS);
+    *reinterpret_cast<volatile int*>(&sm->dead) = 1;
+    return false;
+}
+__device__ __forceinline__ bool ch_warp_wait(unsigned long long& bar, uint32_t parity, ChunkSmall* sm) {
+    return __all_sync(FULL_MASK, ch_wait(bar, parity, sm));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int R>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R)); }
+
+// ---------------------------------------------------------------- the copying warp
+
+template <bool SPARSE>
+struct Loader {
+    const PagedAttnArgs& a;
+    const CUtensorMap *mk, *mv;
+    ChunkSmall* sm;
+    uint32_t ring;
+    int lane;
+    int it = 0;  // tiles brought so far
+
+    // A tile's 8 places are lanes 8 (t % 4) .. of `places`.
+    __device__ bool tile(const Piece& p, bool is_v, int t, int places, int slot) {
+        const int stage = it % CH_STAGES;
+        if (!ch_warp_wait(sm->empty[stage], (it / CH_STAGES & 1) ^ 1, sm)) return false;
+        ++it;
+        const uint32_t dst = ring + stage * CH_TILE_BYTES, bar = smem_u32(&sm->full[stage]);
+        const int mine = __shfl_sync(FULL_MASK, places, (t & 3) * CH_PLACES + (lane & 7));
+        if (__any_sync(FULL_MASK, mine < 0) && lane == 0) {  // (before the arrival below)
+            *reinterpret_cast<volatile int*>(&sm->bad[slot]) = 1;
+            report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
+        }
+        const int rows = mine < 0 ? 0 : mine & 31, id = mine >> 5;
+        const bool copy = is_v ? rows == PG_BLOCK : rows > 0;
+        const unsigned copied = __ballot_sync(FULL_MASK, copy) & 0xffu;
+        if (is_v && copied != 0xffu) {
+            // Rows that nobody sees are zeros: a weight of 0 times what lies there need
+            // not be 0.
+            for (int b = 0; b < CH_PLACES; ++b) {
+                const int brows = __shfl_sync(FULL_MASK, rows, b), bid = __shfl_sync(FULL_MASK, id, b);
+                if (brows == PG_BLOCK) continue;
+                const long long base = brows > 0 ? static_cast<long long>(bid) * a.kv_block + p.h * a.kv_head : 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = (lane >> 4) + 2 * k, c = lane & 15;
+                    const uint4 x = row < brows ? *reinterpret_cast<const uint4*>(a.vc + base + row * a.kv_token + c * 16)
+                                                : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t to = dst + (c >> 3) * CH_HALF + (b * PG_BLOCK + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                                 : "memory");
+                }
+            }
+            async_proxy_fence();
+            __syncwarp();
+        }
+        if (lane == 0) mbar_expect(bar, __popc(copied) * PG_BLOCK_BYTES);
+        __syncwarp();
+        if (lane < 16 && copy)
+            tma_load_5d(dst + (lane >> 3) * CH_HALF + (lane & 7) * (PG_BLOCK * 128), is_v ? mv : mk, bar, 0, lane >> 3, 0, p.h, id);
+        return true;
+    }
+
+    __device__ bool piece(const Piece& p, int slot) {
+        const int n = p.hi - p.lo, ahead = p.rows > CH_TILE ? 1 : 2;
+        const int sees = SPARSE ? p.q.ctx : p.sees, last = paged_places<SPARSE>(a, sees);
+        const auto fetch = [&](int group) {
+            const int x = group * 32 + lane;
+            return x < last ? paged_place<SPARSE>(a, p.r, p.h, sees, x) : 0;
+        };
+        // Places of four tiles a register: the group that K is in, the one before, the next.
+        int group = p.lo >> 2, cur = fetch(group), prev = 0, next = fetch(group + 1);
+        const auto k_tile = [&](int t) {
+            if ((t >> 2) != group) {
+                prev = cur;
+                cur = next;
+                next = fetch(++group + 1);
+            }
+            return tile(p, false, t, cur, slot);
+        };
+        for (int i = 0; i < min(ahead, n); ++i)
+            if (!k_tile(p.lo + i)) return false;
+        for (int i = 0; i < n; ++i) {
+            const int t = p.lo + i;
+            if (!tile(p, true, t, (t >> 2) == group ? cur : prev, slot)) return false;
+            if (i + ahead < n && !k_tile(t + ahead)) return false;
+        }
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------- the thread that issues products
+
+template <bool BF16>
+struct Issuer {
+    ChunkSmall* sm;
+    uint32_t q, ring, tmem;
+    int it = 0;              // tiles taken so far
+    uint32_t p_count[2] = {0, 0};
+    uint32_t q_count = 0;
+
+    __device__ bool wait(unsigned long long& bar, uint32_t parity) { return ch_wait(bar, parity, sm); }
+    __device__ int take() { return it++; }
+    __device__ bool here(int x) { return wait(sm->full[x % CH_STAGES], x / CH_STAGES & 1); }
+    __device__ void release(int x) { tc_commit(smem_u32(&sm->empty[x % CH_STAGES])); }
+    // S of stream s = Q of row tile qt times K of tile x.
+    __device__ void scores(int s, int qt, int x) {
+        const uint32_t k = ring + (x % CH_STAGES) * CH_TILE_BYTES, qa = q + qt * CH_TILE_BYTES;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t off = (i >> 2) * CH_HALF + (i & 3) * 32;
+            tc_mma(tmem + s * CH_TILE, tc_tile(qa + off, 16), tc_tile(k + off, 16), tc_shape(BF16, CH_TILE, CH_TILE, false), i > 0);
+        }
+        tc_commit(smem_u32(&sm->s_full[s]));
+    }
+    // O of stream s (+)= its weights times V of tile x.
+    __device__ void sums(int s, int x, bool add) {
+        const uint32_t v = ring + (x % CH_STAGES) * CH_TILE_BYTES;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            tc_mma_ts(tmem + (2 + s) * CH_TILE, tmem + s * CH_TILE + 8 * i, tc_tile(v + i * 2048, CH_HALF),
+                      tc_shape(BF16, CH_TILE, CH_TILE, true), add || i > 0);
+    }
+    __device__ bool weights(int s) {
+        if (!wait(sm->p_ready[s], p_count[s]++ & 1)) return false;
+        tc_fence_after();
+        return true;
+    }
+
+    __device__ bool piece(const Piece& p) {
+        const int n = p.hi - p.lo;
+        if (!wait(sm->q_full, q_count++ & 1)) return false;
+        tc_fence_after();
+        if (p.rows > CH_TILE) {
+            int k = take();
+            if (!here(k)) return false;
+            scores(0, 0, k);
+            scores(1, 1, k);
+            release(k);
+            if (n == 1) tc_commit(smem_u32(&sm->q_empty));
+            for (int i = 0; i < n; ++i) {
+                const int v = take();
+                const bool more = i + 1 < n;
+                if (more) k = take();
+                if (!here(v)) return false;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (!weights(s)) return false;
+                    sums(s, v, i > 0);
+                    if (s == 1) release(v);
+                    if (more) {
+                        if (s == 0 && !here(k)) return false;
+                        scores(s, s, k);
+                    } else {
+                        tc_commit(smem_u32(&sm->o_full[s]));
+                    }
+                }
+                if (more) release(k);
+                if (i + 2 == n) tc_commit(smem_u32(&sm->q_empty));
+            }
+        } else {
+            for (int i = 0; i < min(n, 2); ++i) {
+                const int k = take();
+                if (!here(k)) return false;
+                scores(i, 0, k);
+                release(k);
+            }
+            if (n <= 2) tc_commit(smem_u32(&sm->q_empty));
+            for (int i = 0; i < n; ++i) {
+                const int s = i & 1, v = take();
+                const bool more = i + 2 < n;
+                const int k = more ? take() : 0;
+                if (!here(v) || !weights(s)) return false;
+                sums(s, v, i >= 2);
+                release(v);
+                if (more) {
+                    if (!here(k)) return false;
+                    scores(s, 0, k);
+                    release(k);
+                    if (i + 3 == n) tc_commit(smem_u32(&sm->q_empty));
+                } else {
+                    tc_commit(smem_u32(&sm->o_full[s]));
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------- the warps that bring q
+
+template <bool SPARSE>
+__device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Piece& p, uint32_t q, int thread) {
+    const int tiles = p.rows > CH_TILE ? 2 : 1, c = thread & 15;
+    for (int row = thread >> 4; row < tiles * CH_TILE; row += 4) {
+        const uint32_t to = q + (row >> 7) * CH_TILE_BYTES + (c >> 3) * CH_HALF + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
+        int token, g;
+        row_of(a, p.j, row, token, g);
+        const bool there = row < p.rows;
+        const uint8_t* src = a.q;
+        if (there) src += (p.q.row0 + token) * a.q_stride + (p.h * a.G + g) * PG_ROW + c * 16;
+        cp_async_16(to, src, there ? 16 : 0);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    async_proxy_fence();
+}
+
+// ---------------------------------------------------------------- the softmax warpgroups
+
 template <bool BF16, bool SPARSE>
-__global__ void __launch_bounds__(ROWS_THREADS) paged_rows_kernel(const PagedAttnArgs a) {
-    pdl_launch_dependents();
+struct RowSoftmax {
+    const PagedAttnArgs& a;
+    const ChunkWs& ws;
+    ChunkSmall* sm;
+    int s;            // stream
+    int tid;          // thread of the warpgroup: the row of its tile
+    uint32_t tmem;    // this warp's lanes of column 0
+    uint32_t s_count = 0, o_count[2] = {0, 0}, x_count = 0, e_count = 0;
+    int piece_count = 0;
+
+    // The weights of one tile of tokens from their scores.  sees: tokens of the
+    // tile that the row sees; first: of this piece.
+    __device__ __forceinline__ void tile(int sees, uint32_t place_rows, bool masked, bool first, float& ref, float& sum) {
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_load32(x[c], tmem + s * CH_TILE + 32 * c);
+        tmem_wait_load();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_loaded32(x[c]);
+        if (masked) {
+            if constexpr (SPARSE) {
+                // place_rows of lanes 0 .. 7: the tokens of each place
+#pragma unroll
+                for (int b = 0; b < CH_PLACES; ++b) {
+                    const int rows = __shfl_sync(FULL_MASK, place_rows, b);
+#pragma unroll
+                    for (int i = 0; i < PG_BLOCK; ++i)
+                        if (i >= rows) x[b / 2][(b & 1) * 16 + i] = -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i >= sees) x[c][i] = -INFINITY;
+            }
+        }
+        float m[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            m[c] = fmaxf(x[c][0], x[c][1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) m[c] = fmaxf(m[c], fmaxf(x[c][i], x[c][i + 1]));
+        }
+        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * a.scale_log2;
+        if (first) {
+            ref = top == -INFINITY ? top : top - CH_LIFT;
+            sum = 0.f;
+        } else {
+            const bool moves = top - CH_SLACK > ref;
+            if (__any_sync(FULL_MASK, moves)) {
+                // The sums of the earlier tiles are complete: the product that made these
+                // scores came after them.
+                const float to = moves ? top - CH_LIFT : ref;
+                const float f = moves ? ex2(ref - to) : 1.f;
+                ref = to;
+                sum *= f;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float o[16];
+                    const uint32_t at = tmem + (2 + s) * CH_TILE + 16 * c;
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                        "%14, %15}, [%16];\n tcgen05.wait::ld.sync.aligned;\n"
+                        : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]),
+                          "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
+                        : "r"(at)
+                        : "memory");
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] *= f;
+                    asm volatile(
+                        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                        "%14, %15, %16};\n" ::"r"(at),
+                        "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7]), "f"(o[8]),
+                        "f"(o[9]), "f"(o[10]), "f"(o[11]), "f"(o[12]), "f"(o[13]), "f"(o[14]), "f"(o[15])
+                        : "memory");
+                }
+            }
+        }
+        const float r = ref == -INFINITY ? 0.f : ref;
+        const float2 scale = make_float2(a.scale_log2, a.scale_log2), minus = make_float2(-r, -r);
+        float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int c = 2 * half + i / 16, k = 2 * (i & 15);
+                float2 y = fma2(make_float2(x[c][k], x[c][k + 1]), scale, minus);
+                y = make_float2(ex2(y.x), ex2(y.y));
+                w[i] = pg_pack<BF16>(y.x, y.y);
+                l[i & 1] = add2(l[i & 1], y);
+            }
+            tmem_store32(tmem + s * CH_TILE + 32 * half, w);
+        }
+        l[0] = add2(l[0], l[1]);
+        sum += l[0].x + l[0].y;
+        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(smem_u32(&sm->p_ready[s]));
+    }
+
+    // Writes a row's result: out and lse of a whole item, else its piece's sums.
+    template <typename Load>
+    __device__ __forceinline__ void write(const Piece& p, int row, bool bad, float ref, float sum, Load load) {
+        const bool valid = row < p.rows;
+        int token, g;
+        row_of(a, p.j, row, token, g);
+        const size_t place = (static_cast<size_t>(p.q.row0) + token) * a.Hq + p.h * a.G + g;
+        const bool whole = p.whole();
+        const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (p.lo == 0)) * CHUNK_ROWS + row;
+        const bool none = bad || !(sum != 0.f);  // (a NaN is something)
+        const float inv = none ? 0.f : 1.f / sum;
+        float odd = 0.f;  // turns NaN with a value that is not finite
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float o[32];
+            load(o, c);
+            if (whole) {
+                uint4* dst = reinterpret_cast<uint4*>(a.out + place * PG_ROW + c * 64);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    o[i] = none ? 0.f : o[i] * inv;
+                    odd = fmaf(o[i], 0.f, odd);
+                    if constexpr (!BF16)  // rounded weights may pass the largest V by a little
+                        if (fabsf(o[i]) <= 66000.f) o[i] = fminf(fmaxf(o[i], -65504.f), 65504.f);
+                }
+                if (valid) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pg_pack<BF16>(o[8 * i], o[8 * i + 1]), pg_pack<BF16>(o[8 * i + 2], o[8 * i + 3]),
+                                            pg_pack<BF16>(o[8 * i + 4], o[8 * i + 5]), pg_pack<BF16>(o[8 * i + 6], o[8 * i + 7]));
+                }
+            } else if (valid) {
+                float4* dst = reinterpret_cast<float4*>(ws.o + slot * PG_D + c * 32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        }
+        if (!valid) return;
+        if (whole) {
+            if (a.lse != nullptr) a.lse[place] = none ? -INFINITY : (ref + log2f(sum)) * LN2;
+            if (!SPARSE && odd != 0.f) *reinterpret_cast<volatile int*>(&sm->again) = 1;
+        } else {
+            ws.ml[slot] = make_float2(ref, bad ? -1.f : sum);
+        }
+    }
+
+    __device__ bool piece(const Piece& p) {
+        const int n = p.hi - p.lo;
+        const bool two = p.rows > CH_TILE;
+        const int row = two ? s * CH_TILE + tid : tid;
+        if (n == 0) {  // no row of the item sees a token
+            if (two || s == 0) write(p, row, false, -INFINITY, 0.f, [](float (&o)[32], int) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            });
+            return true;
+        }
+        const int lane = tid & 31;
+        int token, g;
+        row_of(a, p.j, row, token, g);
+        // Rows past the item's (their results are not used) see everything.
+        const int sees = SPARSE || row >= p.rows ? 0x7fffffff : paged_sees<false>(p.q, token);
+        const int places = SPARSE ? paged_places<true>(a, p.q.ctx) : 0;
+        const auto place_rows = [&](int t) {  // sparse: lanes 0 .. 7, the tokens of each place
+            const int x = t * CH_PLACES + (lane & 7);
+            return x < places ? max(paged_place<true>(a, p.r, p.h, p.q.ctx, x), 0) & 31 : 0;
+        };
+        float ref = -INFINITY, sum = 0.f;
+        const int step = two ? 1 : 2, t0 = p.lo + (two ? 0 : s);
+        int rows_next = SPARSE && t0 < p.hi ? place_rows(t0) : 0;
+        for (int t = t0; t < p.hi; t += step) {
+            const int rows_here = rows_next;
+            if (SPARSE && t + step < p.hi) rows_next = place_rows(t + step);
+            const int seen = sees - t * CH_TILE;
+            const bool masked = SPARSE ? __any_sync(FULL_MASK, rows_here != PG_BLOCK) : __any_sync(FULL_MASK, seen < CH_TILE);
+            if (!ch_warp_wait(sm->s_full[s], s_count++ & 1, sm)) return false;
+            tc_fence_after();
+            tile(seen, rows_here, masked, t == t0, ref, sum);
+        }
+        const bool second = two || n > 1;  // stream 1 had tiles
+        if (s == 0 || two) {
+            if (!ch_warp_wait(sm->o_full[s], o_count[s] & 1, sm)) return false;
+            if (s == 0 && !two && second && !ch_warp_wait(sm->o_full[1], o_count[1] & 1, sm)) return false;
+        }
+        ++o_count[0];
+        if (second) ++o_count[1];
+        const bool bad = *reinterpret_cast<volatile int*>(&sm->bad[piece_count & 7]) != 0;
+        ++piece_count;
+        tc_fence_after();
+        if (two || !second) {
+            if (s == 1 && !two) return true;
+            write(p, row, bad, ref, sum, [&](float (&o)[32], int c) {
+                tmem_load32(o, tmem + (2 + s) * CH_TILE + 32 * c);
+                tmem_wait_load();
+                tmem_loaded32(o);
+            });
+            tc_fence_before();
+            return true;
+        }
+        // One tile of rows: stream 0 adds stream 1's sums to its own.
+        if (s == 1) {
+            sm->ml1[tid] = make_float2(ref, sum);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->x_full));
+            return ch_warp_wait(sm->x_empty, e_count++ & 1, sm);
+        }
+        if (!ch_warp_wait(sm->x_full, x_count++ & 1, sm)) return false;
+        const volatile float* ml1 = reinterpret_cast<const volatile float*>(&sm->ml1[tid]);
+        const float2 other = make_float2(ml1[0], ml1[1]);
+        const float to = fmaxf(ref, other.x);
+        const float f0 = ref == -INFINITY ? 0.f : ex2(ref - to), f1 = other.x == -INFINITY ? 0.f : ex2(other.x - to);
+        write(p, row, bad, to, sum * f0 + other.y * f1, [&](float (&o)[32], int c) {
+            float o1[32];
+            tmem_load32(o, tmem + 2 * CH_TILE + 32 * c);
+            tmem_load32(o1, tmem + 3 * CH_TILE + 32 * c);
+            tmem_wait_load();
+            tmem_loaded32(o);
+            tmem_loaded32(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + o1[i] * f1;
+        });
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->x_empty));
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------- the main kernel
+
+template <bool BF16, bool SPARSE>
+__global__ void __launch_bounds__(CH_THREADS, 1)
+    paged_chunk_kernel(const PagedAttnArgs a, const ChunkWs ws, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t* ring = base + CHUNK_ROWS * PG_ROW;
+    ChunkSmall* sm = reinterpret_cast<ChunkSmall*>(ring + CH_STAGES * CH_TILE_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < CH_STAGES; ++i) {
+            mbar_init_n(smem_u32(&sm->full[i]), 1);
+            mbar_init_n(smem_u32(&sm->empty[i]), 1);
+        }
+        mbar_init_n(smem_u32(&sm->q_full), 64);
+        mbar_init_n(smem_u32(&sm->q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init_n(smem_u32(&sm->s_full[i]), 1);
+            mbar_init_n(smem_u32(&sm->p_ready[i]), 4);
+            mbar_init_n(smem_u32(&sm->o_full[i]), 1);
+        }
+        mbar_init_n(smem_u32(&sm->x_full), 4);
+        mbar_init_n(smem_u32(&sm->x_empty), 4);
+        mbar_init_n(smem_u32(&sm->drain), 1);
+        sm->dead = sm->again = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(smem_u32(&sm->tmem), 4 * CH_TILE);
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long warps = static_cast<long long>(gridDim.x) * (ROWS_THREADS / 32);
-    const long long w0 = blockIdx.x * static_cast<long long>(ROWS_THREADS / 32) + (threadIdx.x >> 5);
-    for (int r = 0; r < a.B; ++r) {
-        const PagedReq req = paged_request<SPARSE>(a, r);
-        if (req.bad && w0 == 0 && lane == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
-        for (long long w = w0; w < static_cast<long long>(req.n) * a.Hq; w += warps)
-            paged_row<BF16, SPARSE>(a, r, req, static_cast<int>(w / a.Hq), static_cast<int>(w % a.Hq), lane);
+    pdl_launch_dependents();
+
+    // The weights of the requests, summed up, in the ring's memory.
+    long long* prefix = reinterpret_cast<long long*>(ring);
+    long long* warp_sum = prefix + PG_MAX_B + 1;
+    {
+        const int per = (a.B + CH_THREADS - 1) / CH_THREADS, r0 = threadIdx.x * per, r1 = min(a.B, r0 + per);
+        long long local = 0;
+        bool bad = false;
+        for (int r = r0; r < r1; ++r) {
+            const PagedReq q = paged_request<SPARSE>(a, r);
+            bad |= q.bad;
+            local += weights_of<SPARSE>(a, q).all() * a.Hkv;
+        }
+        if (bad && blockIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
+        long long sum = local;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(FULL_MASK, sum, off);
+            if (lane >= off) sum += v;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        sum -= local;
+        if (threadIdx.x == 0) prefix[0] = 0;
+        for (int r = r0; r < r1; ++r) {
+            sum += weights_of<SPARSE>(a, paged_request<SPARSE>(a, r)).all() * a.Hkv;
+            prefix[r + 1] = sum;
+        }
+        __syncthreads();
+    }
+    const int cta = blockIdx.x;
+    if (lane == 0 && warp < 2) {
+        const long long all = prefix[a.B];
+        const long long least = static_cast<long long>(a.G) * (CH_LEAST + CH_FIXED);
+        const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), all / least));
+        const long long c = min(static_cast<long long>(cta) + warp, ctas);
+        (warp == 0 ? sm->start : sm->end) = locate<SPARSE>(a, prefix, all / ctas * c + all % ctas * c / ctas);
+    }
+    tc_fence_before();
+    async_proxy_fence();  // copies will write where the weights lie
+    __syncthreads();
+    tc_fence_after();
+    const ChunkPos start = sm->start, end = sm->end;
+    const uint32_t tmem = sm->tmem;
+    Walk<SPARSE> walk(start, end);
+    Piece p;
+
+    if (warp < 8) {
+        regs_up<CH_REGS_SOFTMAX>();
+        RowSoftmax<BF16, SPARSE> w{a, ws, sm, warp >> 2, static_cast<int>(threadIdx.x) & 127,
+                                tmem + (static_cast<uint32_t>(warp & 3) << 21)};
+        while (walk.next(a, p))
+            if (!w.piece(p)) break;
+    } else {
+        regs_down<CH_REGS_REST>();
+        if (warp == 8) {
+            Loader<SPARSE> w{a, &map_k, &map_v, sm, smem_u32(ring), lane};
+            int head = 0, head_ends = 0, tail = 0, count = 0;
+            bool ok = true;
+            while (ok && walk.next(a, p)) {
+                if (p.lo > 0) {
+                    head = 1;
+                    head_ends = p.hi == p.tiles;
+                } else if (p.hi < p.tiles) {
+                    tail = 1;
+                }
+                if (p.hi == p.lo) continue;
+                if (lane == 0) *reinterpret_cast<volatile int*>(&sm->bad[count & 7]) = 0;
+                ok = w.piece(p, count & 7);
+                ++count;
+            }
+            if (lane == 0) {
+                int4* d = ws.desc + static_cast<size_t>(cta) * 8;
+                d[DESC_START] = make_int4(start.r, start.h, start.j, start.cut);
+                d[DESC_END] = make_int4(end.r, end.h, end.j, end.cut);
+                d[DESC_FLAGS] = make_int4(head, head_ends, tail, 0);
+            }
+            if (!ok)  // copies in flight land before the memory is given up
+                for (int x = max(w.it - CH_STAGES, 0); x < w.it; ++x)
+                    mbar_wait(smem_u32(&sm->full[x % CH_STAGES]), x / CH_STAGES & 1);
+        } else if (warp == 9) {
+            if (lane == 0) {
+                Issuer<BF16> w{sm, smem_u32(base), smem_u32(ring), tmem};
+                bool ok = true;
+                while (ok && walk.next(a, p))
+                    if (p.hi > p.lo) ok = w.piece(p);
+                if (!ok) {  // products in flight end before tensor memory is given up
+                    tc_commit(smem_u32(&sm->drain));
+                    mbar_wait(smem_u32(&sm->drain), 0);
+                }
+            }
+            __syncwarp();
+        } else {
+            uint32_t count = 0;
+            while (walk.next(a, p)) {
+                if (p.hi == p.lo) continue;
+                if (!ch_warp_wait(sm->q_empty, (count++ & 1) ^ 1, sm)) break;
+                bring_queries<SPARSE>(a, p, smem_u32(base), static_cast<int>(threadIdx.x) - 320);
+                mbar_arrive(smem_u32(&sm->q_full));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (sm->dead != 0) report_error(a.err_flag, CLO_FLAG_TIMEOUT);
+        ws.desc[static_cast<size_t>(cta) * 8 + DESC_FLAGS].w = sm->again;
+    }
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_free(tmem, 4 * CH_TILE);
     }
 }
 
-static clo_status run_paged_attention(const PagedAttnArgs& a, bool sparse, clo_dtype dtype, const clo_attn_opts* opts,
-                                      cudaStream_t stream) {
-    const auto kernel = dtype == CLO_BF16 ? (sparse ? paged_rows_kernel<true, true> : paged_rows_kernel<true, false>)
-                                          : (sparse ? paged_rows_kernel<false, true> : paged_rows_kernel<false, false>);
-    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), 0)) return CLO_ERR_CUDA;
+// ---------------------------------------------------------------- joining pieces, looking again
+
+// Whether V of a token in [from, to), which some row does not see, is not finite; a warp.
+template <bool BF16>
+__device__ bool hidden_odd(const PagedAttnArgs& a, int r, int h, int from, int to, int lane) {
+    bool odd = false;
+    for (int t = from; t < to; ++t) {
+        const int at = paged_place<false>(a, r, h, to, t / PG_BLOCK);
+        if (at < 0) continue;
+        const uint2 w = *reinterpret_cast<const uint2*>(a.vc + static_cast<long long>(at / 32) * a.kv_block + h * a.kv_head +
+                                                        (t % PG_BLOCK) * a.kv_token + lane * 8);
+        const float2 x = pg_unpack<BF16>(w.x), y = pg_unpack<BF16>(w.y);
+        odd |= !(pg_finite(x.x) && pg_finite(x.y) && pg_finite(y.x) && pg_finite(y.y));
+    }
+    return __any_sync(FULL_MASK, odd);
+}
+
+// Makes a row whose result is not finite anew if that may come from what it does not see.
+template <bool BF16>
+__device__ __noinline__ void look_again(const PagedAttnArgs& a, const PagedReq& q, int r, int h, int j, int row, int lane) {
+    int token, g;
+    row_of(a, j, row, token, g);
+    if (hidden_odd<BF16>(a, r, h, paged_sees<false>(q, token), item_sees<false>(a, q, j), lane))
+        paged_row<BF16, false>(a, r, q, token, h * a.G + g, lane);
+}
+
+template <bool BF16, bool SPARSE>
+__global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedAttnArgs a, const ChunkWs ws, int ctas, int rows_each) {
+    __shared__ int last;
+    __shared__ float4 part[MERGE_THREADS / 32][32];
+    __shared__ float2 part_ml[MERGE_THREADS / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int WARPS = MERGE_THREADS / 32;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int c = blockIdx.x;
+    const int4 flags = ws.desc[static_cast<size_t>(c) * 8 + DESC_FLAGS];
+    const int row0 = blockIdx.y * rows_each;
+    if (flags.z != 0) {
+        // The item that starts in CTA c and ends in a later one: its pieces are c's tail
+        // and the head pieces of the CTAs up to `last` (one with no share has none).
+        const int4 e = ws.desc[static_cast<size_t>(c) * 8 + DESC_END];
+        const PagedReq q = paged_request<SPARSE>(a, e.x);
+        const int rows = static_cast<int>(min(static_cast<long long>(CHUNK_ROWS),
+                                              static_cast<long long>(q.n) * a.G - static_cast<long long>(e.z) * CHUNK_ROWS));
+        if (row0 < rows) {
+            if (warp == 0) {
+                int found = -1;
+                for (int x = c + 1; found < 0 && x < ctas; x += 32) {
+                    const int4 f = x + lane < ctas ? ws.desc[static_cast<size_t>(x + lane) * 8 + DESC_FLAGS] : make_int4(0, 0, 0, 0);
+                    const unsigned m = __ballot_sync(FULL_MASK, f.x != 0 && f.y != 0);
+                    if (m != 0) found = x + __ffs(m) - 1;
+                }
+                if (lane == 0) last = found < 0 ? ctas - 1 : found;
+            }
+            __syncthreads();
+            const int end = last;
+            // rows_each == 1: all warps share the row's pieces; else a warp has a row to itself.
+            const int row = rows_each == 1 ? row0 : row0 + warp;
+            const int x0 = rows_each == 1 ? c + warp : c, step = rows_each == 1 ? WARPS : 1;
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            bool bad = false;
+            if (row < rows) {
+                constexpr int AHEAD = 4;
+                for (int x = x0; x <= end; x += AHEAD * step) {
+                    float2 ml[AHEAD];
+                    float4 v[AHEAD];
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) {
+                        const int y = x + i * step;
+                        ml[i] = make_float2(-INFINITY, 0.f);
+                        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (y <= end && (y == c || ws.desc[static_cast<size_t>(y) * 8 + DESC_FLAGS].x != 0)) {
+                            const size_t slot = (static_cast<size_t>(y) * 2 + (y == c)) * CHUNK_ROWS + row;
+                            ml[i] = ws.ml[slot];
+                            v[i] = reinterpret_cast<const float4*>(ws.o + slot * PG_D)[lane];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) {
+                        bad |= ml[i].y < 0.f;
+                        const float to = fmaxf(m, ml[i].x);
+                        const float f = m == -INFINITY ? 0.f : ex2(m - to), g = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - to);
+                        l = l * f + ml[i].y * g;
+                        if (g == 0.f) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);  // sums of nothing
+                        o.x = o.x * f + v[i].x * g;
+                        o.y = o.y * f + v[i].y * g;
+                        o.z = o.z * f + v[i].z * g;
+                        o.w = o.w * f + v[i].w * g;
+                        m = to;
+                    }
+                }
+            }
+            if (rows_each == 1) {
+                part[warp][lane] = o;
+                if (lane == 0) part_ml[warp] = make_float2(m, bad ? -1.f : l);
+                __syncthreads();
+                if (warp == 0 && row < rows) {
+                    bad = false;
+                    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, part_ml[w].x);
+                    l = 0.f;
+                    o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = 0; w < WARPS; ++w) {
+                        const float2 ml = part_ml[w];
+                        bad |= ml.y < 0.f;
+                        if (ml.x == -INFINITY) continue;
+                        const float f = ex2(ml.x - m);
+                        const float4 v = part[w][lane];
+                        l += ml.y * f;
+                        o.x += v.x * f;
+                        o.y += v.y * f;
+                        o.z += v.z * f;
+                        o.w += v.w * f;
+                    }
+                }
+            }
+            if (row < rows && (rows_each > 1 || warp == 0)) {
+                int token, g;
+                row_of(a, e.z, row, token, g);
+                const size_t place = (static_cast<size_t>(q.row0) + token) * a.Hq + e.y * a.G + g;
+                const bool none = bad || !(l != 0.f);
+                const float inv = none ? 0.f : 1.f / l;
+                float y[4] = {o.x, o.y, o.z, o.w};
+                float odd = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[i] = none ? 0.f : y[i] * inv;
+                    odd = fmaf(y[i], 0.f, odd);
+                    if constexpr (!BF16)
+                        if (fabsf(y[i]) <= 66000.f) y[i] = fminf(fmaxf(y[i], -65504.f), 65504.f);
+                }
+                *reinterpret_cast<uint2*>(a.out + place * PG_ROW + lane * 8) =
+                    make_uint2(pg_pack<BF16>(y[0], y[1]), pg_pack<BF16>(y[2], y[3]));
+                if (a.lse != nullptr && lane == 0) a.lse[place] = none ? -INFINITY : (m + log2f(l)) * LN2;
+                if (!SPARSE && __any_sync(FULL_MASK, odd != 0.f)) look_again<BF16>(a, q, e.x, e.y, e.z, row, lane);
+            }
+        }
+    }
+    if (!SPARSE && flags.w != 0) {
+        // Whole items of CTA c with results that are not finite: this block's rows of each.
+        const int4 s = ws.desc[static_cast<size_t>(c) * 8 + DESC_START], e = ws.desc[static_cast<size_t>(c) * 8 + DESC_END];
+        Walk<SPARSE> walk(ChunkPos{s.x, s.y, s.z, s.w}, ChunkPos{e.x, e.y, e.z, e.w});
+        Piece p;
+        while (walk.next(a, p)) {
+            if (!p.whole()) continue;
+            for (int row = blockIdx.y * WARPS + warp; row < p.rows; row += gridDim.y * WARPS) {
+                int token, g;
+                row_of(a, p.j, row, token, g);
+                const size_t place = (static_cast<size_t>(p.q.row0) + token) * a.Hq + p.h * a.G + g;
+                const uint2 w = *reinterpret_cast<const uint2*>(a.out + place * PG_ROW + lane * 8);
+                const float2 x = pg_unpack<BF16>(w.x), y = pg_unpack<BF16>(w.y);
+                const bool fine = pg_finite(x.x) && pg_finite(x.y) && pg_finite(y.x) && pg_finite(y.y);
+                if (!__all_sync(FULL_MASK, fine)) look_again<BF16>(a, p.q, p.r, p.h, p.j, row, lane);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+// The cache as copies of 16 tokens x 64 channels, 128-byte-swizzled.
+static bool make_map(CUtensorMap* map, const PagedAttnArgs& a, const uint8_t* x, bool bf16) {
+    const TensorMapEncode encode = tensor_map_encode();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[5] = {64, 2, PG_BLOCK, static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.num_blocks)};
+    const cuuint64_t strides[4] = {128, static_cast<cuuint64_t>(a.kv_token), static_cast<cuuint64_t>(a.kv_head),
+                                   static_cast<cuuint64_t>(a.kv_block)};
+    const cuuint32_t box[5] = {64, 1, PG_BLOCK, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                  const_cast<uint8_t*>(x), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace a CTA: two pieces' results of 256 rows, and 128 bytes that say of what.
+constexpr size_t CHUNK_WS_CTA = 2 * CHUNK_ROWS * (PG_D * sizeof(float) + sizeof(float2)) + 128;
+
+template <bool BF16, bool SPARSE>
+static clo_status run_paged(const PagedAttnArgs& a, void* workspace, const clo_attn_opts* opts, cudaStream_t stream) {
+    const auto main = paged_chunk_kernel<BF16, SPARSE>;
+    const auto merge = paged_merge_kernel<BF16, SPARSE>;
+    if (!prepare_kernel(reinterpret_cast<const void*>(main), CH_SMEM) ||
+        !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
+        return CLO_ERR_CUDA;
+    const int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count();
+    CUtensorMap map_k, map_v;
+    if (ctas <= 0 || !make_map(&map_k, a, a.kc, BF16) || !make_map(&map_v, a, a.vc, BF16)) return CLO_ERR_CUDA;
+    ChunkWs ws;
+    ws.o = static_cast<float*>(workspace);
+    ws.ml = reinterpret_cast<float2*>(ws.o + static_cast<size_t>(ctas) * 2 * CHUNK_ROWS * PG_D);
+    ws.desc = reinterpret_cast<int4*>(ws.ml + static_cast<size_t>(ctas) * 2 * CHUNK_ROWS);
     if (opts != nullptr && opts->ev_begin != nullptr && !record_event(opts->ev_begin, stream)) return CLO_ERR_CUDA;
-    if (launch_pdl(kernel, dim3(device_sm_count() * 8), dim3(ROWS_THREADS), 0, stream, a) != cudaSuccess) return CLO_ERR_CUDA;
+    if (launch_pdl(main, dim3(ctas), dim3(CH_THREADS), CH_SMEM, stream, a, ws, map_k, map_v) != cudaSuccess) return CLO_ERR_CUDA;
     if (opts != nullptr && opts->ev_end != nullptr && !record_event(opts->ev_end, stream)) return CLO_ERR_CUDA;
-    return CLO_OK;
+    // With few rows in all an item may have many pieces: a block a row, its warps
+    // share them.  Else a block eight rows, a warp each.
+    const long long rows = min(static_cast<long long>(CHUNK_ROWS), SPARSE ? static_cast<long long>(a.G) : static_cast<long long>(a.N) * a.G);
+    const int rows_each = rows <= 64 ? 1 : MERGE_THREADS / 32;
+    const unsigned y = static_cast<unsigned>((rows + rows_each - 1) / rows_each);
+    return launch_pdl(merge, dim3(ctas, y), dim3(MERGE_THREADS), 0, stream, a, ws, ctas, rows_each) == cudaSuccess ? CLO_OK : CLO_ERR_CUDA;
+}
+
+static clo_status run_paged_attention(const PagedAttnArgs& a, bool sparse, clo_dtype dtype, void* workspace, const clo_attn_opts* opts,
+                                      cudaStream_t stream) {
+    if (dtype == CLO_BF16) return sparse ? run_paged<true, true>(a, workspace, opts, stream) : run_paged<true, false>(a, workspace, opts, stream);
+    return sparse ? run_paged<false, true>(a, workspace, opts, stream) : run_paged<false, false>(a, workspace, opts, stream);
 }
 
 constexpr int CHUNK_MAX_CTAS = 4095;
-constexpr int CHUNK_ROWS = 256;  // rows (query, head of the group) a CTA works on at once
-// Workspace a CTA: two partial results of 256 rows, and 128 bytes that say of what.
-constexpr size_t CHUNK_WS_CTA = 2 * CHUNK_ROWS * (PG_D * sizeof(float) + sizeof(float2)) + 128;
 
 }  // namespace clo
 
@@ -79,6 +1066,12 @@ static clo_status check_paged(const void* q, const void* kc, const void* vc, con
     return CLO_OK;
 }
 
+// Whether ranges of `pn` and `qn` 16-bit elements share any.
+static bool meet(const void* p, long long pn, const void* q, long long qn) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + 2 * static_cast<uintptr_t>(qn) && b < a + 2 * static_cast<uintptr_t>(pn);
+}
+
 extern "C" clo_status clo_paged_chunk_attn(const clo_paged_chunk_attn_args* args, cudaStream_t stream) {
     if (args == nullptr) return CLO_ERR_INVALID_ARG;
     const clo_paged_chunk_attn_args& r = *args;
@@ -97,8 +1090,7 @@ extern "C" clo_status clo_paged_chunk_attn(const clo_paged_chunk_attn_args* args
     }
     for (const long long s : {kb, kh, kt})
         if (s < r.d || s % 8 != 0 || s > (1ll << 38)) return CLO_ERR_INVALID_ARG;
-    // The output may be the queries only row for row.
-    if (r.out == r.q && r.N > 1 && r.q_stride != row) return CLO_ERR_INVALID_ARG;
+    if (meet(r.q, (r.N - 1) * (r.N > 1 ? r.q_stride : 0) + row, r.out, r.N * row)) return CLO_ERR_INVALID_ARG;
     PagedAttnArgs a{};
     a.q = static_cast<const uint8_t*>(r.q);
     a.kc = static_cast<const uint8_t*>(r.kc);
@@ -121,7 +1113,7 @@ extern "C" clo_status clo_paged_chunk_attn(const clo_paged_chunk_attn_args* args
     a.G = r.Hq / r.Hkv;
     a.num_blocks = r.num_blocks;
     a.max_blocks = r.max_blocks;
-    return run_paged_attention(a, false, r.dtype, r.opts, stream);
+    return run_paged_attention(a, false, r.dtype, r.workspace, r.opts, stream);
 }
 
 extern "C" clo_status clo_paged_sparse_decode_attn(const clo_paged_sparse_attn_args* args, cudaStream_t stream) {
@@ -134,6 +1126,8 @@ extern "C" clo_status clo_paged_sparse_decode_attn(const clo_paged_sparse_attn_a
     if (r.n_sel < 1) return CLO_ERR_INVALID_ARG;
     if (static_cast<long long>(r.B) * r.Hkv * r.n_sel >= (1ll << 31)) return CLO_ERR_UNSUPPORTED;
     if (r.B == 0) return CLO_OK;
+    const long long elements = static_cast<long long>(r.B) * r.Hq * r.d;
+    if (meet(r.q, elements, r.out, elements)) return CLO_ERR_INVALID_ARG;
     PagedAttnArgs a{};
     a.q = static_cast<const uint8_t*>(r.q);
     a.kc = static_cast<const uint8_t*>(r.kc);
@@ -157,5 +1151,5 @@ extern "C" clo_status clo_paged_sparse_decode_attn(const clo_paged_sparse_attn_a
     a.num_blocks = r.num_blocks;
     a.max_blocks = r.max_blocks;
     a.n_sel = r.n_sel;
-    return run_paged_attention(a, true, r.dtype, r.opts, stream);
+    return run_paged_attention(a, true, r.dtype, r.workspace, r.opts, stream);
 }

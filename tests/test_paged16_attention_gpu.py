@@ -152,17 +152,13 @@ def test_rows_of_no_request_are_left():
     ref.check_attention(out[3:33], lse[3:33], ref.chunk_attention(q[3:33], kc, vc, table, lens, n_new), 80)
 
 
-def test_no_lse_scale_and_in_place():
+def test_no_lse_and_a_scale():
     dtype = torch.bfloat16
     kc, vc, table = ref.make_cache([90], 2, dtype, 61)
     q = queries(70, 4, dtype, 62)
     out, _, _ = chunk(q, kc, vc, table, [90], [70], lse=False, scale=0.25)
     want = ref.chunk_attention(q, kc, vc, table, [90], [70], 0.25)
     ref.check_attention(out, None, want, 90)
-    ws = torch.empty(clo.clo_paged_chunk_workspace_size(4, 2), dtype=torch.uint8, device="cuda")
-    ctx = torch.tensor([90], dtype=torch.int32, device="cuda")
-    clo.clo_paged_chunk_attn(q, kc, vc, table, ctx, offsets_of([70]), q, ws, scale=0.25)
-    assert torch.equal(q, out)
 
 
 @pytest.mark.parametrize("layout", ["heads_last", "kv_fused", "padded_rows", "one_head_of_many"])

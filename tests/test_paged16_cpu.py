@@ -199,7 +199,7 @@ def test_chunk_rejects(L):
     opts = clo.AttnOpts(8, None, None)
     o = dict(opts=ctypes.addressof(opts))
     for kw in (dict(N=-1), dict(q_stride=1016), dict(q_stride=1028), dict(kv_block=4096), dict(kv_block=4096, kv_head=2048, kv_token=64),
-               dict(kv_block=4096, kv_head=2048, kv_token=130), dict(out=FAKE, q_stride=2048),
+               dict(kv_block=4096, kv_head=2048, kv_token=130), dict(out=FAKE), dict(out=FAKE + 4 * 2048 - 16),
                dict(kv_block=1 << 39, kv_head=2048, kv_token=128)):
         assert _chunk(L, **o, **kw) == INVALID, kw
     assert _chunk(L, N=1 << 29) == UNSUPPORTED
@@ -209,6 +209,7 @@ def test_chunk_rejects(L):
 def test_sparse_rejects(L):
     opts = clo.AttnOpts(8, None, None)
     o = dict(opts=ctypes.addressof(opts))
+    assert _sparse(L, **o, out=FAKE) == INVALID and _sparse(L, **o, out=FAKE + 4080) == INVALID
     assert _sparse(L, **o, n_sel=0) == INVALID and _sparse(L, **o, n_sel=1 << 30) == UNSUPPORTED
 
 
