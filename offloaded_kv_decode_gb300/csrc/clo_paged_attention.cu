@@ -2,8 +2,8 @@
 // paged cache, and decode attention over selected blocks of it.
 //
 // Work.  A request's rows of one KV head (its new tokens times the G heads of the
-// group) are cut into items of 256 rows, two tiles of 128.  An item goes over the
-// tokens that its last row sees, 128 at a time.  All items of a call, weighed by
+// group) are cut into tiles of as many whole tokens as fit 128 rows, and two tiles are
+// an item.  An item goes over the tokens that its last row sees, 128 at a time.  All items of a call, weighed by
 // their tokens, are shared out evenly, one contiguous range a CTA and one CTA an
 // SM; each CTA works its range out by itself from the lengths.  An item that a
 // border cuts leaves a partial result for each piece (sums, reference, denominator), which
@@ -11,16 +11,15 @@
 // long prompt costs each SM the same.
 //
 // A CTA has two streams, each a warpgroup with its own scores and sums in tensor memory (4
-// x 128 columns: all of it).  An item of more than 128 rows gives a tile of rows to
-// each stream, and both go over every tile of tokens, so the tensor cores work on
-// one stream's products while the other's weights are made.  An item of up to 128
-// rows gives the streams alternate tiles of tokens, and their sums are added up at its
-// end.  A row belongs to one thread: no shuffles.  Besides:
+// x 128 columns: all of it).  An item of two tiles of rows gives one to each stream,
+// and both go over every tile of tokens, so the tensor cores work on one stream's
+// products while the other's weights are made.  An item of one tile gives the
+// streams alternate tiles of tokens, and their sums are added up at its end.  A row belongs to one thread: no shuffles.  Besides:
 //   warp 8   brings K and V tiles into a ring of five (16 tokens a copy, whatever the
 //            cache's strides), in the order in which the products take them;
 //   warp 9   issues the products: S = Q K^T, both from shared memory, and O += P V with
 //            P from tensor memory, where it takes the place of S;
-//   warps 10, 11 bring the rows of q.
+//   warp 10  brings the rows of q.
 // Softmax: with a reference that lies 2^6 below a maximum seen so far and moves only when
 // a score passes it by 2^14, weights up to 2^14 fit fp16 and those down to 2^-31 of
 // the largest still count, and sums in tensor memory are seldom rescaled.
@@ -46,7 +45,7 @@ constexpr int CH_PLACES = CH_TILE / PG_BLOCK;     // blocks of a tile
 constexpr int CH_HALF = CH_TILE * 128;            // bytes of 64 channels of a tile
 constexpr int CH_TILE_BYTES = 2 * CH_HALF;
 constexpr int CH_STAGES = 5;
-constexpr int CHUNK_ROWS = 2 * CH_TILE;           // rows of an item
+constexpr int CHUNK_ROWS = 2 * CH_TILE;           // rows of an item, at most
 constexpr int CH_THREADS = 384;
 constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
 constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
@@ -64,7 +63,7 @@ struct ChunkPos {
 };
 
 struct ChunkWs {
-    float* o;     // [CTA][head piece, tail piece][256 rows][128]
+    float4* o;    // [CTA][head piece, tail piece][32][256 rows]: 4 channels of each row together
     float2* ml;   // [CTA][2][256] reference and denominator; denominator -1: bad data
     int4* desc;   // [CTA][8]: see CH_DESC
 };
@@ -83,41 +82,40 @@ static_assert(sizeof(ChunkSmall) <= CH_SMALL, "");
 
 // ---------------------------------------------------------------- shares
 
+// Tokens of a tile of rows.
+__host__ __device__ __forceinline__ int tile_tokens(int G) { return CH_TILE / G; }
+
 // Tokens that the last row of item j sees (sparse: the selected places' length).
 template <bool SPARSE>
 __device__ __forceinline__ int item_sees(const PagedAttnArgs& a, const PagedReq& q, int j) {
-    if constexpr (SPARSE) {
-        return paged_places<true>(a, q.ctx) * PG_BLOCK;
-    } else {
-        const unsigned upto = (static_cast<unsigned>(j + 1) * CHUNK_ROWS + a.G - 1) / static_cast<unsigned>(a.G);
-        return max(q.ctx - q.n + static_cast<int>(min(static_cast<unsigned>(q.n), upto)), 0);
-    }
+    if constexpr (SPARSE) return paged_places<true>(a, q.ctx) * PG_BLOCK;
+    else return max(q.ctx - q.n + static_cast<int>(min(static_cast<unsigned>(q.n), 2u * (j + 1) * a.tt)), 0);
 }
 __device__ __forceinline__ int items_of(const PagedAttnArgs& a, const PagedReq& q) {
-    return static_cast<int>((static_cast<long long>(q.n) * a.G + CHUNK_ROWS - 1) / CHUNK_ROWS);
+    return static_cast<int>((static_cast<unsigned>(q.n) + 2 * a.tt - 1) / (2 * a.tt));
 }
 
-// The weights of a request's items of one KV head, in units of 1 / G token: item j
-// weighs G (tokens before the new ones + CH_FIXED) + 256 (j + 1), the last one
-// by the request's length.
+// The weights of a request's items of one KV head, in tokens: item j weighs the
+// tokens before the new ones, CH_FIXED and the new ones up to its end.
 struct Weights {
     long long each, last;  // each = without the part that rises
-    int items;
+    int items, tt;
     __device__ long long before(int j) const {  // items 0 .. j - 1
-        return j < items ? j * each + (CHUNK_ROWS / 2) * static_cast<long long>(j) * (j + 1) : all();
+        return j < items ? j * each + static_cast<long long>(j) * (j + 1) * tt : all();
     }
     __device__ long long all() const {
         const long long m = items - 1;
-        return items == 0 ? 0 : m * each + (CHUNK_ROWS / 2) * m * (m + 1) + last;
+        return items == 0 ? 0 : m * each + m * (m + 1) * tt + last;
     }
 };
 template <bool SPARSE>
 __device__ __forceinline__ Weights weights_of(const PagedAttnArgs& a, const PagedReq& q) {
     Weights w;
+    w.tt = a.tt;
     w.items = items_of(a, q);
-    const long long G = a.G, base = SPARSE ? 0 : max(q.ctx - q.n, 0);
-    w.each = G * (base + CH_FIXED);
-    w.last = G * ((SPARSE ? item_sees<true>(a, q, 0) : base + q.n) + CH_FIXED);
+    const long long base = SPARSE ? 0 : max(q.ctx - q.n, 0);
+    w.each = base + CH_FIXED;
+    w.last = (SPARSE ? item_sees<true>(a, q, 0) : base + q.n) + CH_FIXED;
     return w;
 }
 
@@ -153,9 +151,10 @@ __device__ ChunkPos locate(const PagedAttnArgs& a, const long long* prefix, long
 struct Piece {
     PagedReq q;
     int r, h, j, lo, hi, tiles;
-    int rows;  // of the item
-    int sees;  // tokens of the item's last row
+    int tokens;  // of the item
+    int sees;    // tokens of the item's last row
     __device__ bool whole() const { return lo == 0 && hi == tiles; }
+    __device__ bool two(const PagedAttnArgs& a) const { return tokens > a.tt; }
 };
 
 // The pieces from `start` to `end`, in order.
@@ -188,8 +187,7 @@ struct Walk {
         p.j = at.j;
         p.sees = item_sees<SPARSE>(a, q, at.j);
         p.tiles = (p.sees + CH_TILE - 1) / CH_TILE;
-        p.rows = static_cast<int>(min(static_cast<long long>(CHUNK_ROWS),
-                                      static_cast<long long>(q.n) * a.G - static_cast<long long>(at.j) * CHUNK_ROWS));
+        p.tokens = min(2 * a.tt, q.n - at.j * 2 * a.tt);
         p.lo = at.cut;
         p.hi = at_end ? min(end.cut, p.tiles) : p.tiles;
         at.cut = 0;
@@ -201,11 +199,14 @@ struct Walk {
     }
 };
 
-// Row (of the item) -> its token among the request's new ones and its head in the group.
-__device__ __forceinline__ void row_of(const PagedAttnArgs& a, int j, int row, int& token, int& g) {
-    const unsigned x = static_cast<unsigned>(j) * CHUNK_ROWS + row;
-    token = x / static_cast<unsigned>(a.G);
-    g = x - token * a.G;
+// Row (tile of rows * 128 + row of the tile) of item j: its token among the
+// request's new ones and its head in the group; whether there is such a row.
+__device__ __forceinline__ bool row_of(const PagedAttnArgs& a, int j, int tokens, int row, int& token, int& g) {
+    const int x = row & (CH_TILE - 1), t = x / a.G;
+    const int i = (row >> 7) * a.tt + t;
+    g = x - t * a.G;
+    token = 2 * j * a.tt + i;
+    return t < a.tt && i < tokens;
 }
 
 // ---------------------------------------------------------------- small parts
@@ -291,7 +292,7 @@ struct Loader {
     }
 
     __device__ bool piece(const Piece& p, int slot) {
-        const int n = p.hi - p.lo, ahead = p.rows > CH_TILE ? 1 : 2;
+        const int n = p.hi - p.lo, ahead = p.two(a) ? 1 : 2;
         const int sees = SPARSE ? p.q.ctx : p.sees, last = paged_places<SPARSE>(a, sees);
         const auto fetch = [&](int group) {
             const int x = group * 32 + lane;
@@ -324,8 +325,9 @@ template <bool BF16>
 struct Issuer {
     ChunkSmall* sm;
     uint32_t q, ring, tmem;
+    int tt;
     int it = 0;              // tiles taken so far
-    uint32_t p_count[2] = {0, 0};
+    uint32_t p_count0 = 0, p_count1 = 0;
     uint32_t q_count = 0;
 
     __device__ bool wait(unsigned long long& bar, uint32_t parity) { return ch_wait(bar, parity, sm); }
@@ -334,24 +336,27 @@ struct Issuer {
     __device__ void release(int x) { tc_commit(smem_u32(&sm->empty[x % CH_STAGES])); }
     // S of stream s = Q of row tile qt times K of tile x.
     __device__ void scores(int s, int qt, int x) {
-        const uint32_t k = ring + (x % CH_STAGES) * CH_TILE_BYTES, qa = q + qt * CH_TILE_BYTES;
+        const uint64_t k = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, 16), qa = tc_tile(q + qt * CH_TILE_BYTES, 16);
+        const uint32_t d = tmem + s * CH_TILE;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t off = (i >> 2) * CH_HALF + (i & 3) * 32;
-            tc_mma(tmem + s * CH_TILE, tc_tile(qa + off, 16), tc_tile(k + off, 16), tc_shape(BF16, CH_TILE, CH_TILE, false), i > 0);
+            const uint32_t off = ((i >> 2) * CH_HALF + (i & 3) * 32) >> 4;
+            tc_mma(d, tc_ahead(qa, off), tc_ahead(k, off), tc_shape(BF16, CH_TILE, CH_TILE, false), i > 0);
         }
         tc_commit(smem_u32(&sm->s_full[s]));
     }
     // O of stream s (+)= its weights times V of tile x.
     __device__ void sums(int s, int x, bool add) {
-        const uint32_t v = ring + (x % CH_STAGES) * CH_TILE_BYTES;
+        const uint64_t v = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, CH_HALF);
+        const uint32_t d = tmem + (2 + s) * CH_TILE, w = tmem + s * CH_TILE;
+        tc_mma_ts(d, w, v, tc_shape(BF16, CH_TILE, CH_TILE, true), add);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            tc_mma_ts(tmem + (2 + s) * CH_TILE, tmem + s * CH_TILE + 8 * i, tc_tile(v + i * 2048, CH_HALF),
-                      tc_shape(BF16, CH_TILE, CH_TILE, true), add || i > 0);
+        for (int i = 1; i < 8; ++i)
+            tc_mma_ts(d, w + 8 * i, tc_ahead(v, i * 2048 >> 4), tc_shape(BF16, CH_TILE, CH_TILE, true), true);
     }
     __device__ bool weights(int s) {
-        if (!wait(sm->p_ready[s], p_count[s]++ & 1)) return false;
+        const uint32_t count = s == 0 ? p_count0++ : p_count1++;
+        if (!wait(sm->p_ready[s], count & 1)) return false;
         tc_fence_after();
         return true;
     }
@@ -360,7 +365,7 @@ struct Issuer {
         const int n = p.hi - p.lo;
         if (!wait(sm->q_full, q_count++ & 1)) return false;
         tc_fence_after();
-        if (p.rows > CH_TILE) {
+        if (p.tokens > tt) {
             int k = take();
             if (!here(k)) return false;
             scores(0, 0, k);
@@ -416,25 +421,6 @@ struct Issuer {
     }
 };
 
-// ---------------------------------------------------------------- the warps that bring q
-
-template <bool SPARSE>
-__device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Piece& p, uint32_t q, int thread) {
-    const int tiles = p.rows > CH_TILE ? 2 : 1, c = thread & 15;
-    for (int row = thread >> 4; row < tiles * CH_TILE; row += 4) {
-        const uint32_t to = q + (row >> 7) * CH_TILE_BYTES + (c >> 3) * CH_HALF + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
-        int token, g;
-        row_of(a, p.j, row, token, g);
-        const bool there = row < p.rows;
-        const uint8_t* src = a.q;
-        if (there) src += (p.q.row0 + token) * a.q_stride + (p.h * a.G + g) * PG_ROW + c * 16;
-        cp_async_16(to, src, there ? 16 : 0);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    async_proxy_fence();
-}
-
 // ---------------------------------------------------------------- the softmax warpgroups
 
 template <bool BF16, bool SPARSE>
@@ -445,7 +431,7 @@ struct RowSoftmax {
     int s;            // stream
     int tid;          // thread of the warpgroup: the row of its tile
     uint32_t tmem;    // this warp's lanes of column 0
-    uint32_t s_count = 0, o_count[2] = {0, 0}, x_count = 0, e_count = 0;
+    uint32_t s_count = 0, o_count0 = 0, o_count1 = 0, x_count = 0, e_count = 0;
     int piece_count = 0;
 
     // The weights of one tile of tokens from their scores.  sees: tokens of the
@@ -544,12 +530,11 @@ struct RowSoftmax {
     // Writes a row's result: out and lse of a whole item, else its piece's sums.
     template <typename Load>
     __device__ __forceinline__ void write(const Piece& p, int row, bool bad, float ref, float sum, Load load) {
-        const bool valid = row < p.rows;
         int token, g;
-        row_of(a, p.j, row, token, g);
+        const bool valid = row_of(a, p.j, p.tokens, row, token, g);
         const size_t place = (static_cast<size_t>(p.q.row0) + token) * a.Hq + p.h * a.G + g;
         const bool whole = p.whole();
-        const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (p.lo == 0)) * CHUNK_ROWS + row;
+        const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + (p.lo == 0);
         const bool none = bad || !(sum != 0.f);  // (a NaN is something)
         const float inv = none ? 0.f : 1.f / sum;
         float odd = 0.f;  // turns NaN with a value that is not finite
@@ -558,24 +543,32 @@ struct RowSoftmax {
             float o[32];
             load(o, c);
             if (whole) {
-                uint4* dst = reinterpret_cast<uint4*>(a.out + place * PG_ROW + c * 64);
+                uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    o[i] = none ? 0.f : o[i] * inv;
-                    odd = fmaf(o[i], 0.f, odd);
-                    if constexpr (!BF16)  // rounded weights may pass the largest V by a little
-                        if (fabsf(o[i]) <= 66000.f) o[i] = fminf(fmaxf(o[i], -65504.f), 65504.f);
+                for (int i = 0; i < 16; ++i) {
+                    const float x = none ? 0.f : o[2 * i] * inv, y = none ? 0.f : o[2 * i + 1] * inv;
+                    odd = fmaf(x, 0.f, odd);
+                    odd = fmaf(y, 0.f, odd);
+                    w[i] = pg_pack_out<BF16>(x, y);
                 }
-                if (valid) {
+                if (valid) {  // whole sectors: a thread's row lies apart from its neighbours'
+                    uint8_t* dst = a.out + place * PG_ROW + c * 64;
+                    const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pg_pack<BF16>(o[8 * i], o[8 * i + 1]), pg_pack<BF16>(o[8 * i + 2], o[8 * i + 3]),
-                                            pg_pack<BF16>(o[8 * i + 4], o[8 * i + 5]), pg_pack<BF16>(o[8 * i + 6], o[8 * i + 7]));
+                    for (int i = 0; i < 2; ++i)
+                        if (!sectors) {
+                            reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]);
+                            reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+                        } else
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 32 * i), "r"(w[8 * i]),
+                                     "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                                     "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                                     : "memory");
                 }
             } else if (valid) {
-                float4* dst = reinterpret_cast<float4*>(ws.o + slot * PG_D + c * 32);
+                float4* dst = ws.o + (slot * 32 + c * 8) * CHUNK_ROWS + row;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 8; ++i) dst[i * CHUNK_ROWS] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         }
         if (!valid) return;
@@ -583,13 +576,13 @@ struct RowSoftmax {
             if (a.lse != nullptr) a.lse[place] = none ? -INFINITY : (ref + log2f(sum)) * LN2;
             if (!SPARSE && odd != 0.f) *reinterpret_cast<volatile int*>(&sm->again) = 1;
         } else {
-            ws.ml[slot] = make_float2(ref, bad ? -1.f : sum);
+            ws.ml[slot * CHUNK_ROWS + row] = make_float2(ref, bad ? -1.f : sum);
         }
     }
 
     __device__ bool piece(const Piece& p) {
         const int n = p.hi - p.lo;
-        const bool two = p.rows > CH_TILE;
+        const bool two = p.two(a);
         const int row = two ? s * CH_TILE + tid : tid;
         if (n == 0) {  // no row of the item sees a token
             if (two || s == 0) write(p, row, false, -INFINITY, 0.f, [](float (&o)[32], int) {
@@ -600,9 +593,9 @@ struct RowSoftmax {
         }
         const int lane = tid & 31;
         int token, g;
-        row_of(a, p.j, row, token, g);
+        const bool valid = row_of(a, p.j, p.tokens, row, token, g);
         // Rows past the item's (their results are not used) see everything.
-        const int sees = SPARSE || row >= p.rows ? 0x7fffffff : paged_sees<false>(p.q, token);
+        const int sees = SPARSE || !valid ? 0x7fffffff : paged_sees<false>(p.q, token);
         const int places = SPARSE ? paged_places<true>(a, p.q.ctx) : 0;
         const auto place_rows = [&](int t) {  // sparse: lanes 0 .. 7, the tokens of each place
             const int x = t * CH_PLACES + (lane & 7);
@@ -622,11 +615,11 @@ struct RowSoftmax {
         }
         const bool second = two || n > 1;  // stream 1 had tiles
         if (s == 0 || two) {
-            if (!ch_warp_wait(sm->o_full[s], o_count[s] & 1, sm)) return false;
-            if (s == 0 && !two && second && !ch_warp_wait(sm->o_full[1], o_count[1] & 1, sm)) return false;
+            if (!ch_warp_wait(sm->o_full[s], (s == 0 ? o_count0 : o_count1) & 1, sm)) return false;
+            if (s == 0 && !two && second && !ch_warp_wait(sm->o_full[1], o_count1 & 1, sm)) return false;
         }
-        ++o_count[0];
-        if (second) ++o_count[1];
+        ++o_count0;
+        if (second) ++o_count1;
         const bool bad = *reinterpret_cast<volatile int*>(&sm->bad[piece_count & 7]) != 0;
         ++piece_count;
         tc_fence_after();
@@ -673,8 +666,8 @@ struct RowSoftmax {
 
 template <bool BF16, bool SPARSE>
 __global__ void __launch_bounds__(CH_THREADS, 1)
-    paged_chunk_kernel(const PagedAttnArgs a, const ChunkWs ws, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v) {
+    paged_chunk_kernel(const PagedAttnArgs a, const ChunkWs ws, const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint8_t* ring = base + CHUNK_ROWS * PG_ROW;
@@ -686,7 +679,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             mbar_init_n(smem_u32(&sm->full[i]), 1);
             mbar_init_n(smem_u32(&sm->empty[i]), 1);
         }
-        mbar_init_n(smem_u32(&sm->q_full), 64);
+        mbar_init_n(smem_u32(&sm->q_full), 1);
         mbar_init_n(smem_u32(&sm->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init_n(smem_u32(&sm->s_full[i]), 1);
@@ -700,6 +693,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 9) tmem_alloc(smem_u32(&sm->tmem), 4 * CH_TILE);
+    if (threadIdx.x == 320) {
+        tma_prefetch(&map_q);
+        tma_prefetch(&map_k);
+        tma_prefetch(&map_v);
+    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -725,19 +723,22 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
         for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-        sum -= local;
         if (threadIdx.x == 0) prefix[0] = 0;
-        for (int r = r0; r < r1; ++r) {
-            sum += weights_of<SPARSE>(a, paged_request<SPARSE>(a, r)).all() * a.Hkv;
-            prefix[r + 1] = sum;
+        if (per == 1) {
+            if (r0 < r1) prefix[r1] = sum;
+        } else {
+            sum -= local;
+            for (int r = r0; r < r1; ++r) {
+                sum += weights_of<SPARSE>(a, paged_request<SPARSE>(a, r)).all() * a.Hkv;
+                prefix[r + 1] = sum;
+            }
         }
         __syncthreads();
     }
     const int cta = blockIdx.x;
     if (lane == 0 && warp < 2) {
         const long long all = prefix[a.B];
-        const long long least = static_cast<long long>(a.G) * (CH_LEAST + CH_FIXED);
-        const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), all / least));
+        const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), all / (CH_LEAST + CH_FIXED)));
         const long long c = min(static_cast<long long>(cta) + warp, ctas);
         (warp == 0 ? sm->start : sm->end) = locate<SPARSE>(a, prefix, all / ctas * c + all % ctas * c / ctas);
     }
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     mbar_wait(smem_u32(&sm->full[x % CH_STAGES]), x / CH_STAGES & 1);
         } else if (warp == 9) {
             if (lane == 0) {
-                Issuer<BF16> w{sm, smem_u32(base), smem_u32(ring), tmem};
+                Issuer<BF16> w{sm, smem_u32(base), smem_u32(ring), tmem, a.tt};
                 bool ok = true;
                 while (ok && walk.next(a, p))
                     if (p.hi > p.lo) ok = w.piece(p);
@@ -795,14 +796,23 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 }
             }
             __syncwarp();
-        } else {
+        } else if (warp == 10 && lane == 0) {
             uint32_t count = 0;
-            while (walk.next(a, p)) {
+            bool ok = true;
+            while (ok && walk.next(a, p)) {
                 if (p.hi == p.lo) continue;
-                if (!ch_warp_wait(sm->q_empty, (count++ & 1) ^ 1, sm)) break;
-                bring_queries<SPARSE>(a, p, smem_u32(base), static_cast<int>(threadIdx.x) - 320);
-                mbar_arrive(smem_u32(&sm->q_full));
+                ok = ch_wait(sm->q_empty, (count & 1) ^ 1, sm);
+                if (!ok) break;
+                ++count;
+                // Rows of tokens behind the request's are others'; they make rows that nobody uses.
+                const int tiles = p.two(a) ? 2 : 1, bytes = a.tt * a.G * PG_ROW;
+                mbar_expect(smem_u32(&sm->q_full), tiles * bytes);
+                for (int t = 0; t < tiles; ++t)
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_4d(smem_u32(base) + t * CH_TILE_BYTES + half * CH_HALF, &map_q, smem_u32(&sm->q_full), 0, half,
+                                    p.h * a.G, p.q.row0 + (2 * p.j + t) * a.tt);
             }
+            if (!ok && count > 0) mbar_wait(smem_u32(&sm->q_full), (count - 1) & 1);
         }
     }
     tc_fence_before();
@@ -834,36 +844,38 @@ __device__ bool hidden_odd(const PagedAttnArgs& a, int r, int h, int from, int t
     return __any_sync(FULL_MASK, odd);
 }
 
-// Makes a row whose result is not finite anew if that may come from what it does not see.
+// Makes a row whose result is not finite anew if that may come from what it does not
+// see.  `mine`: this lane's channels are written.
 template <bool BF16>
-__device__ __noinline__ void look_again(const PagedAttnArgs& a, const PagedReq& q, int r, int h, int j, int row, int lane) {
-    int token, g;
-    row_of(a, j, row, token, g);
+__device__ __noinline__ void look_again(const PagedAttnArgs& a, const PagedReq& q, int r, int h, int j, int token, int g, int lane,
+                                        bool mine) {
     if (hidden_odd<BF16>(a, r, h, paged_sees<false>(q, token), item_sees<false>(a, q, j), lane))
-        paged_row<BF16, false>(a, r, q, token, h * a.G + g, lane);
+        paged_row<BF16, false>(a, r, q, token, h * a.G + g, lane, mine);
 }
 
-template <bool BF16, bool SPARSE>
-__global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedAttnArgs a, const ChunkWs ws, int ctas, int rows_each) {
-    __shared__ int last;
-    __shared__ float4 part[MERGE_THREADS / 32][32];
-    __shared__ float2 part_ml[MERGE_THREADS / 32];
+// Block (c, y) joins the pieces of the item that starts in CTA c's share and ends in a
+// later one's, for ROWS of its rows and 4 * NI of the channels.  Lanes are rows, and with ROWS
+// = 8 four subsets of the pieces; a warp holds 4 channels of its rows, NI / 8 times.
+template <bool BF16, bool SPARSE, int ROWS, int NI>
+__global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedAttnArgs a, const ChunkWs ws, int ctas) {
+    constexpr int SUBS = 32 / ROWS, K = NI / 8, AHEAD = 8 / K;
+    __shared__ int last, odd_row[ROWS];
+    __shared__ uint2 result[ROWS][NI + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int WARPS = MERGE_THREADS / 32;
     pdl_launch_dependents();
     pdl_wait();
     const int c = blockIdx.x;
     const int4 flags = ws.desc[static_cast<size_t>(c) * 8 + DESC_FLAGS];
-    const int row0 = blockIdx.y * rows_each;
     if (flags.z != 0) {
-        // The item that starts in CTA c and ends in a later one: its pieces are c's tail
-        // and the head pieces of the CTAs up to `last` (one with no share has none).
-        const int4 e = ws.desc[static_cast<size_t>(c) * 8 + DESC_END];
+        const int4 e = ws.desc[static_cast<size_t>(c) * 8 + DESC_END];  // (the item ends behind c's share)
         const PagedReq q = paged_request<SPARSE>(a, e.x);
-        const int rows = static_cast<int>(min(static_cast<long long>(CHUNK_ROWS),
-                                              static_cast<long long>(q.n) * a.G - static_cast<long long>(e.z) * CHUNK_ROWS));
-        if (row0 < rows) {
+        const int tokens = min(2 * a.tt, q.n - e.z * 2 * a.tt);
+        const int ib = blockIdx.y % (32 / NI), row0 = blockIdx.y / (32 / NI) * ROWS;
+        int token, g;
+        if (row_of(a, e.z, tokens, row0, token, g)) {  // else no row of the block is one
             if (warp == 0) {
+                // Its pieces are c's tail and the head pieces of the CTAs up to `last` (one
+                // with no share has none).
                 int found = -1;
                 for (int x = c + 1; found < 0 && x < ctas; x += 32) {
                     const int4 f = x + lane < ctas ? ws.desc[static_cast<size_t>(x + lane) * 8 + DESC_FLAGS] : make_int4(0, 0, 0, 0);
@@ -872,87 +884,91 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
                 }
                 if (lane == 0) last = found < 0 ? ctas - 1 : found;
             }
+            if (static_cast<int>(threadIdx.x) < ROWS) odd_row[threadIdx.x] = 0;
             __syncthreads();
-            const int end = last;
-            // rows_each == 1: all warps share the row's pieces; else a warp has a row to itself.
-            const int row = rows_each == 1 ? row0 : row0 + warp;
-            const int x0 = rows_each == 1 ? c + warp : c, step = rows_each == 1 ? WARPS : 1;
+            const int end = last, row = row0 + lane % ROWS;
+            const bool valid = row_of(a, e.z, tokens, row, token, g);
             float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 o[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             bool bad = false;
-            if (row < rows) {
-                constexpr int AHEAD = 4;
-                for (int x = x0; x <= end; x += AHEAD * step) {
-                    float2 ml[AHEAD];
-                    float4 v[AHEAD];
+            for (int x = c + lane / ROWS; x <= end; x += AHEAD * SUBS) {
+                float2 ml[AHEAD];
+                float4 v[AHEAD][K];
+                bool there[AHEAD];
 #pragma unroll
-                    for (int i = 0; i < AHEAD; ++i) {
-                        const int y = x + i * step;
-                        ml[i] = make_float2(-INFINITY, 0.f);
-                        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (y <= end && (y == c || ws.desc[static_cast<size_t>(y) * 8 + DESC_FLAGS].x != 0)) {
-                            const size_t slot = (static_cast<size_t>(y) * 2 + (y == c)) * CHUNK_ROWS + row;
-                            ml[i] = ws.ml[slot];
-                            v[i] = reinterpret_cast<const float4*>(ws.o + slot * PG_D)[lane];
-                        }
-                    }
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int y = min(x + i * SUBS, end);
+                    there[i] = valid && x + i * SUBS <= end && (y == c || ws.desc[static_cast<size_t>(y) * 8 + DESC_FLAGS].x != 0);
+                    const size_t slot = static_cast<size_t>(y) * 2 + (y == c);
+                    ml[i] = ws.ml[slot * CHUNK_ROWS + row];
 #pragma unroll
-                    for (int i = 0; i < AHEAD; ++i) {
-                        bad |= ml[i].y < 0.f;
-                        const float to = fmaxf(m, ml[i].x);
-                        const float f = m == -INFINITY ? 0.f : ex2(m - to), g = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - to);
-                        l = l * f + ml[i].y * g;
-                        if (g == 0.f) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);  // sums of nothing
-                        o.x = o.x * f + v[i].x * g;
-                        o.y = o.y * f + v[i].y * g;
-                        o.z = o.z * f + v[i].z * g;
-                        o.w = o.w * f + v[i].w * g;
-                        m = to;
+                    for (int k = 0; k < K; ++k) v[i][k] = ws.o[(slot * 32 + ib * NI + warp + 8 * k) * CHUNK_ROWS + row];
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (!there[i]) continue;
+                    bad |= ml[i].y < 0.f;
+                    if (ml[i].x == -INFINITY) continue;  // sums of nothing
+                    const float to = fmaxf(m, ml[i].x);
+                    const float f = m == -INFINITY ? 0.f : ex2(m - to), w = ex2(ml[i].x - to);
+                    l = l * f + ml[i].y * w;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        o[k].x = o[k].x * f + v[i][k].x * w;
+                        o[k].y = o[k].y * f + v[i][k].y * w;
+                        o[k].z = o[k].z * f + v[i][k].z * w;
+                        o[k].w = o[k].w * f + v[i][k].w * w;
                     }
+                    m = to;
                 }
             }
-            if (rows_each == 1) {
-                part[warp][lane] = o;
-                if (lane == 0) part_ml[warp] = make_float2(m, bad ? -1.f : l);
-                __syncthreads();
-                if (warp == 0 && row < rows) {
-                    bad = false;
-                    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, part_ml[w].x);
-                    l = 0.f;
-                    o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int w = 0; w < WARPS; ++w) {
-                        const float2 ml = part_ml[w];
-                        bad |= ml.y < 0.f;
-                        if (ml.x == -INFINITY) continue;
-                        const float f = ex2(ml.x - m);
-                        const float4 v = part[w][lane];
-                        l += ml.y * f;
-                        o.x += v.x * f;
-                        o.y += v.y * f;
-                        o.z += v.z * f;
-                        o.w += v.w * f;
-                    }
+#pragma unroll
+            for (int off = ROWS; off < 32; off <<= 1) {
+                const float m2 = __shfl_xor_sync(FULL_MASK, m, off), l2 = __shfl_xor_sync(FULL_MASK, l, off);
+                bad |= __shfl_xor_sync(FULL_MASK, static_cast<int>(bad), off) != 0;
+                const float to = fmaxf(m, m2);
+                const float f = m == -INFINITY ? 0.f : ex2(m - to), w = m2 == -INFINITY ? 0.f : ex2(m2 - to);
+                l = l * f + l2 * w;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    o[k].x = o[k].x * f + __shfl_xor_sync(FULL_MASK, o[k].x, off) * w;
+                    o[k].y = o[k].y * f + __shfl_xor_sync(FULL_MASK, o[k].y, off) * w;
+                    o[k].z = o[k].z * f + __shfl_xor_sync(FULL_MASK, o[k].z, off) * w;
+                    o[k].w = o[k].w * f + __shfl_xor_sync(FULL_MASK, o[k].w, off) * w;
                 }
+                m = to;
             }
-            if (row < rows && (rows_each > 1 || warp == 0)) {
-                int token, g;
-                row_of(a, e.z, row, token, g);
-                const size_t place = (static_cast<size_t>(q.row0) + token) * a.Hq + e.y * a.G + g;
-                const bool none = bad || !(l != 0.f);
-                const float inv = none ? 0.f : 1.f / l;
-                float y[4] = {o.x, o.y, o.z, o.w};
+            const bool none = bad || !(l != 0.f);
+            const float inv = none ? 0.f : 1.f / l;
+            const auto place_of = [&](int t, int gg) { return (static_cast<size_t>(q.row0) + t) * a.Hq + e.y * a.G + gg; };
+            if (lane < ROWS) {
                 float odd = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[i] = none ? 0.f : y[i] * inv;
-                    odd = fmaf(y[i], 0.f, odd);
-                    if constexpr (!BF16)
-                        if (fabsf(y[i]) <= 66000.f) y[i] = fminf(fmaxf(y[i], -65504.f), 65504.f);
+                for (int k = 0; k < K; ++k) {
+                    const float y[4] = {none ? 0.f : o[k].x * inv, none ? 0.f : o[k].y * inv, none ? 0.f : o[k].z * inv,
+                                        none ? 0.f : o[k].w * inv};
+                    odd += (y[0] + y[1] + y[2] + y[3]) * 0.f;
+                    result[lane][warp + 8 * k] = make_uint2(pg_pack_out<BF16>(y[0], y[1]), pg_pack_out<BF16>(y[2], y[3]));
                 }
-                *reinterpret_cast<uint2*>(a.out + place * PG_ROW + lane * 8) =
-                    make_uint2(pg_pack<BF16>(y[0], y[1]), pg_pack<BF16>(y[2], y[3]));
-                if (a.lse != nullptr && lane == 0) a.lse[place] = none ? -INFINITY : (m + log2f(l)) * LN2;
-                if (!SPARSE && __any_sync(FULL_MASK, odd != 0.f)) look_again<BF16>(a, q, e.x, e.y, e.z, row, lane);
+                if (odd != 0.f && valid) odd_row[lane] = 1;
+                if (a.lse != nullptr && valid && warp == 0 && ib == 0)
+                    a.lse[place_of(token, g)] = none ? -INFINITY : (m + log2f(l)) * LN2;
+            }
+            __syncthreads();
+            for (int x = threadIdx.x; x < ROWS * NI; x += MERGE_THREADS) {
+                int t, gg;
+                if (row_of(a, e.z, tokens, row0 + x / NI, t, gg))
+                    reinterpret_cast<uint2*>(a.out + place_of(t, gg) * PG_ROW)[ib * NI + x % NI] = result[x / NI][x % NI];
+            }
+            if constexpr (!SPARSE) {
+                __syncthreads();  // (the rows made anew are written after these)
+                for (int x = warp; x < ROWS; x += MERGE_THREADS / 32) {
+                    int t, gg;
+                    if (odd_row[x] != 0 && row_of(a, e.z, tokens, row0 + x, t, gg))
+                        look_again<BF16>(a, q, e.x, e.y, e.z, t, gg, lane, lane / NI == ib);
+                }
             }
         }
     }
@@ -963,14 +979,14 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
         Piece p;
         while (walk.next(a, p)) {
             if (!p.whole()) continue;
-            for (int row = blockIdx.y * WARPS + warp; row < p.rows; row += gridDim.y * WARPS) {
+            for (int row = blockIdx.y * (MERGE_THREADS / 32) + warp; row < CHUNK_ROWS; row += gridDim.y * (MERGE_THREADS / 32)) {
                 int token, g;
-                row_of(a, p.j, row, token, g);
+                if (!row_of(a, p.j, p.tokens, row, token, g)) continue;
                 const size_t place = (static_cast<size_t>(p.q.row0) + token) * a.Hq + p.h * a.G + g;
                 const uint2 w = *reinterpret_cast<const uint2*>(a.out + place * PG_ROW + lane * 8);
                 const float2 x = pg_unpack<BF16>(w.x), y = pg_unpack<BF16>(w.y);
                 const bool fine = pg_finite(x.x) && pg_finite(x.y) && pg_finite(y.x) && pg_finite(y.y);
-                if (!__all_sync(FULL_MASK, fine)) look_again<BF16>(a, p.q, p.r, p.h, p.j, row, lane);
+                if (!__all_sync(FULL_MASK, fine)) look_again<BF16>(a, p.q, p.r, p.h, p.j, token, g, lane, true);
             }
         }
     }
@@ -991,32 +1007,45 @@ static bool make_map(CUtensorMap* map, const PagedAttnArgs& a, const uint8_t* x,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as copies of a tile of rows (a.tt tokens, a group's heads) x 64 channels.
+static bool make_query_map(CUtensorMap* map, const PagedAttnArgs& a, bool bf16) {
+    const TensorMapEncode encode = tensor_map_encode();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[4] = {64, 2, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.N)};
+    const cuuint64_t strides[3] = {128, PG_ROW, static_cast<cuuint64_t>(a.q_stride)};
+    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tt)}, one[4] = {1, 1, 1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<uint8_t*>(a.q), dims,
+                  strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Workspace a CTA: two pieces' results of 256 rows, and 128 bytes that say of what.
 constexpr size_t CHUNK_WS_CTA = 2 * CHUNK_ROWS * (PG_D * sizeof(float) + sizeof(float2)) + 128;
 
 template <bool BF16, bool SPARSE>
 static clo_status run_paged(const PagedAttnArgs& a, void* workspace, const clo_attn_opts* opts, cudaStream_t stream) {
     const auto main = paged_chunk_kernel<BF16, SPARSE>;
-    const auto merge = paged_merge_kernel<BF16, SPARSE>;
+    // The joining kernel: few rows may have many pieces, so they are spread over more
+    // blocks and lanes.
+    const long long rows = SPARSE ? a.G : static_cast<long long>(a.N) * a.G;
+    const bool few = SPARSE || (rows <= 64 && a.N <= a.tt);
+    const auto merge = few ? paged_merge_kernel<BF16, SPARSE, 8, 8> : paged_merge_kernel<BF16, SPARSE, 32, 32>;
+    const unsigned y = few ? static_cast<unsigned>((rows + 7) / 8) * 4 : CHUNK_ROWS / 32;
     if (!prepare_kernel(reinterpret_cast<const void*>(main), CH_SMEM) ||
         !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
         return CLO_ERR_CUDA;
     const int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count();
-    CUtensorMap map_k, map_v;
-    if (ctas <= 0 || !make_map(&map_k, a, a.kc, BF16) || !make_map(&map_v, a, a.vc, BF16)) return CLO_ERR_CUDA;
+    CUtensorMap map_q, map_k, map_v;
+    if (ctas <= 0 || !make_query_map(&map_q, a, BF16) || !make_map(&map_k, a, a.kc, BF16) || !make_map(&map_v, a, a.vc, BF16))
+        return CLO_ERR_CUDA;
     ChunkWs ws;
-    ws.o = static_cast<float*>(workspace);
-    ws.ml = reinterpret_cast<float2*>(ws.o + static_cast<size_t>(ctas) * 2 * CHUNK_ROWS * PG_D);
+    ws.o = static_cast<float4*>(workspace);
+    ws.ml = reinterpret_cast<float2*>(ws.o + static_cast<size_t>(ctas) * 2 * CHUNK_ROWS * (PG_D / 4));
     ws.desc = reinterpret_cast<int4*>(ws.ml + static_cast<size_t>(ctas) * 2 * CHUNK_ROWS);
     if (opts != nullptr && opts->ev_begin != nullptr && !record_event(opts->ev_begin, stream)) return CLO_ERR_CUDA;
-    if (launch_pdl(main, dim3(ctas), dim3(CH_THREADS), CH_SMEM, stream, a, ws, map_k, map_v) != cudaSuccess) return CLO_ERR_CUDA;
+    if (launch_pdl(main, dim3(ctas), dim3(CH_THREADS), CH_SMEM, stream, a, ws, map_q, map_k, map_v) != cudaSuccess) return CLO_ERR_CUDA;
     if (opts != nullptr && opts->ev_end != nullptr && !record_event(opts->ev_end, stream)) return CLO_ERR_CUDA;
-    // With few rows in all an item may have many pieces: a block a row, its warps
-    // share them.  Else a block eight rows, a warp each.
-    const long long rows = min(static_cast<long long>(CHUNK_ROWS), SPARSE ? static_cast<long long>(a.G) : static_cast<long long>(a.N) * a.G);
-    const int rows_each = rows <= 64 ? 1 : MERGE_THREADS / 32;
-    const unsigned y = static_cast<unsigned>((rows + rows_each - 1) / rows_each);
-    return launch_pdl(merge, dim3(ctas, y), dim3(MERGE_THREADS), 0, stream, a, ws, ctas, rows_each) == cudaSuccess ? CLO_OK : CLO_ERR_CUDA;
+    return launch_pdl(merge, dim3(ctas, y), dim3(MERGE_THREADS), 0, stream, a, ws, ctas) == cudaSuccess ? CLO_OK : CLO_ERR_CUDA;
 }
 
 static clo_status run_paged_attention(const PagedAttnArgs& a, bool sparse, clo_dtype dtype, void* workspace, const clo_attn_opts* opts,
@@ -1101,7 +1130,7 @@ extern "C" clo_status clo_paged_chunk_attn(const clo_paged_chunk_attn_args* args
     a.ctx_len = r.ctx_len;
     a.offsets = r.offsets;
     a.err_flag = r.err_flag;
-    a.q_stride = r.N > 1 ? 2 * r.q_stride : 0;
+    a.q_stride = 2 * (r.N > 1 ? r.q_stride : row);
     a.kv_block = 2 * kb;
     a.kv_head = 2 * kh;
     a.kv_token = 2 * kt;
@@ -1111,6 +1140,7 @@ extern "C" clo_status clo_paged_chunk_attn(const clo_paged_chunk_attn_args* args
     a.Hq = r.Hq;
     a.Hkv = r.Hkv;
     a.G = r.Hq / r.Hkv;
+    a.tt = tile_tokens(a.G);
     a.num_blocks = r.num_blocks;
     a.max_blocks = r.max_blocks;
     return run_paged_attention(a, false, r.dtype, r.workspace, r.opts, stream);
@@ -1148,6 +1178,7 @@ extern "C" clo_status clo_paged_sparse_decode_attn(const clo_paged_sparse_attn_a
     a.Hq = r.Hq;
     a.Hkv = r.Hkv;
     a.G = r.Hq / r.Hkv;
+    a.tt = tile_tokens(a.G);
     a.num_blocks = r.num_blocks;
     a.max_blocks = r.max_blocks;
     a.n_sel = r.n_sel;

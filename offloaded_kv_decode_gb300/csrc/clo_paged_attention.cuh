@@ -21,6 +21,7 @@ struct PagedAttnArgs {
     long long q_stride, kv_block, kv_head, kv_token;  // bytes
     float scale_log2;
     int B, N, Hq, Hkv, G, num_blocks, max_blocks, n_sel;
+    int tt;  // tokens of a tile of rows (clo_paged_attention.cu)
 };
 
 // A request as the kernels take it.
@@ -78,11 +79,25 @@ __device__ __forceinline__ int paged_place(const PagedAttnArgs& a, int r, int h,
     return id * 32 + min(sees - col * PG_BLOCK, PG_BLOCK);
 }
 
+// A pair of results in 16 bits.  Rounded weights may take an fp16 sum past the
+// largest V by a little: finite ones stop at 65504.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pg_pack_out(float lo, float hi) {
+    if constexpr (BF16) {
+        return pg_pack<true>(lo, hi);
+    } else {
+        const float top = 65504.f;
+        const float x = fabsf(lo) <= 66000.f ? fminf(fmaxf(lo, -top), top) : lo;
+        const float y = fabsf(hi) <= 66000.f ? fminf(fmaxf(hi, -top), top) : hi;
+        return pg_pack<false>(x, y);
+    }
+}
+
 // The attention of one query row by one warp, token after token in fp32: lane l
 // holds channels 4l .. 4l + 3.  Slow, and without any value of a token that the
-// row does not see.
+// row does not see.  `mine`: this lane's channels are written.
 template <bool BF16, bool SPARSE>
-__device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const PagedReq& req, int i, int head, int lane) {
+__device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const PagedReq& req, int i, int head, int lane, bool mine) {
     const int h = head / a.G;
     const size_t row = static_cast<size_t>(req.row0) + i;
     const uint2 qw = *reinterpret_cast<const uint2*>(a.q + static_cast<long long>(row) * a.q_stride + head * PG_ROW + lane * 8);
@@ -120,12 +135,10 @@ __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const Page
     const bool none = bad || l == 0.f;
     const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        o[c] = none ? 0.f : o[c] * inv;
-        if (!BF16 && pg_finite(o[c])) o[c] = fminf(fmaxf(o[c], -65504.f), 65504.f);
-    }
+    for (int c = 0; c < 4; ++c) o[c] = none ? 0.f : o[c] * inv;
     const size_t place = row * a.Hq + head;
-    *reinterpret_cast<uint2*>(a.out + place * PG_ROW + lane * 8) = make_uint2(pg_pack<BF16>(o[0], o[1]), pg_pack<BF16>(o[2], o[3]));
+    if (!mine) return;
+    *reinterpret_cast<uint2*>(a.out + place * PG_ROW + lane * 8) = make_uint2(pg_pack_out<BF16>(o[0], o[1]), pg_pack_out<BF16>(o[2], o[3]));
     if (a.lse != nullptr && lane == 0) a.lse[place] = none ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
