@@ -149,7 +149,7 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  * Scores and sums are in fp32; the weights are rounded to `dtype` for the product
  * with V, in fp16 after a factor that keeps what is 2^-31 of the largest.  The same
  * call on the same kind of GPU gives the same bits each time.
- * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, N * Hq < 2^31,
+ * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, N * Hq < 2^29,
  * max_blocks <= 2^20, num_blocks <= 2^26, scale > 0.
  */
 typedef struct clo_paged_chunk_attn_args {
@@ -291,8 +291,8 @@ clo_status clo_paged_block_select(const clo_paged_block_select_args* args, cudaS
  * workspace: >= clo_paged_chunk_workspace_size(Hq, Hkv, d, num_ctas) bytes,
  *            16-byte aligned.
  * Sums are in fp32; the weights are rounded to `dtype` for the product with V.
- * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, num_blocks < 2^26,
- * B * Hkv * n_sel < 2^31.
+ * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, B * Hq < 2^29,
+ * num_blocks <= 2^26, max_blocks <= 2^20, B * Hkv * n_sel < 2^31, scale > 0.
  */
 typedef struct clo_paged_sparse_attn_args {
     const void* q;

@@ -50,8 +50,9 @@ constexpr int CH_THREADS = 384;
 constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
 constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
-constexpr int CH_FIXED = 128;                     // what an item costs beside its tokens, in tokens
-constexpr int CH_LEAST = 256;                     // tokens that are worth a CTA of their own
+constexpr int CH_FIXED = 256;                     // what an item costs beside its tokens, in tokens
+constexpr int CH_LEAST = 384;                     // weight that is worth a CTA of its own
+constexpr int CH_JOIN = 512;                      // what cutting an item costs (partial results, the join), in tokens
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
 constexpr int CH_SMALL = 2048;                    // shared memory beside the tiles
 constexpr int CH_SMEM = CHUNK_ROWS * PG_ROW + CH_STAGES * CH_TILE_BYTES + CH_SMALL + 1024;
@@ -67,11 +68,16 @@ struct ChunkWs {
     float2* ml;   // [CTA][2][256] reference and denominator; denominator -1: bad data
     int4* desc;   // [CTA][8]: see CH_DESC
 };
-enum { DESC_START, DESC_END, DESC_FLAGS };  // flags: x head piece, y that piece ends its item, z tail piece, w look again
+// Of a CTA: where its share starts and ends; flags: x head piece (of an item that starts
+// in an earlier share), y tail piece (of one that ends in a later share), w look again; for
+// the tail piece, the CTA in whose share the item ends, its request's first row and rows.
+enum { DESC_START, DESC_END, DESC_FLAGS, DESC_TAIL };
 
 struct alignas(16) ChunkSmall {
     unsigned long long full[CH_STAGES], empty[CH_STAGES], q_full, q_empty, s_full[2], p_ready[2], o_full[2], x_full, x_empty, drain;
     ChunkPos start, end;
+    PagedReq first;  // the request that the share starts in
+    int4 tail;       // DESC_TAIL
     uint32_t tmem;
     int dead;      // a wait ran out
     int again;     // a complete item has a result that is not finite
@@ -95,56 +101,95 @@ __device__ __forceinline__ int items_of(const PagedAttnArgs& a, const PagedReq& 
     return static_cast<int>((static_cast<unsigned>(q.n) + 2 * a.tt - 1) / (2 * a.tt));
 }
 
-// The weights of a request's items of one KV head, in tokens: item j weighs the
-// tokens before the new ones, CH_FIXED and the new ones up to its end.
+// The weights of a request's items of one KV head, in tokens (or 2^shift of them, so
+// that all of a call's weights stay below 2^31): item j weighs the tokens before the
+// new ones, CH_FIXED and the new ones up to its end.
 struct Weights {
-    long long each, last;  // each = without the part that rises
-    int items, tt;
-    __device__ long long before(int j) const {  // items 0 .. j - 1
-        return j < items ? j * each + static_cast<long long>(j) * (j + 1) * tt : all();
+    unsigned each, last;  // each = without the part that rises
+    int items, tt, shift;
+    __device__ unsigned before(int j) const {  // items 0 .. j - 1
+        return j < items ? j * each + rise(j) : all();
     }
-    __device__ long long all() const {
-        const long long m = items - 1;
-        return items == 0 ? 0 : m * each + m * (m + 1) * tt + last;
+    __device__ unsigned all() const { return items == 0 ? 0 : (items - 1) * each + rise(items - 1) + last; }
+    __device__ unsigned rise(int j) const {
+        return static_cast<unsigned>((static_cast<unsigned long long>(j) * (j + 1) * tt) >> shift);
     }
 };
 template <bool SPARSE>
 __device__ __forceinline__ Weights weights_of(const PagedAttnArgs& a, const PagedReq& q) {
     Weights w;
     w.tt = a.tt;
+    w.shift = a.shift;
     w.items = items_of(a, q);
-    const long long base = SPARSE ? 0 : max(q.ctx - q.n, 0);
-    w.each = base + CH_FIXED;
-    w.last = (SPARSE ? item_sees<true>(a, q, 0) : base + q.n) + CH_FIXED;
+    const int base = SPARSE ? 0 : max(q.ctx - q.n, 0);
+    w.each = max((base + CH_FIXED) >> a.shift, 1);
+    w.last = max(((SPARSE ? item_sees<true>(a, q, 0) : base + q.n) + CH_FIXED) >> a.shift, 1);
     return w;
 }
 
-// The place of weight x; prefix[r] = weight of the requests before r.
-template <bool SPARSE>
-__device__ ChunkPos locate(const PagedAttnArgs& a, const long long* prefix, long long x) {
-    if (x >= prefix[a.B]) return ChunkPos{a.B, 0, 0, 0};
-    int lo = 0, hi = a.B - 1;  // the first r with prefix[r + 1] > x
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid + 1] > x) hi = mid;
-        else lo = mid + 1;
+// What a CTA knows of the requests while it finds its share, in the ring's memory.
+struct Shares {
+    unsigned weight[PG_MAX_B + 1];  // of the requests before
+    int items[PG_MAX_B + 1];        // of all heads
+    PagedReq req[PG_MAX_B];
+    unsigned warp_weight[CH_THREADS / 32];
+    int warp_items[CH_THREADS / 32], warp_most[CH_THREADS / 32];
+};
+static_assert(sizeof(Shares) <= CH_STAGES * CH_TILE_BYTES, "");
+
+// How a call's work is shared out over `grid` CTAs.  Cut: even shares of the weight,
+// wherever they fall.  Whole items, where that is as good: one a CTA if there are enough
+// CTAs, else even shares up to items' starts.  A cut costs CH_JOIN, a whole item up to
+// its own weight more than the even share.
+struct Split {
+    bool whole, by_item;
+    int ctas;
+    unsigned each, more;  // CTA c's share starts at weight each * c + min(c, more)
+    __device__ Split(unsigned all, int items, int most, int grid, int shift) {
+        const unsigned least = max(CH_LEAST >> shift, 1);
+        by_item = items <= grid;
+        whole = by_item ? most <= static_cast<int>(max(all / grid, least)) + (CH_JOIN >> shift) : most <= (CH_JOIN >> shift);
+        by_item &= whole;
+        ctas = items == 0 ? 0 : by_item ? items : whole ? grid : max(min(grid, static_cast<int>(all / least)), 1);
+        if (!whole && ctas > items && items > 0) ctas -= ctas % items;  // items of one size: pieces of one size
+        each = ctas > 0 ? all / ctas : 0;
+        more = all - each * ctas;
     }
-    const int r = lo;
-    const PagedReq q = paged_request<SPARSE>(a, r);
+    __device__ unsigned start(int c) const { return each * c + min(static_cast<unsigned>(c), more); }
+    // The CTA whose share weight x belongs to.
+    __device__ int owner(unsigned x) const {
+        return static_cast<int>(x < (each + 1) * more ? x / (each + 1) : more + (x - (each + 1) * more) / each);
+    }
+};
+
+// Item `x` (counted over the heads) of request r.
+__device__ __forceinline__ ChunkPos item_at(const PagedAttnArgs& a, const PagedReq& q, int r, int x) {
+    const int n = items_of(a, q);
+    return ChunkPos{r, x / n, x % n, 0};
+}
+
+// Where weight `rest` of request r lies; whole: the item that starts there or behind.
+template <bool SPARSE>
+__device__ ChunkPos weight_at(const PagedAttnArgs& a, const PagedReq& q, int r, unsigned rest, bool whole) {
     const Weights w = weights_of<SPARSE>(a, q);
-    const long long head = w.all();
-    long long rest = x - prefix[r];
+    const unsigned head = w.all();
     const int h = static_cast<int>(rest / head);
     rest -= h * head;
-    lo = 0, hi = w.items - 1;  // the last j with before(j) <= rest
+    int lo = 0, hi = w.items - 1;  // the last j with before(j) <= rest
+#pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (w.before(mid) <= rest) lo = mid;
         else hi = mid - 1;
     }
     const int tiles = (item_sees<SPARSE>(a, q, lo) + CH_TILE - 1) / CH_TILE;
-    const long long off = rest - w.before(lo), size = w.before(lo + 1) - w.before(lo);
-    return ChunkPos{r, h, lo, static_cast<int>(off * tiles / size)};
+    const float part = __fdividef(static_cast<float>(rest - w.before(lo)), static_cast<float>(w.before(lo + 1) - w.before(lo)));
+    ChunkPos p{r, h, lo, max(min(static_cast<int>(part * tiles), tiles - 1), 0)};
+    if (whole && rest > w.before(lo)) {
+        p = ChunkPos{r, h, lo + 1, 0};
+        if (p.j == w.items) p = h + 1 < a.Hkv ? ChunkPos{r, h + 1, 0, 0} : ChunkPos{r + 1, 0, 0, 0};
+    }
+    return p;
 }
 
 // One piece of work: tiles lo .. hi - 1 of an item of `tiles`.
@@ -165,6 +210,8 @@ struct Walk {
     int items;
     bool loaded;
     __device__ Walk(const ChunkPos& s, const ChunkPos& e) : at(s), end(e), items(0), loaded(false) {}
+    __device__ Walk(const PagedAttnArgs& a, const ChunkPos& s, const ChunkPos& e, const PagedReq& first)
+        : q(first), at(s), end(e), items(items_of(a, first)), loaded(true) {}
     __device__ bool next(const PagedAttnArgs& a, Piece& p) {
         while (at.r < a.B) {
             if (at.r > end.r) return false;
@@ -481,7 +528,7 @@ struct RowSoftmax {
                 const float f = moves ? ex2(ref - to) : 1.f;
                 ref = to;
                 sum *= f;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     float o[16];
                     const uint32_t at = tmem + (2 + s) * CH_TILE + 16 * c;
@@ -538,7 +585,9 @@ struct RowSoftmax {
         const bool none = bad || !(sum != 0.f);  // (a NaN is something)
         const float inv = none ? 0.f : 1.f / sum;
         float odd = 0.f;  // turns NaN with a value that is not finite
-#pragma unroll
+        if (!__any_sync(FULL_MASK, valid)) return;
+        // (Not unrolled: this runs once a piece, and its instructions come from far.)
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             float o[32];
             load(o, c);
@@ -601,6 +650,7 @@ struct RowSoftmax {
             const int x = t * CH_PLACES + (lane & 7);
             return x < places ? max(paged_place<true>(a, p.r, p.h, p.q.ctx, x), 0) & 31 : 0;
         };
+        const bool idle = !__any_sync(FULL_MASK, valid);
         float ref = -INFINITY, sum = 0.f;
         const int step = two ? 1 : 2, t0 = p.lo + (two ? 0 : s);
         int rows_next = SPARSE && t0 < p.hi ? place_rows(t0) : 0;
@@ -610,6 +660,10 @@ struct RowSoftmax {
             const int seen = sees - t * CH_TILE;
             const bool masked = SPARSE ? __any_sync(FULL_MASK, rows_here != PG_BLOCK) : __any_sync(FULL_MASK, seen < CH_TILE);
             if (!ch_warp_wait(sm->s_full[s], s_count++ & 1, sm)) return false;
+            if (idle) {  // nobody reads what becomes of these rows
+                if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[s]));
+                continue;
+            }
             tc_fence_after();
             tile(seen, rows_here, masked, t == t0, ref, sum);
         }
@@ -701,46 +755,128 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // The weights of the requests, summed up, in the ring's memory.
-    long long* prefix = reinterpret_cast<long long*>(ring);
-    long long* warp_sum = prefix + PG_MAX_B + 1;
-    {
-        const int per = (a.B + CH_THREADS - 1) / CH_THREADS, r0 = threadIdx.x * per, r1 = min(a.B, r0 + per);
-        long long local = 0;
+    // The share: warp 0 finds its end, warp 8 its start.
+    const int cta = blockIdx.x;
+    Shares& sh = *reinterpret_cast<Shares*>(ring);
+    const bool finder = warp == 0 || warp == 8;
+    const bool one_warp = a.B <= 32;  // a request a lane; else summed up by all threads
+    PagedReq req{0, 0, 0, false};
+    unsigned weight = 0, weight1 = 0;  // up to and with this thread's requests; of those alone
+    int items = 0, items1 = 0, most = 0;
+    const auto add = [&](const PagedReq& q) {
+        const Weights w = weights_of<SPARSE>(a, q);
+        weight += w.all() * a.Hkv;
+        items += w.items * a.Hkv;
+        if (w.items > 0) most = max(most, static_cast<int>(w.last));
+    };
+    if (!one_warp || finder) {
+        const int per = one_warp ? 1 : (a.B + CH_THREADS - 1) / CH_THREADS;
+        const int r0 = (one_warp ? lane : static_cast<int>(threadIdx.x)) * per, r1 = min(a.B, r0 + per);
         bool bad = false;
+#pragma unroll 1
         for (int r = r0; r < r1; ++r) {
-            const PagedReq q = paged_request<SPARSE>(a, r);
-            bad |= q.bad;
-            local += weights_of<SPARSE>(a, q).all() * a.Hkv;
+            req = paged_request<SPARSE>(a, r);
+            bad |= req.bad;
+            if (!one_warp) sh.req[r] = req;
+            add(req);
         }
-        if (bad && blockIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
-        long long sum = local;
+        if (bad && cta == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
+        weight1 = weight;
+        items1 = items;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const long long v = __shfl_up_sync(FULL_MASK, sum, off);
-            if (lane >= off) sum += v;
-        }
-        if (lane == 31) warp_sum[warp] = sum;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-        if (threadIdx.x == 0) prefix[0] = 0;
-        if (per == 1) {
-            if (r0 < r1) prefix[r1] = sum;
-        } else {
-            sum -= local;
-            for (int r = r0; r < r1; ++r) {
-                sum += weights_of<SPARSE>(a, paged_request<SPARSE>(a, r)).all() * a.Hkv;
-                prefix[r + 1] = sum;
+            const unsigned v = __shfl_up_sync(FULL_MASK, weight, off);
+            const int n = __shfl_up_sync(FULL_MASK, items, off);
+            if (lane >= off) {
+                weight += v;
+                items += n;
             }
         }
-        __syncthreads();
+        most = __reduce_max_sync(FULL_MASK, most);
+        if (!one_warp) {
+            if (lane == 31) {
+                sh.warp_weight[warp] = weight;
+                sh.warp_items[warp] = items;
+                sh.warp_most[warp] = most;
+            }
+            __syncthreads();
+            weight -= weight1;
+            items -= items1;
+            for (int w = 0; w < warp; ++w) {
+                weight += sh.warp_weight[w];
+                items += sh.warp_items[w];
+            }
+            if (threadIdx.x == 0) {
+                sh.weight[0] = 0;
+                sh.items[0] = 0;
+            }
+#pragma unroll 1
+            for (int r = r0; r < r1; ++r) {
+                add(sh.req[r]);
+                sh.weight[r + 1] = weight;
+                sh.items[r + 1] = items;
+            }
+            __syncthreads();
+            most = __reduce_max_sync(FULL_MASK, lane < CH_THREADS / 32 ? sh.warp_most[lane] : 0);
+        }
     }
-    const int cta = blockIdx.x;
-    if (lane == 0 && warp < 2) {
-        const long long all = prefix[a.B];
-        const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), all / (CH_LEAST + CH_FIXED)));
-        const long long c = min(static_cast<long long>(cta) + warp, ctas);
-        (warp == 0 ? sm->start : sm->end) = locate<SPARSE>(a, prefix, all / ctas * c + all % ctas * c / ctas);
+    if (finder) {
+        const unsigned all = one_warp ? __shfl_sync(FULL_MASK, weight, 31) : sh.weight[a.B];
+        const int n = one_warp ? __shfl_sync(FULL_MASK, items, 31) : sh.items[a.B];
+        const Split split(all, n, most, gridDim.x, a.shift);
+        const int c = cta + (warp == 0);
+        ChunkPos p{a.B, 0, 0, 0};
+        PagedReq q{0, 0, 0, false};
+        int4 tail = make_int4(0, 0, 0, 0);
+        if (c < split.ctas) {
+            // The request: the first whose end lies behind the start's weight or item.
+            const unsigned x = split.start(c);
+            int r;
+            unsigned w0;
+            int i0;
+            if (one_warp) {
+                r = __popc(__ballot_sync(FULL_MASK, split.by_item ? items <= c : weight <= x));
+                w0 = __shfl_sync(FULL_MASK, weight - weight1, r);
+                i0 = __shfl_sync(FULL_MASK, items - items1, r);
+                q.row0 = __shfl_sync(FULL_MASK, req.row0, r);
+                q.n = __shfl_sync(FULL_MASK, req.n, r);
+                q.ctx = __shfl_sync(FULL_MASK, req.ctx, r);
+            } else {
+                int lo = 0, hi = a.B - 1;
+#pragma unroll 1
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (split.by_item ? sh.items[mid + 1] > c : sh.weight[mid + 1] > x) hi = mid;
+                    else lo = mid + 1;
+                }
+                r = lo;
+                w0 = sh.weight[r];
+                i0 = sh.items[r];
+                q = sh.req[r];
+            }
+            p = split.by_item ? item_at(a, q, r, c - i0) : weight_at<SPARSE>(a, q, r, x - w0, split.whole);
+            if (warp == 0 && p.cut > 0) {
+                const Weights w = weights_of<SPARSE>(a, q);
+                tail = make_int4(split.owner(w0 + p.h * w.all() + w.before(p.j + 1) - 1), q.row0, q.n, q.ctx);
+            }
+            if (p.r != r) q = p.r < a.B ? paged_request<SPARSE>(a, p.r) : PagedReq{0, 0, 0, false};
+        }
+        if (lane == 0) {
+            if (warp == 0) {
+                sm->end = p;
+                sm->tail = tail;
+            } else {
+                sm->start = p;
+                sm->first = q;
+            }
+        }
+        if (warp == 8 && p.r < a.B && q.n > 0) {  // the first places' blocks, on their way while the roles begin
+            const int x = p.cut * CH_PLACES + lane;
+            if (!SPARSE && x < paged_places<SPARSE>(a, item_sees<SPARSE>(a, q, p.j)))
+                prefetch_l1(a.table + static_cast<size_t>(p.r) * a.max_blocks + x);
+            if (SPARSE && x < paged_places<SPARSE>(a, q.ctx))
+                prefetch_l1(a.sel + (static_cast<size_t>(p.r) * a.Hkv + p.h) * a.n_sel + x);
+        }
     }
     tc_fence_before();
     async_proxy_fence();  // copies will write where the weights lie
@@ -748,7 +884,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     tc_fence_after();
     const ChunkPos start = sm->start, end = sm->end;
     const uint32_t tmem = sm->tmem;
-    Walk<SPARSE> walk(start, end);
+    Walk<SPARSE> walk(a, start, end, sm->first);
     Piece p;
 
     if (warp < 8) {
@@ -761,15 +897,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         regs_down<CH_REGS_REST>();
         if (warp == 8) {
             Loader<SPARSE> w{a, &map_k, &map_v, sm, smem_u32(ring), lane};
-            int head = 0, head_ends = 0, tail = 0, count = 0;
+            int head = 0, tail = 0, count = 0;
             bool ok = true;
             while (ok && walk.next(a, p)) {
-                if (p.lo > 0) {
-                    head = 1;
-                    head_ends = p.hi == p.tiles;
-                } else if (p.hi < p.tiles) {
-                    tail = 1;
-                }
+                if (p.lo > 0) head = 1;
+                else if (p.hi < p.tiles) tail = 1;
                 if (p.hi == p.lo) continue;
                 if (lane == 0) *reinterpret_cast<volatile int*>(&sm->bad[count & 7]) = 0;
                 ok = w.piece(p, count & 7);
@@ -779,7 +911,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 int4* d = ws.desc + static_cast<size_t>(cta) * 8;
                 d[DESC_START] = make_int4(start.r, start.h, start.j, start.cut);
                 d[DESC_END] = make_int4(end.r, end.h, end.j, end.cut);
-                d[DESC_FLAGS] = make_int4(head, head_ends, tail, 0);
+                d[DESC_FLAGS] = make_int4(head, tail, 0, 0);
+                d[DESC_TAIL] = sm->tail;
             }
             if (!ok)  // copies in flight land before the memory is given up
                 for (int x = max(w.it - CH_STAGES, 0); x < w.it; ++x)
@@ -859,34 +992,25 @@ __device__ __noinline__ void look_again(const PagedAttnArgs& a, const PagedReq& 
 template <bool BF16, bool SPARSE, int ROWS, int NI>
 __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedAttnArgs a, const ChunkWs ws, int ctas) {
     constexpr int SUBS = 32 / ROWS, K = NI / 8, AHEAD = 8 / K;
-    __shared__ int last, odd_row[ROWS];
+    __shared__ int odd_row[ROWS];
     __shared__ uint2 result[ROWS][NI + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
     const int c = blockIdx.x;
-    const int4 flags = ws.desc[static_cast<size_t>(c) * 8 + DESC_FLAGS];
-    if (flags.z != 0) {
-        const int4 e = ws.desc[static_cast<size_t>(c) * 8 + DESC_END];  // (the item ends behind c's share)
-        const PagedReq q = paged_request<SPARSE>(a, e.x);
+    const int4* desc = ws.desc + static_cast<size_t>(c) * 8;
+    const int4 flags = desc[DESC_FLAGS], e = desc[DESC_END], tail = desc[DESC_TAIL];
+    if (flags.y != 0) {
+        // Item e of request e.x: its pieces are c's tail and the head pieces of the CTAs up
+        // to tail.x (one with too small a share has none).
+        const PagedReq q{tail.y, tail.z, tail.w, false};
         const int tokens = min(2 * a.tt, q.n - e.z * 2 * a.tt);
         const int ib = blockIdx.y % (32 / NI), row0 = blockIdx.y / (32 / NI) * ROWS;
         int token, g;
         if (row_of(a, e.z, tokens, row0, token, g)) {  // else no row of the block is one
-            if (warp == 0) {
-                // Its pieces are c's tail and the head pieces of the CTAs up to `last` (one
-                // with no share has none).
-                int found = -1;
-                for (int x = c + 1; found < 0 && x < ctas; x += 32) {
-                    const int4 f = x + lane < ctas ? ws.desc[static_cast<size_t>(x + lane) * 8 + DESC_FLAGS] : make_int4(0, 0, 0, 0);
-                    const unsigned m = __ballot_sync(FULL_MASK, f.x != 0 && f.y != 0);
-                    if (m != 0) found = x + __ffs(m) - 1;
-                }
-                if (lane == 0) last = found < 0 ? ctas - 1 : found;
-            }
             if (static_cast<int>(threadIdx.x) < ROWS) odd_row[threadIdx.x] = 0;
             __syncthreads();
-            const int end = last, row = row0 + lane % ROWS;
+            const int end = min(tail.x, ctas - 1), row = row0 + lane % ROWS;
             const bool valid = row_of(a, e.z, tokens, row, token, g);
             float m = -INFINITY, l = 0.f;
             float4 o[K];
@@ -974,7 +1098,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
     }
     if (!SPARSE && flags.w != 0) {
         // Whole items of CTA c with results that are not finite: this block's rows of each.
-        const int4 s = ws.desc[static_cast<size_t>(c) * 8 + DESC_START], e = ws.desc[static_cast<size_t>(c) * 8 + DESC_END];
+        const int4 s = desc[DESC_START];
         Walk<SPARSE> walk(ChunkPos{s.x, s.y, s.z, s.w}, ChunkPos{e.x, e.y, e.z, e.w});
         Piece p;
         while (walk.next(a, p)) {
@@ -1023,8 +1147,13 @@ static bool make_query_map(CUtensorMap* map, const PagedAttnArgs& a, bool bf16) 
 constexpr size_t CHUNK_WS_CTA = 2 * CHUNK_ROWS * (PG_D * sizeof(float) + sizeof(float2)) + 128;
 
 template <bool BF16, bool SPARSE>
-static clo_status run_paged(const PagedAttnArgs& a, void* workspace, const clo_attn_opts* opts, cudaStream_t stream) {
+static clo_status run_paged(PagedAttnArgs a, void* workspace, const clo_attn_opts* opts, cudaStream_t stream) {
     const auto main = paged_chunk_kernel<BF16, SPARSE>;
+    // No item weighs more than the longest request, the new tokens and CH_FIXED.
+    const double items = (a.N / (2.0 * a.tt) + min(a.B, a.N)) * a.Hkv;
+    const double most = items * (CH_FIXED + (SPARSE ? 16.0 * a.n_sel : 16.0 * a.max_blocks + a.N));
+    a.shift = 0;
+    while (most / static_cast<double>(1ll << a.shift) >= 1.0e9) ++a.shift;
     // The joining kernel: few rows may have many pieces, so they are spread over more
     // blocks and lanes.
     const long long rows = SPARSE ? a.G : static_cast<long long>(a.N) * a.G;
@@ -1084,7 +1213,7 @@ static clo_status check_paged(const void* q, const void* kc, const void* vc, con
     for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(ctx), static_cast<const void*>(lists),
                           static_cast<const void*>(lse), static_cast<const void*>(err_flag)})
         if (!pg_aligned(p, 4)) return CLO_ERR_INVALID_ARG;
-    if (d != PG_D || block_size != PG_BLOCK || Hq / Hkv > PG_MAX_G || B > PG_MAX_B || rows * Hq >= (1ll << 31) ||
+    if (d != PG_D || block_size != PG_BLOCK || Hq / Hkv > PG_MAX_G || B > PG_MAX_B || rows * Hq >= (1ll << 29) ||
         max_blocks > (1 << 20) || num_blocks > (1 << 26) || (opts != nullptr && opts->num_ctas > CHUNK_MAX_CTAS))
         return CLO_ERR_UNSUPPORTED;
     if (B > 0 && rows > 0) {

@@ -21,7 +21,7 @@ struct PagedAttnArgs {
     long long q_stride, kv_block, kv_head, kv_token;  // bytes
     float scale_log2;
     int B, N, Hq, Hkv, G, num_blocks, max_blocks, n_sel;
-    int tt;  // tokens of a tile of rows (clo_paged_attention.cu)
+    int tt, shift;  // tokens of a tile of rows; unit of weights (clo_paged_attention.cu)
 };
 
 // A request as the kernels take it.

@@ -129,9 +129,10 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) block_bounds_kernel(const Boun
 
 // ---------------------------------------------------------------- scores
 
-constexpr int SCORE_THREADS = 128;
-constexpr int SCORE_AHEAD = 4;                                   // records an 8-lane group keeps in flight
-constexpr int SCORE_BLOCKS = SCORE_THREADS / 8 * SCORE_AHEAD;    // columns a CTA scores
+constexpr int SCORE_THREADS = 256;
+constexpr int SCORE_GROUPS = SCORE_THREADS / 8;                  // an 8-lane group a record
+constexpr int SCORE_AHEAD = 4;                                   // records a group keeps in flight
+constexpr int SCORE_BLOCKS = SCORE_GROUPS * 8;                   // columns a CTA scores: 8 a group
 constexpr uint32_t KEY_ALWAYS = 0xffffffffu;                     // above every score's key
 
 struct SelectArgs {
@@ -139,10 +140,10 @@ struct SelectArgs {
     const uint8_t* bounds;
     const int32_t* table;
     const int32_t* ctx_len;
-    uint32_t* keys;  // [B * Hkv][max_blocks]
+    uint32_t* keys;  // [B * Hkv][key_stride]
     int32_t* sel;
     int32_t* err_flag;
-    int Hq, Hkv, G, num_blocks, max_blocks, n_sel, n_first, n_last;
+    int Hq, Hkv, G, num_blocks, max_blocks, n_sel, n_first, n_last, key_stride;
 };
 
 // The blocks of a request, or -1 for a bad length.
@@ -158,10 +159,13 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// 256 columns of one request and KV head a CTA.  HBM-bound (272 bytes a record): a group's
+// lane u looks up the block of its u-th column, all eight at once, and the records come
+// four at a time while the query's codes are made and then the ones before are summed up.
 template <bool BF16>
-__global__ void __launch_bounds__(SCORE_THREADS) block_score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SCORE_THREADS, 4) block_score_kernel(const SelectArgs a) {
     __shared__ float warp_max[SCORE_THREADS / 32];
-    __shared__ uint32_t pos_codes[PG_D / 4], neg_codes[PG_D / 4];
+    __shared__ __align__(16) uint32_t pos_codes[PG_D / 4], neg_codes[PG_D / 4];
     pdl_launch_dependents();
     pdl_wait();
     const int r = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
@@ -170,37 +174,48 @@ __global__ void __launch_bounds__(SCORE_THREADS) block_score_kernel(const Select
     if (nb < 0 && blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
     if (nb <= a.n_sel || first >= nb) return;  // all blocks are selected: no scores
 
-    const int u = threadIdx.x & 7, grp = threadIdx.x >> 3;  // an 8-lane group a record
+    const int u = threadIdx.x & 7, grp = threadIdx.x >> 3;
+    // Column of the group's j-th record: neighbouring groups take neighbouring columns.
+    const int mine = first + u * SCORE_GROUPS + grp;
+    int id = 0;
+    if (mine < nb) {
+        id = a.table[static_cast<size_t>(r) * a.max_blocks + mine];
+        if (id < 0 || id >= a.num_blocks) {
+            report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
+            id = -1;
+        }
+    }
+    const int lane0 = threadIdx.x & 24;  // the group's first lane
     uint4 rec[SCORE_AHEAD][2];
     float scale[SCORE_AHEAD];
-    bool bad = false;
+    const auto load = [&](int j0) {
 #pragma unroll
-    for (int j = 0; j < SCORE_AHEAD; ++j) {
-        const int col = first + j * (SCORE_THREADS / 8) + grp;
-        rec[j][0] = rec[j][1] = make_uint4(0u, 0u, 0u, 0u);
-        scale[j] = 0.f;
-        if (col < nb) {
-            const int id = a.table[static_cast<size_t>(r) * a.max_blocks + col];
-            if (id < 0 || id >= a.num_blocks) {
-                bad = true;
-                scale[j] = INFINITY;
-            } else {
-                const uint8_t* p = a.bounds + (static_cast<size_t>(id) * a.Hkv + g) * PG_RECORD;
+        for (int j = 0; j < SCORE_AHEAD; ++j) {
+            const int block = __shfl_sync(FULL_MASK, id, lane0 + j0 + j);
+            rec[j][0] = rec[j][1] = make_uint4(0u, 0u, 0u, 0u);
+            scale[j] = INFINITY;
+            if (block >= 0 && first + (j0 + j) * SCORE_GROUPS + grp < nb) {
+                const uint8_t* p = a.bounds + (static_cast<size_t>(block) * a.Hkv + g) * PG_RECORD;
                 rec[j][0] = *reinterpret_cast<const uint4*>(p + 32 * u);
                 rec[j][1] = *reinterpret_cast<const uint4*>(p + 32 * u + 16);
                 scale[j] = *reinterpret_cast<const float*>(p + 256);
             }
         }
-    }
+    };
+    load(0);
     // The query's codes: thread c sums channel c over the group's heads, in order.
     float s = 0.f;
-    {
+    if (threadIdx.x < PG_D) {
         const uint16_t* q = static_cast<const uint16_t*>(a.q) +
                             (static_cast<size_t>(r) * a.Hq + static_cast<size_t>(g) * a.G) * PG_D + threadIdx.x;
-        for (int h = 0; h < a.G; ++h) {
-            const float x = pg_unpack<BF16>(q[h * PG_D]).x;
-            s = h == 0 ? x : s + x;
-        }
+        uint16_t x[PG_MAX_G];
+#pragma unroll
+        for (int h = 0; h < PG_MAX_G; ++h)
+            if (h < a.G) x[h] = q[h * PG_D];
+        s = pg_unpack<BF16>(x[0]).x;
+#pragma unroll
+        for (int h = 1; h < PG_MAX_G; ++h)
+            if (h < a.G) s += pg_unpack<BF16>(x[h]).x;
     }
     float m = fabsf(s);
     const bool finite = __syncthreads_and(pg_finite(s)) != 0;
@@ -208,130 +223,167 @@ __global__ void __launch_bounds__(SCORE_THREADS) block_score_kernel(const Select
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, off));
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(warp_max[0], warp_max[1]), fmaxf(warp_max[2], warp_max[3]));
-    const float step = __fdiv_rn(m, 127.f);
-    const int code = finite && step > 0.f
-                         ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(s, step)), -127.f), 127.f)) : 0;
-    reinterpret_cast<int8_t*>(pos_codes)[threadIdx.x] = static_cast<int8_t>(max(code, 0));
-    reinterpret_cast<int8_t*>(neg_codes)[threadIdx.x] = static_cast<int8_t>(min(code, 0));
+    m = fmaxf(fmaxf(warp_max[0], warp_max[1]), fmaxf(warp_max[2], warp_max[3]));  // (four warps have the channels)
+    if (threadIdx.x < PG_D) {
+        const float step = __fdiv_rn(m, 127.f);
+        const int code = finite && step > 0.f
+                             ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(s, step)), -127.f), 127.f)) : 0;
+        reinterpret_cast<int8_t*>(pos_codes)[threadIdx.x] = static_cast<int8_t>(max(code, 0));
+        reinterpret_cast<int8_t*>(neg_codes)[threadIdx.x] = static_cast<int8_t>(min(code, 0));
+    }
     __syncthreads();
     const uint4 qp = *reinterpret_cast<const uint4*>(pos_codes + 4 * u), qn = *reinterpret_cast<const uint4*>(neg_codes + 4 * u);
 #pragma unroll
-    for (int j = 0; j < SCORE_AHEAD; ++j) {
-        int sum = __dp4a(static_cast<int>(rec[j][0].x), static_cast<int>(qp.x), 0);
-        sum = __dp4a(static_cast<int>(rec[j][0].y), static_cast<int>(qn.x), sum);
-        sum = __dp4a(static_cast<int>(rec[j][0].z), static_cast<int>(qp.y), sum);
-        sum = __dp4a(static_cast<int>(rec[j][0].w), static_cast<int>(qn.y), sum);
-        sum = __dp4a(static_cast<int>(rec[j][1].x), static_cast<int>(qp.z), sum);
-        sum = __dp4a(static_cast<int>(rec[j][1].y), static_cast<int>(qn.z), sum);
-        sum = __dp4a(static_cast<int>(rec[j][1].z), static_cast<int>(qp.w), sum);
-        sum = __dp4a(static_cast<int>(rec[j][1].w), static_cast<int>(qn.w), sum);
-        sum += __shfl_xor_sync(FULL_MASK, sum, 4);
-        sum += __shfl_xor_sync(FULL_MASK, sum, 2);
-        sum += __shfl_xor_sync(FULL_MASK, sum, 1);
-        const int col = first + j * (SCORE_THREADS / 8) + grp;
-        if (u == 0 && col < nb) {
-            const bool always = col < a.n_first || col >= nb - a.n_last || !pg_finite(scale[j]);
-            a.keys[static_cast<size_t>(blockIdx.y) * a.max_blocks + col] =
-                always ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale[j]);
+    for (int j0 = 0; j0 < 8; j0 += SCORE_AHEAD) {
+#pragma unroll
+        for (int j = 0; j < SCORE_AHEAD; ++j) {
+            int sum = __dp4a(static_cast<int>(rec[j][0].x), static_cast<int>(qp.x), 0);
+            sum = __dp4a(static_cast<int>(rec[j][0].y), static_cast<int>(qn.x), sum);
+            sum = __dp4a(static_cast<int>(rec[j][0].z), static_cast<int>(qp.y), sum);
+            sum = __dp4a(static_cast<int>(rec[j][0].w), static_cast<int>(qn.y), sum);
+            sum = __dp4a(static_cast<int>(rec[j][1].x), static_cast<int>(qp.z), sum);
+            sum = __dp4a(static_cast<int>(rec[j][1].y), static_cast<int>(qn.z), sum);
+            sum = __dp4a(static_cast<int>(rec[j][1].z), static_cast<int>(qp.w), sum);
+            sum = __dp4a(static_cast<int>(rec[j][1].w), static_cast<int>(qn.w), sum);
+            sum += __shfl_xor_sync(FULL_MASK, sum, 4);
+            sum += __shfl_xor_sync(FULL_MASK, sum, 2);
+            sum += __shfl_xor_sync(FULL_MASK, sum, 1);
+            const int col = first + (j0 + j) * SCORE_GROUPS + grp;
+            if (u == 0 && col < nb) {
+                const bool always = col < a.n_first || col >= nb - a.n_last || !pg_finite(scale[j]);
+                a.keys[static_cast<size_t>(blockIdx.y) * a.key_stride + col] =
+                    always ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale[j]);
+            }
         }
+        if (j0 + SCORE_AHEAD < 8) load(j0 + SCORE_AHEAD);
     }
-    if (bad && u == 0) report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
 }
 
 // ---------------------------------------------------------------- selection
 
-constexpr int PICK_THREADS = 512;
+constexpr int PICK_THREADS = 1024;
 constexpr int PICK_WARPS = PICK_THREADS / 32;
-constexpr int PICK_HELD = 16;  // keys a thread holds in registers; further ones are read again
+constexpr int PICK_HELD = 8;                             // neighbouring keys a thread takes in a round
+constexpr int PICK_ROUND = PICK_THREADS * PICK_HELD;     // columns of a round: 128K tokens
+constexpr int PICK_BITS = 11;                            // of a digit: 11, 11 and 10
+constexpr int PICK_BINS = 1 << PICK_BITS;
+
+// Sum of x over the threads before this one, and over all (in `total`).
+__device__ __forceinline__ int scan_threads(int x, int* warp_sum, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(FULL_MASK, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int w = warp_sum[lane];  // PICK_WARPS == 32
+    int all = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(FULL_MASK, all, off);
+        if (lane >= off) all += v;
+    }
+    total = __shfl_sync(FULL_MASK, all, 31);
+    const int before = __shfl_sync(FULL_MASK, all - w, warp);
+    __syncthreads();  // warp_sum may be written again
+    return before + incl - x;
+}
 
 // One CTA a (request, KV head).  The n_sel-th largest key is found digit by digit
-// (four of 8 bits): each pass counts the keys that agree with the digits found so
-// far by their next digit.  Then one pass in the order of the columns writes those
-// above it, and of the equal ones the first.
+// (three passes that count the keys that agree with the digits found so far by their next
+// one); then the keys above it, and of the equal ones the first, are written in the
+// order of the columns.  Up to 8192 columns stay in registers; latency bounds it.
 __global__ void __launch_bounds__(PICK_THREADS) block_pick_kernel(const SelectArgs a) {
-    __shared__ int hist[256];
-    __shared__ int found[2];           // digit, keys above it
-    __shared__ int2 warp_count[PICK_WARPS];
+    __shared__ int hist[PICK_BINS];
+    __shared__ int warp_sum[PICK_WARPS];
+    __shared__ int found[2];  // digit, keys above it
+    static_assert(PICK_WARPS == 32 && PICK_BINS == 2 * PICK_THREADS, "");
     pdl_launch_dependents();
     pdl_wait();
     const int r = blockIdx.x / a.Hkv;
     const int nb = max(select_blocks(a, r), 0);
     int32_t* sel = a.sel + static_cast<size_t>(blockIdx.x) * a.n_sel;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     if (nb <= a.n_sel) {
         for (int i = tid; i < a.n_sel; i += PICK_THREADS) sel[i] = i < nb ? i : -1;
         return;
     }
-    const uint32_t* keys = a.keys + static_cast<size_t>(blockIdx.x) * a.max_blocks;
-    uint32_t held[PICK_HELD];
+    const uint32_t* keys = a.keys + static_cast<size_t>(blockIdx.x) * a.key_stride;
+    uint32_t key[PICK_HELD];
+    const auto load = [&](int base) {  // this thread's keys of a round; a row of keys is padded to 8
 #pragma unroll
-    for (int j = 0; j < PICK_HELD; ++j) held[j] = tid + j * PICK_THREADS < nb ? keys[tid + j * PICK_THREADS] : 0u;
+        for (int j = 0; j < PICK_HELD; j += 4) {
+            const int i = base + tid * PICK_HELD + j;
+            const uint4 v = i < nb ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0u, 0u, 0u, 0u);
+            key[j] = v.x;
+            key[j + 1] = v.y;
+            key[j + 2] = v.z;
+            key[j + 3] = v.w;
+        }
+    };
+    const bool once = nb <= PICK_ROUND;
+    if (once) load(0);
     uint32_t prefix = 0u;
     int want = a.n_sel;  // how many of the keys that agree with the prefix are selected
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+#pragma unroll 1
+    for (int top = 32; top > 0; top -= PICK_BITS) {  // bits top - width .. top - 1
+        const int width = min(PICK_BITS, top), shift = top - width;
+        const uint32_t mask = (1u << width) - 1u;
+        hist[tid] = 0;
+        hist[tid + PICK_THREADS] = 0;
         __syncthreads();
-        const auto count = [&](uint32_t key) {
-            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
-        };
+#pragma unroll 1
+        for (int base = 0; base < nb; base += PICK_ROUND) {
+            if (!once) load(base);
 #pragma unroll
-        for (int j = 0; j < PICK_HELD; ++j)
-            if (tid + j * PICK_THREADS < nb) count(held[j]);
-        for (int i = tid + PICK_HELD * PICK_THREADS; i < nb; i += PICK_THREADS) count(keys[i]);
+            for (int j = 0; j < PICK_HELD; ++j)
+                if (base + tid * PICK_HELD + j < nb && (top == 32 || (key[j] >> top) == (prefix >> top)))
+                    atomicAdd(&hist[(key[j] >> shift) & mask], 1);
+        }
         __syncthreads();
-        if (warp == 0) {
-            // Lane l holds digits 255 - 8l .. 248 - 8l; a scan gives the keys above.
-            int c[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
-            int above = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int v = __shfl_up_sync(FULL_MASK, above, off);
-                if (lane >= off) above += v;
-            }
-            above -= sum;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (above < want && above + c[j] >= want) {
-                    found[0] = 255 - 8 * lane - j;
-                    found[1] = above;
-                }
-                above += c[j];
-            }
+        // Thread t has the bins 2047 - 2t and 2046 - 2t: the largest digits first.
+        const int hi = PICK_BINS - 1 - 2 * tid, n_hi = hist[hi], n_lo = hist[hi - 1];
+        int total;
+        const int above = scan_threads(n_hi + n_lo, warp_sum, total);
+        if (above < want && above + n_hi >= want) {
+            found[0] = hi;
+            found[1] = above;
+        } else if (above + n_hi < want && above + n_hi + n_lo >= want) {
+            found[0] = hi - 1;
+            found[1] = above + n_hi;
         }
         __syncthreads();
         prefix |= static_cast<uint32_t>(found[0]) << shift;
         want -= found[1];
     }
-    // Column order: thread t takes columns base + t of one round after another.
-    int above = 0, equal = 0;  // selected above, and equal keys, in earlier rounds
-    for (int base = 0; base < nb; base += PICK_THREADS) {
-        const int i = base + tid;
-        const uint32_t key = i < nb ? keys[i] : 0u;
-        const bool gt = i < nb && key > prefix, eq = i < nb && key == prefix;
-        const unsigned mg = __ballot_sync(FULL_MASK, gt), me = __ballot_sync(FULL_MASK, eq);
-        if (lane == 0) warp_count[warp] = make_int2(__popc(mg), __popc(me));
-        __syncthreads();
-        int g0 = above, e0 = equal, gt_all = 0, eq_all = 0;
+    int above = 0, equal = 0;  // keys above and equal ones in earlier rounds
+#pragma unroll 1
+    for (int base = 0; base < nb; base += PICK_ROUND) {
+        if (!once) load(base);
+        int n_gt = 0, n_eq = 0;
 #pragma unroll
-        for (int w = 0; w < PICK_WARPS; ++w) {
-            const int2 c = warp_count[w];
-            if (w < warp) {
-                g0 += c.x;
-                e0 += c.y;
-            }
-            gt_all += c.x;
-            eq_all += c.y;
+        for (int j = 0; j < PICK_HELD; ++j) {
+            const bool in = base + tid * PICK_HELD + j < nb;
+            n_gt += in && key[j] > prefix;
+            n_eq += in && key[j] == prefix;
         }
-        const unsigned before = (1u << lane) - 1u;
-        g0 += __popc(mg & before);
-        e0 += __popc(me & before);
-        if (gt || (eq && e0 < want)) sel[g0 + min(e0, want)] = i;
-        above += gt_all;
-        equal += eq_all;
-        __syncthreads();
+        // Both counts are below 2^14 in a round.
+        int total;
+        const int before = scan_threads(n_gt << 16 | n_eq, warp_sum, total);
+        int g0 = above + (before >> 16), e0 = equal + (before & 0xffff);
+#pragma unroll
+        for (int j = 0; j < PICK_HELD; ++j) {
+            const int i = base + tid * PICK_HELD + j;
+            if (i >= nb) break;
+            if (key[j] > prefix || (key[j] == prefix && e0 < want)) sel[g0 + min(e0, want)] = i;
+            g0 += key[j] > prefix;
+            e0 += key[j] == prefix;
+        }
+        above += total >> 16;
+        equal += total & 0xffff;
     }
 }
 
@@ -369,10 +421,12 @@ static bool select_sizes_ok(int B, int Hkv, int max_blocks) {
            static_cast<long long>(B) * Hkv <= 65535 && static_cast<long long>(B) * Hkv * max_blocks < (1ll << 31);
 }
 
+// Keys of a row, padded for 16-byte loads.
+static int key_stride(int max_blocks) { return (max_blocks + 7) / 8 * 8; }
+
 extern "C" size_t clo_paged_select_workspace_size(int B, int Hkv, int max_blocks) {
     if (!select_sizes_ok(B, Hkv, max_blocks)) return 0;
-    const size_t n = static_cast<size_t>(B) * Hkv * max_blocks * sizeof(uint32_t);
-    return n < 16 ? 16 : n;
+    return static_cast<size_t>(B) * Hkv * key_stride(max_blocks) * sizeof(uint32_t) + 16;
 }
 
 extern "C" clo_status clo_paged_block_select(const clo_paged_block_select_args* args, cudaStream_t stream) {
@@ -394,7 +448,7 @@ extern "C" clo_status clo_paged_block_select(const clo_paged_block_select_args* 
         !pg_aligned(r.workspace, 16))
         return CLO_ERR_WORKSPACE;
     const SelectArgs a{r.q, r.bounds, r.block_table, r.ctx_len, static_cast<uint32_t*>(r.workspace), r.sel, r.err_flag,
-                       r.Hq, r.Hkv, r.Hq / r.Hkv, r.num_blocks, r.max_blocks, r.n_sel, r.n_first, r.n_last};
+                       r.Hq, r.Hkv, r.Hq / r.Hkv, r.num_blocks, r.max_blocks, r.n_sel, r.n_first, r.n_last, key_stride(r.max_blocks)};
     const auto score = r.dtype == CLO_BF16 ? block_score_kernel<true> : block_score_kernel<false>;
     if (!prepare_kernel(reinterpret_cast<const void*>(score), 0) ||
         !prepare_kernel(reinterpret_cast<const void*>(block_pick_kernel), 0))
