@@ -12,6 +12,7 @@
 // dp4a for every four channels.
 #include <math.h>
 
+#include "clo_kv4_math.cuh"  // barriers and bulk copies
 #include "clo_paged.cuh"
 
 namespace clo {
@@ -130,9 +131,8 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) block_bounds_kernel(const Boun
 // ---------------------------------------------------------------- scores
 
 constexpr int SCORE_THREADS = 256;
-constexpr int SCORE_GROUPS = SCORE_THREADS / 8;                  // an 8-lane group a record
-constexpr int SCORE_AHEAD = 4;                                   // records a group keeps in flight
-constexpr int SCORE_BLOCKS = SCORE_GROUPS * 8;                   // columns a CTA scores: 8 a group
+constexpr int SCORE_COLS = SCORE_THREADS / 8;    // columns a CTA scores: 8 lanes a column
+constexpr int SCORE_HEADS = 8;                   // KV heads a CTA scores, at most
 constexpr uint32_t KEY_ALWAYS = 0xffffffffu;                     // above every score's key
 
 struct SelectArgs {
@@ -159,103 +159,111 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// 256 columns of one request and KV head a CTA.  HBM-bound (272 bytes a record): a group's
-// lane u looks up the block of its u-th column, all eight at once, and the records come
-// four at a time while the query's codes are made and then the ones before are summed up.
+// 32 columns of one request and up to 8 KV heads a CTA.  HBM-bound (272 bytes a record).  A
+// block's heads lie side by side: one bulk copy a column brings its records, all 32 at
+// once, while the queries' codes are made; then 8 lanes sum up a record.  Three CTAs share
+// an SM.  (Loads of 16 bytes a lane into registers had half the bandwidth: a record is not
+// a multiple of a sector, and the registers hold too few of them.)
 template <bool BF16>
-__global__ void __launch_bounds__(SCORE_THREADS, 4) block_score_kernel(const SelectArgs a) {
-    __shared__ float warp_max[SCORE_THREADS / 32];
-    __shared__ __align__(16) uint32_t pos_codes[PG_D / 4], neg_codes[PG_D / 4];
+__global__ void __launch_bounds__(SCORE_THREADS, 3) block_score_kernel(const SelectArgs a) {
+    extern __shared__ __align__(16) uint8_t records[];  // [SCORE_COLS][heads][PG_RECORD]
+    __shared__ __align__(16) uint32_t codes[SCORE_HEADS][2][PG_D / 4];  // positive, negative
+    __shared__ unsigned long long bar;
+    const uint32_t b = smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        mbar_init(b);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
-    const int r = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+    const int head_groups = (a.Hkv + SCORE_HEADS - 1) / SCORE_HEADS;
+    const int r = blockIdx.y / head_groups, g0 = blockIdx.y % head_groups * SCORE_HEADS;
+    const int heads = min(SCORE_HEADS, a.Hkv - g0), bytes = heads * PG_RECORD;
+    const int first = blockIdx.x * SCORE_COLS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = threadIdx.x & 7;
+    // (The table's entry and the length come together; an entry behind the length is not used.)
+    int id = -1;
+    if (warp == 0 && first + lane < a.max_blocks) id = a.table[static_cast<size_t>(r) * a.max_blocks + first + lane];
     const int nb = select_blocks(a, r);
-    const int first = blockIdx.x * SCORE_BLOCKS;
     if (nb < 0 && blockIdx.x == 0 && threadIdx.x == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
     if (nb <= a.n_sel || first >= nb) return;  // all blocks are selected: no scores
-
-    const int u = threadIdx.x & 7, grp = threadIdx.x >> 3;
-    // Column of the group's j-th record: neighbouring groups take neighbouring columns.
-    const int mine = first + u * SCORE_GROUPS + grp;
-    int id = 0;
-    if (mine < nb) {
-        id = a.table[static_cast<size_t>(r) * a.max_blocks + mine];
-        if (id < 0 || id >= a.num_blocks) {
+    if (warp == 0) {
+        const bool there = first + lane < nb, ok = there && id >= 0 && id < a.num_blocks;
+        const unsigned copies = __popc(__ballot_sync(FULL_MASK, ok));
+        if (lane == 0) mbar_expect(b, copies * bytes);
+        __syncwarp();
+        uint8_t* to = records + lane * bytes;
+        if (ok) {
+            bulk_load(smem_u32(to), a.bounds + (static_cast<size_t>(id) * a.Hkv + g0) * PG_RECORD, bytes, b, l2_evict_first_policy());
+        } else if (there) {  // a bad block is always selected
             report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
-            id = -1;
+            for (int h = 0; h < heads; ++h) *reinterpret_cast<float*>(to + h * PG_RECORD + 256) = INFINITY;
         }
     }
-    const int lane0 = threadIdx.x & 24;  // the group's first lane
-    uint4 rec[SCORE_AHEAD][2];
-    float scale[SCORE_AHEAD];
-    const auto load = [&](int j0) {
-#pragma unroll
-        for (int j = 0; j < SCORE_AHEAD; ++j) {
-            const int block = __shfl_sync(FULL_MASK, id, lane0 + j0 + j);
-            rec[j][0] = rec[j][1] = make_uint4(0u, 0u, 0u, 0u);
-            scale[j] = INFINITY;
-            if (block >= 0 && first + (j0 + j) * SCORE_GROUPS + grp < nb) {
-                const uint8_t* p = a.bounds + (static_cast<size_t>(block) * a.Hkv + g) * PG_RECORD;
-                rec[j][0] = *reinterpret_cast<const uint4*>(p + 32 * u);
-                rec[j][1] = *reinterpret_cast<const uint4*>(p + 32 * u + 16);
-                scale[j] = *reinterpret_cast<const float*>(p + 256);
-            }
-        }
-    };
-    load(0);
-    // The query's codes: thread c sums channel c over the group's heads, in order.
-    float s = 0.f;
-    if (threadIdx.x < PG_D) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) +
-                            (static_cast<size_t>(r) * a.Hq + static_cast<size_t>(g) * a.G) * PG_D + threadIdx.x;
-        uint16_t x[PG_MAX_G];
+    // The queries' codes: a warp a KV head, a lane four channels; the group's heads added up
+    // in order.
+    if (warp < heads) {
+        const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) +
+                                                        (static_cast<size_t>(r) * a.Hq + static_cast<size_t>(g0 + warp) * a.G) * PG_D) + lane;
+        uint2 w[PG_MAX_G];
 #pragma unroll
         for (int h = 0; h < PG_MAX_G; ++h)
-            if (h < a.G) x[h] = q[h * PG_D];
-        s = pg_unpack<BF16>(x[0]).x;
+            if (h < a.G) w[h] = q[h * (PG_D / 4)];
+        float s[4];
 #pragma unroll
-        for (int h = 1; h < PG_MAX_G; ++h)
-            if (h < a.G) s += pg_unpack<BF16>(x[h]).x;
-    }
-    float m = fabsf(s);
-    const bool finite = __syncthreads_and(pg_finite(s)) != 0;
+        for (int h = 0; h < PG_MAX_G; ++h)
+            if (h < a.G) {
+                const float2 x = pg_unpack<BF16>(w[h].x), y = pg_unpack<BF16>(w[h].y);
+                s[0] = h == 0 ? x.x : s[0] + x.x;
+                s[1] = h == 0 ? x.y : s[1] + x.y;
+                s[2] = h == 0 ? y.x : s[2] + y.x;
+                s[3] = h == 0 ? y.y : s[3] + y.y;
+            }
+        bool finite = pg_finite(s[0]) && pg_finite(s[1]) && pg_finite(s[2]) && pg_finite(s[3]);
+        finite = __all_sync(FULL_MASK, finite);
+        float m = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, off));
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(warp_max[0], warp_max[1]), fmaxf(warp_max[2], warp_max[3]));  // (four warps have the channels)
-    if (threadIdx.x < PG_D) {
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, off));
         const float step = __fdiv_rn(m, 127.f);
-        const int code = finite && step > 0.f
-                             ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(s, step)), -127.f), 127.f)) : 0;
-        reinterpret_cast<int8_t*>(pos_codes)[threadIdx.x] = static_cast<int8_t>(max(code, 0));
-        reinterpret_cast<int8_t*>(neg_codes)[threadIdx.x] = static_cast<int8_t>(min(code, 0));
-    }
-    __syncthreads();
-    const uint4 qp = *reinterpret_cast<const uint4*>(pos_codes + 4 * u), qn = *reinterpret_cast<const uint4*>(neg_codes + 4 * u);
+        uint32_t pos = 0u, neg = 0u;
+        if (finite && step > 0.f) {
 #pragma unroll
-    for (int j0 = 0; j0 < 8; j0 += SCORE_AHEAD) {
-#pragma unroll
-        for (int j = 0; j < SCORE_AHEAD; ++j) {
-            int sum = __dp4a(static_cast<int>(rec[j][0].x), static_cast<int>(qp.x), 0);
-            sum = __dp4a(static_cast<int>(rec[j][0].y), static_cast<int>(qn.x), sum);
-            sum = __dp4a(static_cast<int>(rec[j][0].z), static_cast<int>(qp.y), sum);
-            sum = __dp4a(static_cast<int>(rec[j][0].w), static_cast<int>(qn.y), sum);
-            sum = __dp4a(static_cast<int>(rec[j][1].x), static_cast<int>(qp.z), sum);
-            sum = __dp4a(static_cast<int>(rec[j][1].y), static_cast<int>(qn.z), sum);
-            sum = __dp4a(static_cast<int>(rec[j][1].z), static_cast<int>(qp.w), sum);
-            sum = __dp4a(static_cast<int>(rec[j][1].w), static_cast<int>(qn.w), sum);
-            sum += __shfl_xor_sync(FULL_MASK, sum, 4);
-            sum += __shfl_xor_sync(FULL_MASK, sum, 2);
-            sum += __shfl_xor_sync(FULL_MASK, sum, 1);
-            const int col = first + (j0 + j) * SCORE_GROUPS + grp;
-            if (u == 0 && col < nb) {
-                const bool always = col < a.n_first || col >= nb - a.n_last || !pg_finite(scale[j]);
-                a.keys[static_cast<size_t>(blockIdx.y) * a.key_stride + col] =
-                    always ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale[j]);
+            for (int c = 0; c < 4; ++c) {
+                const int code = static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(s[c], step)), -127.f), 127.f));
+                pos |= static_cast<uint32_t>(max(code, 0)) << (8 * c);
+                neg |= (static_cast<uint32_t>(min(code, 0)) & 0xffu) << (8 * c);
             }
         }
-        if (j0 + SCORE_AHEAD < 8) load(j0 + SCORE_AHEAD);
+        codes[warp][0][lane] = pos;
+        codes[warp][1][lane] = neg;
+    }
+    __syncthreads();
+    if (!mbar_wait(b, 0) && lane == 0) report_error(a.err_flag, CLO_FLAG_TIMEOUT);
+    const int col = first + (threadIdx.x >> 3);
+    const uint8_t* rec = records + (threadIdx.x >> 3) * bytes;
+#pragma unroll 2
+    for (int h = 0; h < heads; ++h, rec += PG_RECORD) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // channels 8u .. 8u + 7, then 64 + 8u ..
+            const uint4 x = *reinterpret_cast<const uint4*>(rec + 128 * i + 16 * u);
+            const uint2 qp = *reinterpret_cast<const uint2*>(&codes[h][0][16 * i + 2 * u]);
+            const uint2 qn = *reinterpret_cast<const uint2*>(&codes[h][1][16 * i + 2 * u]);
+            sum = __dp4a(static_cast<int>(x.x), static_cast<int>(qp.x), sum);
+            sum = __dp4a(static_cast<int>(x.y), static_cast<int>(qn.x), sum);
+            sum = __dp4a(static_cast<int>(x.z), static_cast<int>(qp.y), sum);
+            sum = __dp4a(static_cast<int>(x.w), static_cast<int>(qn.y), sum);
+        }
+        sum += __shfl_xor_sync(FULL_MASK, sum, 4);
+        sum += __shfl_xor_sync(FULL_MASK, sum, 2);
+        sum += __shfl_xor_sync(FULL_MASK, sum, 1);
+        if (u == 0 && col < nb) {
+            const float scale = *reinterpret_cast<const float*>(rec + 256);
+            const bool always = col < a.n_first || col >= nb - a.n_last || !pg_finite(scale);
+            a.keys[(static_cast<size_t>(r) * a.Hkv + g0 + h) * a.key_stride + col] =
+                always ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale);
+        }
     }
 }
 
@@ -450,11 +458,14 @@ extern "C" clo_status clo_paged_block_select(const clo_paged_block_select_args* 
     const SelectArgs a{r.q, r.bounds, r.block_table, r.ctx_len, static_cast<uint32_t*>(r.workspace), r.sel, r.err_flag,
                        r.Hq, r.Hkv, r.Hq / r.Hkv, r.num_blocks, r.max_blocks, r.n_sel, r.n_first, r.n_last, key_stride(r.max_blocks)};
     const auto score = r.dtype == CLO_BF16 ? block_score_kernel<true> : block_score_kernel<false>;
-    if (!prepare_kernel(reinterpret_cast<const void*>(score), 0) ||
+    const int smem = SCORE_COLS * min(r.Hkv, SCORE_HEADS) * PG_RECORD;
+    if (!prepare_kernel(reinterpret_cast<const void*>(score), smem) ||
         !prepare_kernel(reinterpret_cast<const void*>(block_pick_kernel), 0))
         return CLO_ERR_CUDA;
     const unsigned sets = static_cast<unsigned>(r.B) * r.Hkv;
-    if (launch_pdl(score, dim3((r.max_blocks + SCORE_BLOCKS - 1) / SCORE_BLOCKS, sets), dim3(SCORE_THREADS), 0, stream, a) !=
+    const unsigned head_groups = static_cast<unsigned>(r.Hkv + SCORE_HEADS - 1) / SCORE_HEADS;
+    if (launch_pdl(score, dim3((r.max_blocks + SCORE_COLS - 1) / SCORE_COLS, r.B * head_groups), dim3(SCORE_THREADS), smem,
+                   stream, a) !=
         cudaSuccess)
         return CLO_ERR_CUDA;
     return launch_pdl(block_pick_kernel, dim3(sets), dim3(PICK_THREADS), 0, stream, a) == cudaSuccess ? CLO_OK : CLO_ERR_CUDA;
