@@ -341,17 +341,33 @@ struct Loader {
     __device__ bool piece(const Piece& p, int slot) {
         const int n = p.hi - p.lo, ahead = p.two(a) ? 1 : 2;
         const int sees = SPARSE ? p.q.ctx : p.sees, last = paged_places<SPARSE>(a, sees);
-        const auto fetch = [&](int group) {
+        // Places of four tiles a register: of the group that K is in, the one before, and on
+        // their way the next one's blocks and (sparse) the columns of the one after that.
+        const int nb = (sees + PG_BLOCK - 1) / PG_BLOCK;
+        const auto column = [&](int group) {
             const int x = group * 32 + lane;
-            return x < last ? paged_place<SPARSE>(a, p.r, p.h, sees, x) : 0;
+            if constexpr (SPARSE) return x < last ? a.sel[(static_cast<size_t>(p.r) * a.Hkv + p.h) * a.n_sel + x] : -1;
+            else return x < last ? x : -1;
         };
-        // Places of four tiles a register: the group that K is in, the one before, the next.
-        int group = p.lo >> 2, cur = fetch(group), prev = 0, next = fetch(group + 1);
+        const auto block = [&](int col) {
+            return col >= 0 && col < nb ? a.table[static_cast<size_t>(p.r) * a.max_blocks + col] : -1;
+        };
+        const auto pack = [&](int col, int id) {
+            const bool bad = col < -1 || col >= nb || (col >= 0 && (id < 0 || id >= a.num_blocks));
+            return bad ? -1 : col < 0 ? 0 : id * 32 + min(sees - col * PG_BLOCK, PG_BLOCK);
+        };
+        int group = p.lo >> 2;
+        int cur_col = column(group), next_col = column(group + 1), after_col = column(group + 2);
+        int cur_id = block(cur_col), next_id = block(next_col);
+        int cur = pack(cur_col, cur_id), prev = 0;
         const auto k_tile = [&](int t) {
             if ((t >> 2) != group) {
+                ++group;
                 prev = cur;
-                cur = next;
-                next = fetch(++group + 1);
+                cur = pack(next_col, next_id);
+                next_col = after_col;
+                next_id = block(next_col);
+                after_col = column(group + 2);
             }
             return tile(p, false, t, cur, slot);
         };
@@ -646,17 +662,20 @@ struct RowSoftmax {
         // Rows past the item's (their results are not used) see everything.
         const int sees = SPARSE || !valid ? 0x7fffffff : paged_sees<false>(p.q, token);
         const int places = SPARSE ? paged_places<true>(a, p.q.ctx) : 0;
-        const auto place_rows = [&](int t) {  // sparse: lanes 0 .. 7, the tokens of each place
+        const int nb = (p.q.ctx + PG_BLOCK - 1) / PG_BLOCK;
+        const auto column = [&](int t) {  // sparse: lanes 0 .. 7, the column of each place
             const int x = t * CH_PLACES + (lane & 7);
-            return x < places ? max(paged_place<true>(a, p.r, p.h, p.q.ctx, x), 0) & 31 : 0;
+            return x < places ? a.sel[(static_cast<size_t>(p.r) * a.Hkv + p.h) * a.n_sel + x] : -1;
         };
         const bool idle = !__any_sync(FULL_MASK, valid);
         float ref = -INFINITY, sum = 0.f;
         const int step = two ? 1 : 2, t0 = p.lo + (two ? 0 : s);
-        int rows_next = SPARSE && t0 < p.hi ? place_rows(t0) : 0;
+        int next_col = SPARSE && t0 < p.hi ? column(t0) : 0;
         for (int t = t0; t < p.hi; t += step) {
-            const int rows_here = rows_next;
-            if (SPARSE && t + step < p.hi) rows_next = place_rows(t + step);
+            // (The next tile's columns are on their way; nothing waits for them here.)
+            const int col = next_col;
+            if (SPARSE && t + step < p.hi) next_col = column(t + step);
+            const int rows_here = col >= 0 && col < nb ? min(p.q.ctx - col * PG_BLOCK, PG_BLOCK) : 0;
             const int seen = sees - t * CH_TILE;
             const bool masked = SPARSE ? __any_sync(FULL_MASK, rows_here != PG_BLOCK) : __any_sync(FULL_MASK, seen < CH_TILE);
             if (!ch_warp_wait(sm->s_full[s], s_count++ & 1, sm)) return false;
