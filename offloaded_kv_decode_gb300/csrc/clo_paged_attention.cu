@@ -15,7 +15,7 @@
 // and both go over every tile of tokens, so the tensor cores work on one stream's
 // products while the other's weights are made.  An item of one tile gives the
 // streams alternate tiles of tokens, and their sums are added up at its end.  A row belongs to one thread: no shuffles.  Besides:
-//   warp 8   brings K and V tiles into a ring of five (16 tokens a copy, whatever the
+//   warp 8   brings K and V tiles into a ring of five (a copy a block, whatever the
 //            cache's strides), in the order in which the products take them;
 //   warp 9   issues the products: S = Q K^T, both from shared memory, and O += P V with
 //            P from tensor memory, where it takes the place of S;
@@ -51,6 +51,7 @@ constexpr int CH_REGS = 168;                      // a thread at launch: 65536 /
 constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
 constexpr int CH_FIXED = 256;                     // what an item costs beside its tokens, in tokens
+constexpr int CH_ONE = 16;                         // a token of an item of one tile of rows, in 16ths of one of two
 constexpr int CH_LEAST = 384;                     // weight that is worth a CTA of its own
 constexpr int CH_JOIN = 512;                      // what cutting an item costs (partial results, the join), in tokens
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
@@ -123,7 +124,9 @@ __device__ __forceinline__ Weights weights_of(const PagedAttnArgs& a, const Page
     w.items = items_of(a, q);
     const int base = SPARSE ? 0 : max(q.ctx - q.n, 0);
     w.each = max((base + CH_FIXED) >> a.shift, 1);
-    w.last = max(((SPARSE ? item_sees<true>(a, q, 0) : base + q.n) + CH_FIXED) >> a.shift, 1);
+    const int seen = SPARSE ? item_sees<true>(a, q, 0) : base + q.n;
+    const bool one = q.n - (w.items - 1) * 2 * a.tt <= a.tt;
+    w.last = max(((one ? seen / 16 * CH_ONE : seen) + CH_FIXED) >> a.shift, 1);
     return w;
 }
 
@@ -323,7 +326,8 @@ struct Loader {
                     const int row = (lane >> 4) + 2 * k, c = lane & 15;
                     const uint4 x = row < brows ? *reinterpret_cast<const uint4*>(a.vc + base + row * a.kv_token + c * 16)
                                                 : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t to = dst + (c >> 3) * CH_HALF + (b * PG_BLOCK + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    const uint32_t to = dst + b * PG_BLOCK_BYTES + (row >> 3) * 2048 + (c >> 3) * 1024 + (row & 7) * 128 +
+                                        (((c & 7) ^ (row & 7)) << 4);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                                  : "memory");
                 }
@@ -333,8 +337,8 @@ struct Loader {
         }
         if (lane == 0) mbar_expect(bar, __popc(copied) * PG_BLOCK_BYTES);
         __syncwarp();
-        if (lane < 16 && copy)
-            tma_load_5d(dst + (lane >> 3) * CH_HALF + (lane & 7) * (PG_BLOCK * 128), is_v ? mv : mk, bar, 0, lane >> 3, 0, p.h, id);
+        if (lane < CH_PLACES && copy)
+            tma_load_5d(dst + lane * PG_BLOCK_BYTES, is_v ? mv : mk, bar, 0, 0, 0, 0, static_cast<int>(id * a.unit_block + p.h * a.unit_head));
         return true;
     }
 
@@ -399,23 +403,23 @@ struct Issuer {
     __device__ void release(int x) { tc_commit(smem_u32(&sm->empty[x % CH_STAGES])); }
     // S of stream s = Q of row tile qt times K of tile x.
     __device__ void scores(int s, int qt, int x) {
-        const uint64_t k = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, 16), qa = tc_tile(q + qt * CH_TILE_BYTES, 16);
+        const uint64_t k = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, 16, 2048), qa = tc_tile(q + qt * CH_TILE_BYTES, 16, 1024);
         const uint32_t d = tmem + s * CH_TILE;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t off = ((i >> 2) * CH_HALF + (i & 3) * 32) >> 4;
-            tc_mma(d, tc_ahead(qa, off), tc_ahead(k, off), tc_shape(BF16, CH_TILE, CH_TILE, false), i > 0);
+            const uint32_t off = (i & 3) * 32;
+            tc_mma(d, tc_ahead(qa, ((i >> 2) * CH_HALF + off) >> 4), tc_ahead(k, ((i >> 2) * 1024 + off) >> 4), tc_shape(BF16, CH_TILE, CH_TILE, false), i > 0);
         }
         tc_commit(smem_u32(&sm->s_full[s]));
     }
     // O of stream s (+)= its weights times V of tile x.
     __device__ void sums(int s, int x, bool add) {
-        const uint64_t v = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, CH_HALF);
+        const uint64_t v = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, 1024, 2048);
         const uint32_t d = tmem + (2 + s) * CH_TILE, w = tmem + s * CH_TILE;
         tc_mma_ts(d, w, v, tc_shape(BF16, CH_TILE, CH_TILE, true), add);
 #pragma unroll
         for (int i = 1; i < 8; ++i)
-            tc_mma_ts(d, w + 8 * i, tc_ahead(v, i * 2048 >> 4), tc_shape(BF16, CH_TILE, CH_TILE, true), true);
+            tc_mma_ts(d, w + 8 * i, tc_ahead(v, i * PG_BLOCK_BYTES >> 4), tc_shape(BF16, CH_TILE, CH_TILE, true), true);
     }
     __device__ bool weights(int s) {
         const uint32_t count = s == 0 ? p_count0++ : p_count1++;
@@ -1137,14 +1141,19 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
 
 // ---------------------------------------------------------------- host
 
-// The cache as copies of 16 tokens x 64 channels, 128-byte-swizzled.
-static bool make_map(CUtensorMap* map, const PagedAttnArgs& a, const uint8_t* x, bool bf16) {
+// The cache as copies of a block and head, 4 KB, into units of 8 tokens x 64 channels
+// (128-byte-swizzled): those of channels 0 .. 63 and 64 .. 127 of tokens 0 .. 7, then of
+// tokens 8 .. 15.  So 8-token groups of either half lie 2048 bytes apart throughout a
+// tile, as the products want them, with one copy a block: with a copy for each half (2 KB)
+// the copies alone took 1.5 us a tile of K and V.  Blocks and heads share the fifth dimension, in
+// units of what divides both strides.
+static bool make_map(CUtensorMap* map, const PagedAttnArgs& a, const uint8_t* x, bool bf16, long long unit, long long units) {
     const TensorMapEncode encode = tensor_map_encode();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[5] = {64, 2, PG_BLOCK, static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.num_blocks)};
-    const cuuint64_t strides[4] = {128, static_cast<cuuint64_t>(a.kv_token), static_cast<cuuint64_t>(a.kv_head),
-                                   static_cast<cuuint64_t>(a.kv_block)};
-    const cuuint32_t box[5] = {64, 1, PG_BLOCK, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+    const cuuint64_t dims[5] = {64, 8, 2, 2, static_cast<cuuint64_t>(units)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(a.kv_token), 128, static_cast<cuuint64_t>(8 * a.kv_token),
+                                   static_cast<cuuint64_t>(unit)};
+    const cuuint32_t box[5] = {64, 8, 2, 2, 1}, one[5] = {1, 1, 1, 1, 1};
     return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                   const_cast<uint8_t*>(x), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1183,8 +1192,19 @@ static clo_status run_paged(PagedAttnArgs a, void* workspace, const clo_attn_opt
         !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
         return CLO_ERR_CUDA;
     const int ctas = opts != nullptr && opts->num_ctas > 0 ? opts->num_ctas : device_sm_count();
+    long long unit = a.kv_block, rest = a.kv_head;
+    while (rest != 0) {
+        const long long x = unit % rest;
+        unit = rest;
+        rest = x;
+    }
+    a.unit_block = a.kv_block / unit;
+    a.unit_head = a.kv_head / unit;
+    const long long units = (a.num_blocks - 1) * a.unit_block + (a.Hkv - 1) * a.unit_head + 1;
+    if (units >= (1ll << 31)) return CLO_ERR_UNSUPPORTED;
     CUtensorMap map_q, map_k, map_v;
-    if (ctas <= 0 || !make_query_map(&map_q, a, BF16) || !make_map(&map_k, a, a.kc, BF16) || !make_map(&map_v, a, a.vc, BF16))
+    if (ctas <= 0 || !make_query_map(&map_q, a, BF16) || !make_map(&map_k, a, a.kc, BF16, unit, units) ||
+        !make_map(&map_v, a, a.vc, BF16, unit, units))
         return CLO_ERR_CUDA;
     ChunkWs ws;
     ws.o = static_cast<float4*>(workspace);

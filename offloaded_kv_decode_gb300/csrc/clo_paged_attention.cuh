@@ -19,6 +19,7 @@ struct PagedAttnArgs {
     const int32_t* sel;      // sparse: [B][Hkv][n_sel] columns of the table
     int32_t* err_flag;
     long long q_stride, kv_block, kv_head, kv_token;  // bytes
+    long long unit_block, unit_head;  // kv_block and kv_head in units of their greatest common divisor
     float scale_log2;
     int B, N, Hq, Hkv, G, num_blocks, max_blocks, n_sel;
     int tt, shift;  // tokens of a tile of rows; unit of weights (clo_paged_attention.cu)

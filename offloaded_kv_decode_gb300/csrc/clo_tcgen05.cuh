@@ -53,12 +53,13 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&w)[
 
 // ---------------------------------------------------------------- products
 
-// A tile of rows of 128 bytes with the 128-byte swizzle, at a 1024-byte boundary:
-// 8 rows are 1024 bytes.  `next` is the distance of the next 64 elements along
-// the rows of an operand whose rows run along M or N (unused if they run along K).
-__device__ __forceinline__ uint64_t tc_tile(uint32_t addr, uint32_t next) {
+// A tile of rows of 128 bytes with the 128-byte swizzle: units of 8 rows, 1024 bytes at
+// a 1024-byte boundary, `group` bytes apart.  `next` is the distance of the next 64
+// elements along the rows of an operand whose rows run along M or N (unused if they
+// run along K).
+__device__ __forceinline__ uint64_t tc_tile(uint32_t addr, uint32_t next, uint32_t group) {
     return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(next >> 4) << 16) |
-           (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+           (static_cast<uint64_t>(group >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
 // The tile `units` of 16 bytes further on (within shared memory: no carry).
