@@ -51,7 +51,7 @@ constexpr int CH_REGS = 168;                      // a thread at launch: 65536 /
 constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
 constexpr int CH_FIXED = 256;                     // what an item costs beside its tokens, in tokens
-constexpr int CH_ONE = 16;                         // a token of an item of one tile of rows, in 16ths of one of two
+constexpr int CH_ONE = 12;                         // a token of an item of one tile of rows, in 16ths of one of two
 constexpr int CH_LEAST = 384;                     // weight that is worth a CTA of its own
 constexpr int CH_JOIN = 512;                      // what cutting an item costs (partial results, the join), in tokens
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
