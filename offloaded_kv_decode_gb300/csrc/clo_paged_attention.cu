@@ -19,7 +19,8 @@
 //            cache's strides), in the order in which the products take them;
 //   warp 9   issues the products: S = Q K^T, both from shared memory, and O += P V with
 //            P from tensor memory, where it takes the place of S;
-//   warp 10  brings the rows of q.
+//   warp 10  brings the rows of q;
+//   warp 11  tells the others their pieces of work, ahead of time.
 // Softmax: with a reference that lies 2^6 below a maximum seen so far and moves only when
 // a score passes it by 2^14, weights up to 2^14 fit fp16 and those down to 2^-31 of
 // the largest still count, and sums in tensor memory are seldom rescaled.
@@ -57,6 +58,7 @@ constexpr int CH_JOIN = 512;                      // what cutting an item costs 
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
 constexpr int CH_SMALL = 2048;                    // shared memory beside the tiles
 constexpr int CH_SMEM = CHUNK_ROWS * PG_ROW + CH_STAGES * CH_TILE_BYTES + CH_SMALL + 1024;
+constexpr int CH_PIECES = 4;                      // pieces told ahead
 constexpr int MERGE_THREADS = 256;
 
 // Where a range starts or ends: tile `cut` of item (request, KV head, item).
@@ -75,8 +77,10 @@ struct ChunkWs {
 enum { DESC_START, DESC_END, DESC_FLAGS, DESC_TAIL };
 
 struct alignas(16) ChunkSmall {
+    unsigned long long told[CH_PIECES], heard[CH_PIECES];
     unsigned long long full[CH_STAGES], empty[CH_STAGES], q_full, q_empty, s_full[2], p_ready[2], o_full[2], x_full, x_empty, drain;
     ChunkPos start, end;
+    int4 piece[CH_PIECES][3];
     PagedReq first;  // the request that the share starts in
     int4 tail;       // DESC_TAIL
     uint32_t tmem;
@@ -288,6 +292,50 @@ template <int R>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R)); }
+
+// ---------------------------------------------------------------- pieces of work
+
+// The pieces of a CTA, as warp 11 tells them: each role takes them in turn.
+struct Pieces {
+    ChunkSmall* sm;
+    int it = 0;
+    // For a whole warp (lane) or for one thread of it (lane = -1).
+    __device__ __forceinline__ bool next(Piece& p, int lane) {
+        const int slot = it % CH_PIECES;
+        const uint32_t parity = it / CH_PIECES & 1;
+        ++it;
+        if (lane < 0 ? !ch_wait(sm->told[slot], parity, sm) : !ch_warp_wait(sm->told[slot], parity, sm)) return false;
+        const int4 x = sm->piece[slot][0], y = sm->piece[slot][1], z = sm->piece[slot][2];
+        p.q = PagedReq{x.x, x.y, x.z, false};
+        p.r = x.w;
+        p.h = y.x;
+        p.j = y.y;
+        p.lo = y.z;
+        p.hi = y.w;
+        p.tiles = z.x;
+        p.tokens = z.y;
+        p.sees = z.z;
+        if (lane >= 0) __syncwarp();
+        if (lane <= 0) mbar_arrive(smem_u32(&sm->heard[slot]));
+        return p.tokens > 0;  // else that was the end
+    }
+};
+
+template <bool SPARSE>
+__device__ __forceinline__ void tell_pieces(const PagedAttnArgs& a, ChunkSmall* sm, Walk<SPARSE>& walk) {  // one thread
+    for (int it = 0;; ++it) {
+        const int slot = it % CH_PIECES;
+        Piece p;
+        const bool more = walk.next(a, p);
+        if (!more) p.tokens = 0;
+        if (!ch_wait(sm->heard[slot], (it / CH_PIECES & 1) ^ 1, sm)) return;
+        sm->piece[slot][0] = make_int4(p.q.row0, p.q.n, p.q.ctx, p.r);
+        sm->piece[slot][1] = make_int4(p.h, p.j, p.lo, p.hi);
+        sm->piece[slot][2] = make_int4(p.tiles, p.tokens, p.sees, 0);
+        mbar_arrive(smem_u32(&sm->told[slot]));
+        if (!more) return;
+    }
+}
 
 // ---------------------------------------------------------------- the copying warp
 
@@ -613,12 +661,18 @@ struct RowSoftmax {
             load(o, c);
             if (whole) {
                 uint32_t w[16];
+                float2 sink = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float x = none ? 0.f : o[2 * i] * inv, y = none ? 0.f : o[2 * i + 1] * inv;
-                    odd = fmaf(x, 0.f, odd);
-                    odd = fmaf(y, 0.f, odd);
-                    w[i] = pg_pack_out<BF16>(x, y);
+                    const float2 x = mul2(make_float2(o[2 * i], o[2 * i + 1]), make_float2(inv, inv));
+                    sink = fma2(x, make_float2(0.f, 0.f), sink);
+                    w[i] = none ? 0u : kv4_pack2_finite<BF16>(x.x, x.y);  // (see pg_pack_out)
+                }
+                sink.x += sink.y;
+                if (!none && sink.x != 0.f) {  // something is not finite
+                    odd = sink.x;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pg_pack_out<BF16>(o[2 * i] * inv, o[2 * i + 1] * inv);
                 }
                 if (valid) {  // whole sectors: a thread's row lies apart from its neighbours'
                     uint8_t* dst = a.out + place * PG_ROW + c * 64;
@@ -755,6 +809,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         for (int i = 0; i < CH_STAGES; ++i) {
             mbar_init_n(smem_u32(&sm->full[i]), 1);
             mbar_init_n(smem_u32(&sm->empty[i]), 1);
+        }
+        for (int i = 0; i < CH_PIECES; ++i) {
+            mbar_init_n(smem_u32(&sm->told[i]), 1);
+            mbar_init_n(smem_u32(&sm->heard[i]), 11);  // eight warps, copies, products, queries
         }
         mbar_init_n(smem_u32(&sm->q_full), 1);
         mbar_init_n(smem_u32(&sm->q_empty), 1);
@@ -907,14 +965,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     tc_fence_after();
     const ChunkPos start = sm->start, end = sm->end;
     const uint32_t tmem = sm->tmem;
-    Walk<SPARSE> walk(a, start, end, sm->first);
+    Pieces pieces{sm};
     Piece p;
 
     if (warp < 8) {
         regs_up<CH_REGS_SOFTMAX>();
         RowSoftmax<BF16, SPARSE> w{a, ws, sm, warp >> 2, static_cast<int>(threadIdx.x) & 127,
                                 tmem + (static_cast<uint32_t>(warp & 3) << 21)};
-        while (walk.next(a, p))
+        while (pieces.next(p, lane))
             if (!w.piece(p)) break;
     } else {
         regs_down<CH_REGS_REST>();
@@ -922,7 +980,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             Loader<SPARSE> w{a, &map_k, &map_v, sm, smem_u32(ring), lane};
             int head = 0, tail = 0, count = 0;
             bool ok = true;
-            while (ok && walk.next(a, p)) {
+            while (ok && pieces.next(p, lane)) {
                 if (p.lo > 0) head = 1;
                 else if (p.hi < p.tiles) tail = 1;
                 if (p.hi == p.lo) continue;
@@ -944,7 +1002,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             if (lane == 0) {
                 Issuer<BF16> w{sm, smem_u32(base), smem_u32(ring), tmem, a.tt};
                 bool ok = true;
-                while (ok && walk.next(a, p))
+                while (ok && pieces.next(p, -1))
                     if (p.hi > p.lo) ok = w.piece(p);
                 if (!ok) {  // products in flight end before tensor memory is given up
                     tc_commit(smem_u32(&sm->drain));
@@ -955,7 +1013,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         } else if (warp == 10 && lane == 0) {
             uint32_t count = 0;
             bool ok = true;
-            while (ok && walk.next(a, p)) {
+            while (ok && pieces.next(p, -1)) {
                 if (p.hi == p.lo) continue;
                 ok = ch_wait(sm->q_empty, (count & 1) ^ 1, sm);
                 if (!ok) break;
@@ -969,6 +1027,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                                     p.h * a.G, p.q.row0 + (2 * p.j + t) * a.tt);
             }
             if (!ok && count > 0) mbar_wait(smem_u32(&sm->q_full), (count - 1) & 1);
+        } else if (warp == 11 && lane == 0) {
+            Walk<SPARSE> walk(a, start, end, sm->first);
+            tell_pieces<SPARSE>(a, sm, walk);
         }
     }
     tc_fence_before();
