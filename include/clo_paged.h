@@ -150,7 +150,9 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  * with V, in fp16 after a factor that keeps what is 2^-31 of the largest.  The same
  * call on the same kind of GPU gives the same bits each time.
  * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, N * Hq < 2^29,
- * max_blocks <= 2^20, num_blocks <= 2^26, scale > 0.
+ * max_blocks <= 2^20, num_blocks <= 2^26, scale > 0, strides of at most 2^38 (kv_token
+ * 2^34) and a cache that spans less than 2^31 times the greatest common divisor of
+ * kv_block and kv_head.
  */
 typedef struct clo_paged_chunk_attn_args {
     const void* q;

@@ -47,6 +47,7 @@ constexpr int CH_HALF = CH_TILE * 128;            // bytes of 64 channels of a t
 constexpr int CH_TILE_BYTES = 2 * CH_HALF;
 constexpr int CH_STAGES = 5;
 constexpr int CHUNK_ROWS = 2 * CH_TILE;           // rows of an item, at most
+constexpr int CH_ROLES = 8;                       // warps of the softmax; behind them: copies, products, queries, pieces
 constexpr int CH_THREADS = 384;
 constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
 constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
@@ -86,6 +87,7 @@ struct alignas(16) ChunkSmall {
     uint32_t tmem;
     int dead;      // a wait ran out
     int again;     // a complete item has a result that is not finite
+    int copied, asked;  // tiles and queries whose copies were issued
     int bad[8];    // by item: a place that could not be read
     float2 ml1[CH_TILE];  // stream 1's reference and denominator, for items with one tile of rows
 };
@@ -824,11 +826,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         mbar_init_n(smem_u32(&sm->x_full), 4);
         mbar_init_n(smem_u32(&sm->x_empty), 4);
         mbar_init_n(smem_u32(&sm->drain), 1);
-        sm->dead = sm->again = 0;
+        sm->dead = sm->again = sm->copied = sm->asked = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(smem_u32(&sm->tmem), 4 * CH_TILE);
-    if (threadIdx.x == 320) {
+    if (warp == CH_ROLES + 1) tmem_alloc(smem_u32(&sm->tmem), 4 * CH_TILE);
+    if (threadIdx.x == (CH_ROLES + 2) * 32) {
         tma_prefetch(&map_q);
         tma_prefetch(&map_k);
         tma_prefetch(&map_v);
@@ -968,7 +970,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     Pieces pieces{sm};
     Piece p;
 
-    if (warp < 8) {
+    if (warp < CH_ROLES) {
         regs_up<CH_REGS_SOFTMAX>();
         RowSoftmax<BF16, SPARSE> w{a, ws, sm, warp >> 2, static_cast<int>(threadIdx.x) & 127,
                                 tmem + (static_cast<uint32_t>(warp & 3) << 21)};
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             if (!w.piece(p)) break;
     } else {
         regs_down<CH_REGS_REST>();
-        if (warp == 8) {
+        if (warp == CH_ROLES) {
             Loader<SPARSE> w{a, &map_k, &map_v, sm, smem_u32(ring), lane};
             int head = 0, tail = 0, count = 0;
             bool ok = true;
@@ -995,22 +997,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 d[DESC_FLAGS] = make_int4(head, tail, 0, 0);
                 d[DESC_TAIL] = sm->tail;
             }
-            if (!ok)  // copies in flight land before the memory is given up
-                for (int x = max(w.it - CH_STAGES, 0); x < w.it; ++x)
-                    mbar_wait(smem_u32(&sm->full[x % CH_STAGES]), x / CH_STAGES & 1);
-        } else if (warp == 9) {
+            if (lane == 0) sm->copied = w.it;
+        } else if (warp == CH_ROLES + 1) {
             if (lane == 0) {
                 Issuer<BF16> w{sm, smem_u32(base), smem_u32(ring), tmem, a.tt};
                 bool ok = true;
                 while (ok && pieces.next(p, -1))
                     if (p.hi > p.lo) ok = w.piece(p);
-                if (!ok) {  // products in flight end before tensor memory is given up
-                    tc_commit(smem_u32(&sm->drain));
-                    mbar_wait(smem_u32(&sm->drain), 0);
-                }
             }
             __syncwarp();
-        } else if (warp == 10 && lane == 0) {
+        } else if (warp == CH_ROLES + 2 && lane == 0) {
             uint32_t count = 0;
             bool ok = true;
             while (ok && pieces.next(p, -1)) {
@@ -1026,19 +1022,30 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                         tma_load_4d(smem_u32(base) + t * CH_TILE_BYTES + half * CH_HALF, &map_q, smem_u32(&sm->q_full), 0, half,
                                     p.h * a.G, p.q.row0 + (2 * p.j + t) * a.tt);
             }
-            if (!ok && count > 0) mbar_wait(smem_u32(&sm->q_full), (count - 1) & 1);
-        } else if (warp == 11 && lane == 0) {
+            sm->asked = count;
+        } else if (warp == CH_ROLES + 3 && lane == 0) {
             Walk<SPARSE> walk(a, start, end, sm->first);
             tell_pieces<SPARSE>(a, sm, walk);
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (sm->dead != 0) {  // what is in flight ends before the memory is given up (or the limits run out)
+        if (warp == CH_ROLES && lane == 0) {
+            report_error(a.err_flag, CLO_FLAG_TIMEOUT);
+            for (int x = max(sm->copied - CH_STAGES, 0); x < sm->copied; ++x)
+                mbar_wait(smem_u32(&sm->full[x % CH_STAGES]), x / CH_STAGES & 1);
+            if (sm->asked > 0) mbar_wait(smem_u32(&sm->q_full), (sm->asked - 1) & 1);
+        } else if (warp == CH_ROLES + 1 && lane == 0) {
+            tc_commit(smem_u32(&sm->drain));
+            mbar_wait(smem_u32(&sm->drain), 0);
+        }
+        __syncthreads();
+    }
     if (threadIdx.x == 0) {
-        if (sm->dead != 0) report_error(a.err_flag, CLO_FLAG_TIMEOUT);
         ws.desc[static_cast<size_t>(cta) * 8 + DESC_FLAGS].w = sm->again;
     }
-    if (warp == 9) {
+    if (warp == CH_ROLES + 1) {
         tc_fence_after();
         tmem_free(tmem, 4 * CH_TILE);
     }
@@ -1346,8 +1353,9 @@ extern "C" clo_status clo_paged_chunk_attn(const clo_paged_chunk_attn_args* args
         kh = static_cast<long long>(PG_BLOCK) * r.d;
         kb = kh * r.Hkv;
     }
-    for (const long long s : {kb, kh, kt})
+    for (const long long s : {kb, kh, 16 * kt})
         if (s < r.d || s % 8 != 0 || s > (1ll << 38)) return CLO_ERR_INVALID_ARG;
+    if (kt < r.d || kt % 8 != 0) return CLO_ERR_INVALID_ARG;
     if (meet(r.q, (r.N - 1) * (r.N > 1 ? r.q_stride : 0) + row, r.out, r.N * row)) return CLO_ERR_INVALID_ARG;
     PagedAttnArgs a{};
     a.q = static_cast<const uint8_t*>(r.q);
