@@ -3,24 +3,42 @@
 //
 // Work.  A request's rows of one KV head (its new tokens times the G heads of the
 // group) are cut into tiles of as many whole tokens as fit 128 rows, and two tiles are
-// an item.  An item goes over the tokens that its last row sees, 128 at a time.  All items of a call, weighed by
-// their tokens, are shared out evenly, one contiguous range a CTA and one CTA an
-// SM; each CTA works its range out by itself from the lengths.  An item that a
-// border cuts leaves a partial result for each piece (sums, reference, denominator), which
-// paged_merge_kernel joins.  So few rows over a long context occupy every SM, and a
-// long prompt costs each SM the same.
+// an item.  An item goes over the tokens that its last row sees, 128 at a time.  All
+// items of a call, weighed by their tokens, are shared out evenly, one contiguous range
+// a CTA and one CTA an SM; each CTA works its range out by itself from the lengths.  An
+// item that a border cuts leaves a partial result for each piece (sums, reference,
+// denominator), which paged_merge_kernel joins.  So few rows over a long context occupy
+// every SM, and a long prompt costs each SM the same.
 //
-// A CTA has two streams, each a warpgroup with its own scores and sums in tensor memory (4
-// x 128 columns: all of it).  An item of two tiles of rows gives one to each stream,
+// A CTA has two streams, each a warpgroup with its own scores and sums in tensor memory
+// (4 x 128 columns: all of it).  An item of two tiles of rows gives one to each stream,
 // and both go over every tile of tokens, so the tensor cores work on one stream's
-// products while the other's weights are made.  An item of one tile gives the
-// streams alternate tiles of tokens, and their sums are added up at its end.  A row belongs to one thread: no shuffles.  Besides:
+// products while the other's weights are made.  An item of one tile gives the streams
+// alternate tiles of tokens, and their sums are added up at its end.  A row belongs to
+// one thread: no shuffles.  Besides:
 //   warp 8   brings K and V tiles into a ring of five (a copy a block, whatever the
 //            cache's strides), in the order in which the products take them;
 //   warp 9   issues the products: S = Q K^T, both from shared memory, and O += P V with
 //            P from tensor memory, where it takes the place of S;
 //   warp 10  brings the rows of q;
 //   warp 11  tells the others their pieces of work, ahead of time.
+//
+// What bounds it, and the figures (one GB300).  Many rows: the chain of one stream, the
+// products of its tile (16 instructions, about 1250 clocks for the 1024 they are worth:
+// Q K^T reads both operands from shared memory) and its softmax (1130 clocks for 128 scores
+// a thread: exponentials, conversions and sums together), with about 700 clocks of
+// hand-overs between the two; 1.5 us a pair of tiles.  4096 tokens after 61440 with 32
+// query heads take 2.71 to 2.76 ms from idle (1.57 PFLOP/s, 0.83 of the measured burst rate
+// of bf16 products) and 3.1 to 3.2 ms back to back, under the power limit (1.35, 0.78 of the
+// sustained rate).  Few rows: HBM; 64 requests of 8001 tokens and 8 KV heads, a token
+// each, take 308 us (6.8 TB/s), one of 128K 90 us (6.0).  Short calls: about 3 us until the
+// first copies, 2 a piece's end, 4 for the join.
+//   Tried and not kept: two warpgroups a stream, 64 scores a thread (+4%: the exponentials
+// take as long, and more warps wait); the maximum beside the weights instead of before them
+// (+4%); the first half of a tile's weights handed over early (+3%); one lane of a warp, or
+// none, asking a barrier that others wait for (+3 to 6%); asking without suspending the warp
+// (+18%, in one thread alone); results turned within the warp so that a store writes whole
+// lines (+1 to 3%).
 // Softmax: with a reference that lies 2^6 below a maximum seen so far and moves only when
 // a score passes it by 2^14, weights up to 2^14 fit fp16 and those down to 2^-31 of
 // the largest still count, and sums in tensor memory are seldom rescaled.
@@ -34,6 +52,8 @@
 //
 // Every wait has a limit (about 2 s); one that runs out ends the CTA's work in order.
 #include <math.h>
+
+#include <atomic>
 
 #include "clo_kv4_math.cuh"  // barriers, fp32 pairs
 #include "clo_paged_attention.cuh"
@@ -52,10 +72,14 @@ constexpr int CH_THREADS = 384;
 constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
 constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
-constexpr int CH_FIXED = 256;                     // what an item costs beside its tokens, in tokens
-constexpr int CH_ONE = 12;                         // a token of an item of one tile of rows, in 16ths of one of two
-constexpr int CH_LEAST = 384;                     // weight that is worth a CTA of its own
-constexpr int CH_JOIN = 512;                      // what cutting an item costs (partial results, the join), in tokens
+// Weights, in tokens of an item of two tiles of rows.  Fitted to the CTAs' times in mixed
+// steps: a tile of tokens takes 1.5 us with two tiles of rows and 1.15 us with one, an item
+// 6 and 4.5 us beside its tiles.  (A mixed step of 64 requests takes 844 us on average over
+// six draws; with 256 tokens an item 919, with equal weights for both kinds 981 to 928.)
+constexpr int CH_FIXED = 512;                     // an item, beside its tokens
+constexpr int CH_ONE = 12;                        // a token of an item of one tile of rows, in 16ths
+constexpr int CH_LEAST = 384;                     // what is worth a CTA of its own
+constexpr int CH_JOIN = 640;                      // cutting an item (partial results, the join)
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
 constexpr int CH_SMALL = 2048;                    // shared memory beside the tiles
 constexpr int CH_SMEM = CHUNK_ROWS * PG_ROW + CH_STAGES * CH_TILE_BYTES + CH_SMALL + 1024;
@@ -971,7 +995,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     Piece p;
 
     if (warp < CH_ROLES) {
-        regs_up<CH_REGS_SOFTMAX>();
+        regs_up<CH_REGS_SOFTMAX>();  // (granted once the other four warps have given theirs up)
         RowSoftmax<BF16, SPARSE> w{a, ws, sm, warp >> 2, static_cast<int>(threadIdx.x) & 127,
                                 tmem + (static_cast<uint32_t>(warp & 3) << 21)};
         while (pieces.next(p, lane))
@@ -1245,6 +1269,14 @@ constexpr size_t CHUNK_WS_CTA = 2 * CHUNK_ROWS * (PG_D * sizeof(float) + sizeof(
 template <bool BF16, bool SPARSE>
 static clo_status run_paged(PagedAttnArgs a, void* workspace, const clo_attn_opts* opts, cudaStream_t stream) {
     const auto main = paged_chunk_kernel<BF16, SPARSE>;
+    // The roles' registers are taken from those of the launch: with fewer the softmax warps would
+    // wait for ever.
+    static std::atomic<bool> looked{false};
+    if (!looked.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, main) != cudaSuccess || attr.numRegs < CH_REGS) return CLO_ERR_CUDA;
+        looked.store(true, std::memory_order_relaxed);
+    }
     // No item weighs more than the longest request, the new tokens and CH_FIXED.
     const double items = (a.N / (2.0 * a.tt) + min(a.B, a.N)) * a.Hkv;
     const double most = items * (CH_FIXED + (SPARSE ? 16.0 * a.n_sel : 16.0 * a.max_blocks + a.N));
