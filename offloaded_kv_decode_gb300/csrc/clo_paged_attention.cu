@@ -43,6 +43,12 @@
 // a score passes it by 2^14, weights up to 2^14 fit fp16 and those down to 2^-31 of
 // the largest still count, and sums in tensor memory are seldom rescaled.
 //
+// Weights in 16 bits: each is off by half a step, 2^-9 or 2^-12 of itself, and so is a row of a
+// few tokens, where the roundings of many do not cancel out.  In items of up to CH_FINE tiles
+// of tokens what the rounding took off is a second set of weights, and both meet V: half
+// again as many products in items that have few (a prompt of 2000 tokens takes 62 us
+// instead of 59), and bf16 results of short contexts are off by their own rounding alone.
+//
 // What a row does not see.  Scores are replaced before anything is made of them.  A
 // weight of 0 does not hide a V that is not finite: rows of V behind the item's
 // last token are zeroed as they are brought in; one between a row's last token and
@@ -70,7 +76,7 @@ constexpr int CHUNK_ROWS = 2 * CH_TILE;           // rows of an item, at most
 constexpr int CH_ROLES = 8;                       // warps of the softmax; behind them: copies, products, queries, pieces
 constexpr int CH_THREADS = 384;
 constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
-constexpr int CH_REGS_SOFTMAX = 216, CH_REGS_REST = 72;
+constexpr int CH_REGS_SOFTMAX = 200, CH_REGS_REST = 104;  // (no spills; 216 and 72 had them in the thread of the products)
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
 // Weights, in tokens of an item of two tiles of rows.  Fitted to the CTAs' times in mixed
 // steps: a tile of tokens takes 1.5 us with two tiles of rows and 1.15 us with one, an item
@@ -81,6 +87,7 @@ constexpr int CH_ONE = 12;                        // a token of an item of one t
 constexpr int CH_LEAST = 384;                     // what is worth a CTA of its own
 constexpr int CH_JOIN = 640;                      // cutting an item (partial results, the join)
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
+constexpr int CH_FINE = 1;                        // tiles up to which weights come in two parts: see above
 constexpr int CH_SMALL = 2048;                    // shared memory beside the tiles
 constexpr int CH_SMEM = CHUNK_ROWS * PG_ROW + CH_STAGES * CH_TILE_BYTES + CH_SMALL + 1024;
 constexpr int CH_PIECES = 4;                      // pieces told ahead
@@ -232,6 +239,7 @@ struct Piece {
     int tokens;  // of the item
     int sees;    // tokens of the item's last row
     __device__ bool whole() const { return lo == 0 && hi == tiles; }
+    __device__ bool fine() const { return tiles <= CH_FINE; }
     __device__ bool two(const PagedAttnArgs& a) const { return tokens > a.tt; }
 };
 
@@ -487,13 +495,17 @@ struct Issuer {
         tc_commit(smem_u32(&sm->s_full[s]));
     }
     // O of stream s (+)= its weights times V of tile x.
-    __device__ void sums(int s, int x, bool add) {
+    __device__ void sums(int s, int x, bool add, bool fine) {
         const uint64_t v = tc_tile(ring + (x % CH_STAGES) * CH_TILE_BYTES, 1024, 2048);
         const uint32_t d = tmem + (2 + s) * CH_TILE, w = tmem + s * CH_TILE;
         tc_mma_ts(d, w, v, tc_shape(BF16, CH_TILE, CH_TILE, true), add);
 #pragma unroll
         for (int i = 1; i < 8; ++i)
             tc_mma_ts(d, w + 8 * i, tc_ahead(v, i * PG_BLOCK_BYTES >> 4), tc_shape(BF16, CH_TILE, CH_TILE, true), true);
+        if (fine)
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i)
+                tc_mma_ts(d, w + 64 + 8 * i, tc_ahead(v, i * PG_BLOCK_BYTES >> 4), tc_shape(BF16, CH_TILE, CH_TILE, true), true);
     }
     __device__ bool weights(int s) {
         const uint32_t count = s == 0 ? p_count0++ : p_count1++;
@@ -521,7 +533,7 @@ struct Issuer {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!weights(s)) return false;
-                    sums(s, v, i > 0);
+                    sums(s, v, i > 0, p.fine());
                     if (s == 1) release(v);
                     if (more) {
                         if (s == 0 && !here(k)) return false;
@@ -546,7 +558,7 @@ struct Issuer {
                 const bool more = i + 2 < n;
                 const int k = more ? take() : 0;
                 if (!here(v) || !weights(s)) return false;
-                sums(s, v, i >= 2);
+                sums(s, v, i >= 2, p.fine());
                 release(v);
                 if (more) {
                     if (!here(k)) return false;
@@ -577,6 +589,7 @@ struct RowSoftmax {
 
     // The weights of one tile of tokens from their scores.  sees: tokens of the
     // tile that the row sees; first: of this piece.
+    template <bool FINE>
     __device__ __forceinline__ void tile(int sees, uint32_t place_rows, bool masked, bool first, float& ref, float& sum) {
         float x[4][32];
 #pragma unroll
@@ -647,18 +660,36 @@ struct RowSoftmax {
         const float r = ref == -INFINITY ? 0.f : ref;
         const float2 scale = make_float2(a.scale_log2, a.scale_log2), minus = make_float2(-r, -r);
         float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if constexpr (!FINE) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t w[32];
+            for (int half = 0; half < 2; ++half) {
+                uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int c = 2 * half + i / 16, k = 2 * (i & 15);
-                float2 y = fma2(make_float2(x[c][k], x[c][k + 1]), scale, minus);
-                y = make_float2(ex2(y.x), ex2(y.y));
-                w[i] = pg_pack<BF16>(y.x, y.y);
-                l[i & 1] = add2(l[i & 1], y);
+                for (int i = 0; i < 32; ++i) {
+                    const int c = 2 * half + i / 16, k = 2 * (i & 15);
+                    float2 y = fma2(make_float2(x[c][k], x[c][k + 1]), scale, minus);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    w[i] = pg_pack<BF16>(y.x, y.y);
+                    l[i & 1] = add2(l[i & 1], y);
+                }
+                tmem_store32(tmem + s * CH_TILE + 32 * half, w);
             }
-            tmem_store32(tmem + s * CH_TILE + 32 * half, w);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16], rest[16];  // the weights, and what their rounding took off
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float2 y = fma2(make_float2(x[c][2 * i], x[c][2 * i + 1]), scale, minus);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    w[i] = pg_pack<BF16>(y.x, y.y);
+                    const float2 z = pg_unpack<BF16>(w[i]);
+                    rest[i] = pg_pack<BF16>(y.x - z.x, y.y - z.y);
+                    l[i & 1] = add2(l[i & 1], y);
+                }
+                tmem_store16(tmem + s * CH_TILE + 16 * c, w);
+                tmem_store16(tmem + s * CH_TILE + 64 + 16 * c, rest);
+            }
         }
         l[0] = add2(l[0], l[1]);
         sum += l[0].x + l[0].y;
@@ -768,7 +799,8 @@ struct RowSoftmax {
                 continue;
             }
             tc_fence_after();
-            tile(seen, rows_here, masked, t == t0, ref, sum);
+            if (p.fine()) tile<true>(seen, rows_here, masked, t == t0, ref, sum);
+            else tile<false>(seen, rows_here, masked, t == t0, ref, sum);
         }
         const bool second = two || n > 1;  // stream 1 had tiles
         if (s == 0 || two) {

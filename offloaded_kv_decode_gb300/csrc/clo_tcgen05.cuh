@@ -51,6 +51,15 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&w)[
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&w)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};\n" ::"r"(addr),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+        : "memory");
+}
+
 // ---------------------------------------------------------------- products
 
 // A tile of rows of 128 bytes with the 128-byte swizzle: units of 8 rows, 1024 bytes at

@@ -95,6 +95,21 @@ def test_flat_and_sharp_weights(size, dtype):
     check([700], [200], 4, 1, dtype, seed=21, size=size)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_short_contexts_are_as_exact_as_the_output(dtype):
+    """Up to 128 tokens the weights have twice the bits: what is left is the output's own
+    rounding, the scores' and the sums' in fp32."""
+    lens, n_new = [2, 3, 5, 17, 40, 128, 100], [2, 1, 5, 17, 8, 128, 60]
+    kc, vc, table = ref.make_cache(lens, 2, dtype, 23, fill=float("nan"))
+    q = queries(sum(n_new), 8, dtype, 24)
+    out, lse, err = chunk(q, kc, vc, table, lens, n_new)
+    assert err == 0
+    want, _, mag, size = ref.chunk_attention(q, kc, vc, table, lens, n_new)
+    d = 2.0 ** -19 * size + 2.0 ** -20
+    tol = ref.half_step(dtype) * want.abs() + (2.0 ** -15 + 2 * d[..., None] + 16 * 2.0 ** -23) * mag + 2.0 ** -24
+    assert ((out.double() - want).abs() <= tol).all()
+
+
 def test_rising_scores():
     """Each token outweighs all before it: the running maximum moves at every step."""
     T, dtype = 600, torch.float16
@@ -406,6 +421,50 @@ def test_sparse_twice_the_same_block():
     out, lse, err = sparse(q, kc, vc, table, [200], sel)
     assert err == 0
     ref.check_attention(out, lse, sparse_ref(q, kc, vc, table, [200], sel), 200)
+
+
+def test_selected_blocks_in_a_graph():
+    """Bounds, selection and attention captured once and replayed with other queries, keys
+    and lengths in the same buffers."""
+    dtype, Hkv, lens = torch.bfloat16, 2, [700, 33, 1500]
+    kc, vc, table = ref.make_cache(lens, Hkv, dtype, 15)
+    q = queries(3, 8, dtype, 16)
+    last = [table[r, (T - 1) // 16].item() * 16 + (T - 1) % 16 for r, T in enumerate(lens)]
+    slots = [t for r, T in enumerate(lens) for p in range(ref.blocks_of(T))
+             for t in range(table[r, p].item() * 16, table[r, p].item() * 16 + min(16, T - 16 * p))]
+    slots = torch.tensor(slots, dtype=torch.int32, device="cuda")
+    assert slots[-1] == last[-1]
+    bounds = torch.zeros(kc.shape[0], Hkv, ref.RECORD, dtype=torch.uint8, device="cuda")
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    sel = torch.empty(3, Hkv, 20, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(3, 8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sws = torch.empty(clo.clo_paged_select_workspace_size(3, Hkv, table.shape[1]), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(clo.clo_paged_chunk_workspace_size(8, Hkv), dtype=torch.uint8, device="cuda")
+    calls = [clo.prepare_paged_block_bounds(kc, slots, bounds, err_flag=err),
+             clo.prepare_paged_block_select(q, bounds, table, ctx, sel, sws, 1, 2, err_flag=err),
+             clo.prepare_paged_sparse_decode_attn(q, kc, vc, table, ctx, sel, out, ws, lse=lse, err_flag=err)]
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c in calls:
+            c()
+    for step in range(2):
+        if step == 1:
+            kc.mul_(-0.5)
+            q.copy_(queries(3, 8, dtype, 17))
+            ctx.copy_(torch.tensor([690, 20, 1499], dtype=torch.int32))
+            lens = [690, 20, 1499]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        for r, T in enumerate(lens):
+            nb = ref.blocks_of(T)
+            for h in range(Hkv):
+                assert sel[r, h].tolist() == ref.select(q[r, 4 * h:4 * h + 4].cpu(), bounds[table[r, :nb].long(), h].cpu(), nb, 20, 1, 2)
+        ref.check_attention(out, lse, sparse_ref(q, kc, vc, table, lens, sel), 1500)
 
 
 def test_sparse_bad_entries():
