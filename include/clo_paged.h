@@ -8,8 +8,8 @@
  *     written to the slots that clo_paged_plan gave (clo_paged_rope_append);
  *   - the attention of each request's new tokens, one or thousands, over its
  *     cached tokens, themselves among them (clo_paged_chunk_attn);
- *   - for long contexts, a selection of blocks by a score that reads an
- *     eighth of a byte for each byte of the keys' (clo_paged_block_bounds,
+ *   - for long contexts, a selection of blocks by a score that reads a
+ *     fifteenth of the keys' bytes (clo_paged_block_bounds,
  *     clo_paged_block_select) and the decode attention over the selected
  *     blocks alone (clo_paged_sparse_decode_attn).  It is to a paged cache what
  *     clo_topk_retrieve and the Cache Buffer are to an offloaded one.
