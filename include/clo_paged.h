@@ -140,7 +140,8 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  * workspace:   >= clo_paged_chunk_workspace_size(...) bytes, 16-byte aligned.
  * err_flag:    a length out of range or offsets that descend or leave [0, N] set
  *              CLO_FLAG_BAD_CTX: a bad length zeroes the request's rows, and
- *              requests with bad offsets are passed over.  A bad block sets
+ *              requests with bad offsets are passed over, all requests if the
+ *              others' rows come to more than 2 N.  A bad block sets
  *              CLO_FLAG_BAD_INDEX and zeroes the rows (of that KV head) that see it,
  *              and it may zero other rows of the request and KV head.  A copy or a
  *              product that does not end within about 2 s, which says that the GPU

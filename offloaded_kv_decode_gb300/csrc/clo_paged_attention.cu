@@ -76,7 +76,7 @@ constexpr int CHUNK_ROWS = 2 * CH_TILE;           // rows of an item, at most
 constexpr int CH_ROLES = 8;                       // warps of the softmax; behind them: copies, products, queries, pieces
 constexpr int CH_THREADS = 384;
 constexpr int CH_REGS = 168;                      // a thread at launch: 65536 / 384, in eights
-constexpr int CH_REGS_SOFTMAX = 200, CH_REGS_REST = 104;  // (no spills; 216 and 72 had them in the thread of the products)
+constexpr int CH_REGS_SOFTMAX = 200, CH_REGS_REST = 104;  // (with 216 and 72 the thread of the products spills)
 static_assert(2 * CH_REGS_SOFTMAX + CH_REGS_REST <= 3 * CH_REGS, "a split may not ask for more than the launch has");
 // Weights, in tokens of an item of two tiles of rows.  Fitted to the CTAs' times in mixed
 // steps: a tile of tokens takes 1.5 us with two tiles of rows and 1.15 us with one, an item
@@ -119,6 +119,7 @@ struct alignas(16) ChunkSmall {
     int dead;      // a wait ran out
     int again;     // a complete item has a result that is not finite
     int copied, asked;  // tiles and queries whose copies were issued
+    int odd;       // a request is bad
     int bad[8];    // by item: a place that could not be read
     float2 ml1[CH_TILE];  // stream 1's reference and denominator, for items with one tile of rows
 };
@@ -354,6 +355,18 @@ struct Pieces {
         return p.tokens > 0;  // else that was the end
     }
 };
+
+// Where offsets descend the others' requests may overlap, and with more than 2 N rows the
+// weights' sums, made for N, might pass 32 bits: such a call has no pieces.
+__device__ __noinline__ bool too_many_rows(const int32_t* offsets, int B, int N) {
+    long long rows = 0;
+#pragma unroll 1
+    for (int r = 0; r < B; ++r) {
+        const int first = offsets[r], end = offsets[r + 1];
+        if (first >= 0 && first <= end && end <= N) rows += end - first;
+    }
+    return rows > 2ll * N;
+}
 
 template <bool SPARSE>
 __device__ __forceinline__ void tell_pieces(const PagedAttnArgs& a, ChunkSmall* sm, Walk<SPARSE>& walk) {  // one thread
@@ -886,6 +899,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == CH_ROLES + 1) tmem_alloc(smem_u32(&sm->tmem), 4 * CH_TILE);
+    if (threadIdx.x == CH_ROLES * 32) sm->odd = 0;
+    __syncwarp();
     if (threadIdx.x == (CH_ROLES + 2) * 32) {
         tma_prefetch(&map_q);
         tma_prefetch(&map_k);
@@ -911,6 +926,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     if (!one_warp || finder) {
         const int per = one_warp ? 1 : (a.B + CH_THREADS - 1) / CH_THREADS;
         const int r0 = (one_warp ? lane : static_cast<int>(threadIdx.x)) * per, r1 = min(a.B, r0 + per);
+        if (!SPARSE && !one_warp) __syncthreads();  // (odd)
         bool bad = false;
 #pragma unroll 1
         for (int r = r0; r < r1; ++r) {
@@ -919,7 +935,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             if (!one_warp) sh.req[r] = req;
             add(req);
         }
-        if (bad && cta == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
+        if (bad) {
+            if (cta == 0) report_error(a.err_flag, CLO_FLAG_BAD_CTX);
+            *reinterpret_cast<volatile int*>(&sm->odd) = 1;
+        }
         weight1 = weight;
         items1 = items;
 #pragma unroll
@@ -1081,6 +1100,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             sm->asked = count;
         } else if (warp == CH_ROLES + 3 && lane == 0) {
             Walk<SPARSE> walk(a, start, end, sm->first);
+            if (!SPARSE && sm->odd != 0 && too_many_rows(a.offsets, a.B, a.N)) walk.at.r = a.B;
             tell_pieces<SPARSE>(a, sm, walk);
         }
     }

@@ -238,6 +238,18 @@ def test_bad_lengths_offsets_and_blocks():
     assert torch.all(out[260:] == 3)
 
 
+@pytest.mark.parametrize("B", [7, 70])  # a request a lane; summed up by all threads
+def test_offsets_that_overlap_many_times_are_passed_over(B):
+    """Every other request descends, the others have all rows: more than 2 N, so no row is written."""
+    dtype = torch.float16
+    kc, vc, table = ref.make_cache([64] * B, 2, dtype, 83)
+    q = queries(40, 4, dtype, 86)
+    offs = torch.tensor([40 * (r % 2) for r in range(B + 1)], dtype=torch.int32, device="cuda")
+    out, lse, err = chunk(q, kc, vc, table, [64] * B, [40] * B, offsets=offs, fill=3.0)
+    assert err == clo.FLAG_BAD_CTX
+    assert torch.all(out == 3)
+
+
 def test_a_block_that_no_row_sees_may_be_bad():
     """Table entries behind the context are not looked at."""
     dtype = torch.float16
