@@ -202,7 +202,7 @@ size_t clo_paged_bounds_bytes(int block_size, int d);
  *     code of a channel's largest  = its quotient by scale (fp32), rounded up,
  *     code of a channel's smallest = its quotient by scale (fp32), rounded down,
  * both limited to +-127.  A block with a NaN or an infinity gets codes of 0 and
- * the scale +inf: it is always selected.
+ * the scale +inf: it is selected before those with a score.
  * kc:       [num_blocks][Hkv][16][d] of type `dtype`, contiguous.
  * slot_map: [N] int32.  A request's new tokens follow one another, as
  *           clo_paged_plan writes them: the last entry of a run of consecutive
@@ -240,14 +240,15 @@ size_t clo_paged_select_workspace_size(int B, int Hkv, int max_blocks);
  * the whole numbers exact and the product in fp32.  In exact numbers this is an
  * upper bound of the summed score s . K_t that clo_topk_retrieve ranks tokens by.
  * The first n_first blocks of a request and the last n_last, the one being
- * filled among them, are always selected (as
- * long as there is room); of the others those with the highest
- * scores, equal ones going to the lower block, until there are n_sel.  A request
- * with no more than n_sel blocks has them all.
+ * filled among them, are always selected.  Of the others those without a finite
+ * scale or entry come next (see bounds and block_table), with those whose score is
+ * beyond fp32, then those with the highest scores, equal ones going to the lower
+ * block, until there are n_sel.  A request with no more than n_sel blocks has them
+ * all.
  * q:           [B][Hq][d] of type `dtype`, contiguous.
  * bounds:      as clo_paged_block_bounds writes them.
  * block_table, ctx_len: as for clo_paged_decode_attn.  A block out of range sets
- *              CLO_FLAG_BAD_INDEX and counts as one that is always selected (what
+ *              CLO_FLAG_BAD_INDEX and counts as one without a finite scale (what
  *              attends to it reports it); a bad length sets CLO_FLAG_BAD_CTX and
  *              selects nothing.
  * sel:         [B][Hkv][n_sel] int32 output: columns of block_table, ascending,

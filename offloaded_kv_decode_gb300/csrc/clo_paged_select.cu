@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) block_bounds_kernel(const Boun
 constexpr int SCORE_THREADS = 256;
 constexpr int SCORE_COLS = SCORE_THREADS / 8;    // columns a CTA scores: 8 lanes a column
 constexpr int SCORE_HEADS = 8;                   // KV heads a CTA scores, at most
-constexpr uint32_t KEY_ALWAYS = 0xffffffffu;                     // above every score's key
+// Above every score's key: a block that has none, and above those the first and last ones,
+// for which n_sel always has room.
+constexpr uint32_t KEY_ALWAYS = 0xfffffffeu, KEY_FORCED = 0xffffffffu;
 
 struct SelectArgs {
     const void* q;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, 3) block_score_kernel(const Sel
         uint8_t* to = records + lane * bytes;
         if (ok) {
             bulk_load(smem_u32(to), a.bounds + (static_cast<size_t>(id) * a.Hkv + g0) * PG_RECORD, bytes, b, l2_evict_first_policy());
-        } else if (there) {  // a bad block is always selected
+        } else if (there) {  // a bad block counts as one without a score
             report_error(a.err_flag, CLO_FLAG_BAD_INDEX);
             for (int h = 0; h < heads; ++h) *reinterpret_cast<float*>(to + h * PG_RECORD + 256) = INFINITY;
         }
@@ -266,9 +268,9 @@ __global__ void __launch_bounds__(SCORE_THREADS, 3) block_score_kernel(const Sel
         sum += __shfl_xor_sync(FULL_MASK, sum, 1);
         if (u == 0 && col < nb) {
             const float scale = *reinterpret_cast<const float*>(rec + 256);
-            const bool always = col < a.n_first || col >= nb - a.n_last || !pg_finite(scale);
+            const bool forced = col < a.n_first || col >= nb - a.n_last;
             a.keys[(static_cast<size_t>(r) * a.Hkv + g0 + h) * a.key_stride + col] =
-                always ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale);
+                forced ? KEY_FORCED : !pg_finite(scale) ? KEY_ALWAYS : score_key(static_cast<float>(sum) * scale);
         }
     }
 }
