@@ -148,9 +148,10 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  *              is in trouble, sets CLO_FLAG_TIMEOUT; the outputs are then undefined.
  * opts:        optional: num_ctas, at most 4095; the events bracket the main kernel.
  * Scores and sums are in fp32; the weights are rounded to `dtype` for the product
- * with V, in fp16 after a factor that keeps what is 2^-31 of the largest; where the
- * last of a tile's rows sees at most 128 tokens, to twice the bits.  The same
- * call on the same kind of GPU gives the same bits each time.
+ * with V, in fp16 after a factor that keeps what is 2^-31 of the largest; in tiles of
+ * rows (a request's new tokens in groups of floor(128 Hkv / Hq)) whose last one sees at
+ * most 128 tokens, to twice the bits.  The same call on the same kind of GPU gives the
+ * same bits each time.
  * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, N * Hq < 2^29,
  * max_blocks <= 2^20, num_blocks <= 2^26, scale > 0, strides of at most 2^38 (kv_token
  * 2^34) and a cache that spans less than 2^31 times the greatest common divisor of

@@ -44,10 +44,11 @@
 // the largest still count, and sums in tensor memory are seldom rescaled.
 //
 // Weights in 16 bits: each is off by half a step, 2^-9 or 2^-12 of itself, and so is a row of a
-// few tokens, where the roundings of many do not cancel out.  In items of up to CH_FINE tiles
-// of tokens what the rounding took off is a second set of weights, and both meet V: half
-// again as many products in items that have few (a prompt of 2000 tokens takes 62 us
-// instead of 59), and bf16 results of short contexts are off by their own rounding alone.
+// few tokens, where the roundings of many do not cancel out.  In tiles of rows that see up to
+// CH_FINE tiles of tokens what the rounding took off is a second set of weights, and both meet
+// V: half again as many products in items that have few (a prompt of 2000 tokens takes 62 us
+// instead of 59; one of 300 with a query head a KV head 16.3 instead of 14.3), and bf16 results
+// of short contexts are off by their own rounding alone.
 //
 // What a row does not see.  Scores are replaced before anything is made of them.  A
 // weight of 0 does not hide a V that is not finite: rows of V behind the item's
@@ -87,7 +88,7 @@ constexpr int CH_ONE = 12;                        // a token of an item of one t
 constexpr int CH_LEAST = 384;                     // what is worth a CTA of its own
 constexpr int CH_JOIN = 640;                      // cutting an item (partial results, the join)
 constexpr float CH_LIFT = 6.f, CH_SLACK = 14.f;   // log2 units: see above
-constexpr int CH_FINE = 1;                        // tiles up to which weights come in two parts: see above
+constexpr int CH_FINE = 1;                        // tiles of tokens up to which weights come in two parts: see above
 constexpr int CH_SMALL = 2048;                    // shared memory beside the tiles
 constexpr int CH_SMEM = CHUNK_ROWS * PG_ROW + CH_STAGES * CH_TILE_BYTES + CH_SMALL + 1024;
 constexpr int CH_PIECES = 4;                      // pieces told ahead
@@ -236,12 +237,16 @@ __device__ ChunkPos weight_at(const PagedAttnArgs& a, const PagedReq& q, int r, 
 // One piece of work: tiles lo .. hi - 1 of an item of `tiles`.
 struct Piece {
     PagedReq q;
-    int r, h, j, lo, hi, tiles;
+    int r, h, j, lo, hi;
+    int marks;   // the item's tiles; bits 30 + s: stream s makes weights in two parts (with one
+                 // tile of rows both say so).  One register: with two the softmax spills.
     int tokens;  // of the item
     int sees;    // tokens of the item's last row
-    __device__ bool whole() const { return lo == 0 && hi == tiles; }
-    __device__ bool fine() const { return tiles <= CH_FINE; }
+    __device__ int tiles() const { return marks & 0x3fffffff; }
+    __device__ bool whole() const { return lo == 0 && hi == tiles(); }
     __device__ bool two(const PagedAttnArgs& a) const { return tokens > a.tt; }
+    // (Behind CH_FINE tiles of tokens all of such a stream's weights are 0.)
+    __device__ bool fine(int s, int t) const { return t < CH_FINE && (static_cast<unsigned>(marks) >> (30 + s) & 1) != 0; }
 };
 
 // The pieces from `start` to `end`, in order.
@@ -275,10 +280,10 @@ struct Walk {
         p.h = at.h;
         p.j = at.j;
         p.sees = item_sees<SPARSE>(a, q, at.j);
-        p.tiles = (p.sees + CH_TILE - 1) / CH_TILE;
+        p.marks = (p.sees + CH_TILE - 1) / CH_TILE;
         p.tokens = min(2 * a.tt, q.n - at.j * 2 * a.tt);
         p.lo = at.cut;
-        p.hi = at_end ? min(end.cut, p.tiles) : p.tiles;
+        p.hi = at_end ? min(end.cut, p.marks) : p.marks;
         at.cut = 0;
         if (++at.j == items) {
             at.j = 0;
@@ -347,7 +352,7 @@ struct Pieces {
         p.j = y.y;
         p.lo = y.z;
         p.hi = y.w;
-        p.tiles = z.x;
+        p.marks = z.x;
         p.tokens = z.y;
         p.sees = z.z;
         if (lane >= 0) __syncwarp();
@@ -378,7 +383,10 @@ __device__ __forceinline__ void tell_pieces(const PagedAttnArgs& a, ChunkSmall* 
         if (!ch_wait(sm->heard[slot], (it / CH_PIECES & 1) ^ 1, sm)) return;
         sm->piece[slot][0] = make_int4(p.q.row0, p.q.n, p.q.ctx, p.r);
         sm->piece[slot][1] = make_int4(p.h, p.j, p.lo, p.hi);
-        sm->piece[slot][2] = make_int4(p.tiles, p.tokens, p.sees, 0);
+        // By what the last row of a stream's own tile sees, be that the first of an item's two or not.
+        const int first_sees = p.sees - (p.two(a) ? p.tokens - a.tt : 0);
+        const unsigned fine = (first_sees <= CH_FINE * CH_TILE ? 1u << 30 : 0u) | (p.sees <= CH_FINE * CH_TILE ? 1u << 31 : 0u);
+        sm->piece[slot][2] = make_int4(static_cast<int>(p.marks | fine), p.tokens, p.sees, 0);
         mbar_arrive(smem_u32(&sm->told[slot]));
         if (!more) return;
     }
@@ -546,7 +554,7 @@ struct Issuer {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!weights(s)) return false;
-                    sums(s, v, i > 0, p.fine());
+                    sums(s, v, i > 0, p.fine(s, p.lo + i));
                     if (s == 1) release(v);
                     if (more) {
                         if (s == 0 && !here(k)) return false;
@@ -571,7 +579,7 @@ struct Issuer {
                 const bool more = i + 2 < n;
                 const int k = more ? take() : 0;
                 if (!here(v) || !weights(s)) return false;
-                sums(s, v, i >= 2, p.fine());
+                sums(s, v, i >= 2, p.fine(1, p.lo + i));
                 release(v);
                 if (more) {
                     if (!here(k)) return false;
@@ -812,7 +820,7 @@ struct RowSoftmax {
                 continue;
             }
             tc_fence_after();
-            if (p.fine()) tile<true>(seen, rows_here, masked, t == t0, ref, sum);
+            if (p.fine(s, t)) tile<true>(seen, rows_here, masked, t == t0, ref, sum);
             else tile<false>(seen, rows_here, masked, t == t0, ref, sum);
         }
         const bool second = two || n > 1;  // stream 1 had tiles
@@ -1059,7 +1067,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             bool ok = true;
             while (ok && pieces.next(p, lane)) {
                 if (p.lo > 0) head = 1;
-                else if (p.hi < p.tiles) tail = 1;
+                else if (p.hi < p.tiles()) tail = 1;
                 if (p.hi == p.lo) continue;
                 if (lane == 0) *reinterpret_cast<volatile int*>(&sm->bad[count & 7]) = 0;
                 ok = w.piece(p, count & 7);

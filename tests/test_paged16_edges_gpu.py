@@ -6,9 +6,11 @@ import torch
 
 import offloaded_kv_decode_gb300 as clo
 import paged_ref as ref
+from test_paged16_attention_gpu import chunk, queries
 from test_paged16_cache_gpu import rand, random_bounds, select
 
 pytestmark = pytest.mark.gpu
+DTYPES = [torch.float16, torch.bfloat16]
 
 
 # ---------------------------------------------------------------- selection
@@ -37,3 +39,29 @@ def test_first_and_last_blocks_come_before_those_without_a_score(n_first, n_last
     for h in range(Hkv):
         assert sel[0, h].tolist() == want
         assert sel[1, h].tolist() == ([0, 1] + [-1] * n_sel)[:n_sel] if n_sel > 1 else [1]
+
+
+# ---------------------------------------------------------------- short contexts
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("G,Hkv", [(1, 4), (3, 2), (5, 1), (7, 2), (4, 1)])
+@pytest.mark.parametrize("T,cached", [(129, 0), (300, 0), (1000, 0), (190, 37)])
+def test_first_rows_of_a_prompt_are_as_exact_as_the_output(T, cached, G, Hkv, dtype):
+    """The rows of a tile (of as many whole tokens as make 128 rows) whose last one sees at
+    most 128 tokens have weights of twice the bits, however long the prompt is.  What is left:
+    the output's own rounding; weights of 2^-16 (bf16) or 2^-22 (fp16) of themselves, so
+    2^-15 together with their sum; the scores' and the sums' roundings in fp32, as in
+    check_attention."""
+    n = T - (cached if G > 1 else 0)  # (with one head a tile is 128 tokens)
+    kc, vc, table = ref.make_cache([T], Hkv, dtype, T + G, fill=float("nan"))
+    q = queries(n, G * Hkv, dtype, T + G + 1)
+    out, _, err = chunk(q, kc, vc, table, [T], [n])
+    assert err == 0
+    want, _, mag, size = ref.chunk_attention(q, kc, vc, table, [T], [n])
+    tile = 128 // G
+    rows = [i for i in range(n) if T - n + min(n, (i // tile + 1) * tile) <= 128]  # of tiles that end within 128 tokens
+    assert rows
+    d = 2.0 ** -19 * size + 2.0 ** -20
+    tol = ref.half_step(dtype) * want.abs() + (2.0 ** -15 + 2 * d[..., None] + 16 * 2.0 ** -23) * mag + 2.0 ** -24
+    err = (out.double() - want).abs()
+    assert (err[rows] <= tol[rows]).all()
