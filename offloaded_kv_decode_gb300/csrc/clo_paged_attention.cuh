@@ -96,7 +96,8 @@ __device__ __forceinline__ uint32_t pg_pack_out(float lo, float hi) {
 
 // The attention of one query row by one warp, token after token in fp32: lane l
 // holds channels 4l .. 4l + 3.  Slow, and without any value of a token that the
-// row does not see.  `mine`: this lane's channels are written.
+// row does not see.  `mine`: this lane's channels are written.  The row's lse is left:
+// values do not enter it, and blocks that make different channels anew share it.
 template <bool BF16, bool SPARSE>
 __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const PagedReq& req, int i, int head, int lane, bool mine) {
     const int h = head / a.G;
@@ -140,7 +141,6 @@ __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const Page
     const size_t place = row * a.Hq + head;
     if (!mine) return;
     *reinterpret_cast<uint2*>(a.out + place * PG_ROW + lane * 8) = make_uint2(pg_pack_out<BF16>(o[0], o[1]), pg_pack_out<BF16>(o[2], o[3]));
-    if (a.lse != nullptr && lane == 0) a.lse[place] = none ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
 }  // namespace clo

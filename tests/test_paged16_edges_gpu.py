@@ -65,3 +65,30 @@ def test_first_rows_of_a_prompt_are_as_exact_as_the_output(T, cached, G, Hkv, dt
     tol = ref.half_step(dtype) * want.abs() + (2.0 ** -15 + 2 * d[..., None] + 16 * 2.0 ** -23) * mag + 2.0 ** -24
     err = (out.double() - want).abs()
     assert (err[rows] <= tol[rows]).all()
+
+
+# ---------------------------------------------------------------- rows that are made anew
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("channel", [0, 37, 127])
+@pytest.mark.parametrize("T,n,Hq,num_ctas", [(9000, 4, 4, 0), (9000, 9, 4, 0), (700, 200, 4, 0), (700, 200, 4, 1), (2000, 5, 16, 5)])
+def test_rows_made_anew_keep_their_lse(T, n, Hq, num_ctas, channel, dtype):
+    """A V that is not finite, in one channel of a request's last token, which its other rows do
+    not see: those are right, and their lse has the bits that it has beside a finite V, also
+    where several blocks put the channels of one row together."""
+    kc, vc, table = ref.make_cache([T], 2, dtype, 51, fill=float("nan"))
+    q = queries(n, Hq, dtype, 52)
+    want = ref.chunk_attention(q, kc, vc, table, [T], [n])
+    plain, lse0, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0
+    vc[table[0, (T - 1) // 16].long(), :, (T - 1) % 16, channel] = math.nan
+    first = None
+    for _ in range(3):
+        out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+        assert err == 0 and torch.equal(lse, lse0)
+        ref.check_attention(out[:-1], lse[:-1], tuple(x[:-1] for x in want), T)
+        assert torch.isnan(out[-1, :, channel]).all()
+        others = torch.arange(ref.D, device="cuda") != channel
+        assert torch.equal(out[-1][:, others], plain[-1][:, others])
+        assert first is None or torch.equal(out.nan_to_num(7.0), first.nan_to_num(7.0))
+        first = out
