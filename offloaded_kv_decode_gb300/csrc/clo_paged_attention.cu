@@ -1209,7 +1209,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
                 for (int i = 0; i < AHEAD; ++i) {
                     if (!there[i]) continue;
                     bad |= ml[i].y < 0.f;
-                    if (ml[i].x == -INFINITY) continue;  // sums of nothing
+                    if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;  // sums of nothing (NaN is something)
                     const float to = fmaxf(m, ml[i].x);
                     const float f = m == -INFINITY ? 0.f : ex2(m - to), w = ex2(ml[i].x - to);
                     l = l * f + ml[i].y * w;

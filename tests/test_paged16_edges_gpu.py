@@ -6,7 +6,7 @@ import torch
 
 import offloaded_kv_decode_gb300 as clo
 import paged_ref as ref
-from test_paged16_attention_gpu import chunk, queries
+from test_paged16_attention_gpu import chunk, queries, sparse
 from test_paged16_cache_gpu import rand, random_bounds, select
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +92,48 @@ def test_rows_made_anew_keep_their_lse(T, n, Hq, num_ctas, channel, dtype):
         assert torch.equal(out[-1][:, others], plain[-1][:, others])
         assert first is None or torch.equal(out.nan_to_num(7.0), first.nan_to_num(7.0))
         first = out
+
+
+# ---------------------------------------------------------------- scores that are not finite
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n,num_ctas", [(9000, 3, 0), (9000, 3, 1), (20000, 1, 0), (700, 200, 0)])
+def test_queries_of_nan_give_nan(T, n, num_ctas, dtype):
+    """However the work is split: a row that sees tokens is not one that sees none."""
+    kc, vc, table = ref.make_cache([T], 2, dtype, 61, fill=float("nan"))
+    q = queries(n, 8, dtype, 62)
+    want = ref.chunk_attention(q, kc, vc, table, [T], [n])
+    q[n // 2, 5, 7] = math.nan
+    out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0
+    assert torch.isnan(out[n // 2, 5]).all() and torch.isnan(lse[n // 2, 5])
+    keep = torch.ones(n, 8, dtype=torch.bool, device="cuda")
+    keep[n // 2, 5] = False
+    ref.check_attention(out[keep], lse[keep], tuple(x[keep] for x in want), T)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_keys_of_nan_give_nan(dtype):
+    """A long run of keys without a number, which some pieces of the work lie in altogether."""
+    T = 40000
+    kc, vc, table = ref.make_cache([T], 2, dtype, 63)
+    kc[table[0, 500:2000].long(), 1, :, 9] = math.nan
+    q = queries(1, 8, dtype, 64)
+    out, lse, err = chunk(q, kc, vc, table, [T], [1])
+    assert err == 0 and torch.isfinite(out[:, :4]).all() and torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all()
+    sel = torch.arange(500, 2000, dtype=torch.int32, device="cuda").expand(1, 2, 1500).contiguous()
+    out, lse, err = sparse(q, kc, vc, table, [T], sel)
+    assert err == 0 and torch.isfinite(out[:, :4]).all() and torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_piece_of_keys_of_nan_behind_what_a_row_sees(dtype):
+    """The keys from 384 on are without a number, and so is every row that sees one, though the
+    last piece of the work holds nothing else of it than those and tokens that it does not see."""
+    T, n = 640, 256
+    kc, vc, table = ref.make_cache([T], 1, dtype, 67)
+    kc[table[0, 24:].long()] = math.nan
+    q = queries(n, 1, dtype, 68)
+    for num_ctas in (0, 1, 2, 5):
+        out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+        assert err == 0 and torch.isnan(out).all() and torch.isnan(lse).all(), num_ctas
