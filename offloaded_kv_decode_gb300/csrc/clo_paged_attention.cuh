@@ -122,7 +122,7 @@ __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const Page
             for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(FULL_MASK, x, off);
             x *= a.scale_log2;
             const float mn = fmaxf(m, x);
-            const float old = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(x - mn);
+            const float old = m == -INFINITY ? 0.f : exp2f(m - mn), w = x == -INFINITY ? 0.f : exp2f(x - mn);
             const uint2 vw = *reinterpret_cast<const uint2*>(a.vc + base + t * a.kv_token);
             const float2 v0 = pg_unpack<BF16>(vw.x), v1 = pg_unpack<BF16>(vw.y);
             l = l * old + w;

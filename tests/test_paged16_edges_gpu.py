@@ -137,3 +137,29 @@ def test_a_piece_of_keys_of_nan_behind_what_a_row_sees(dtype):
     for num_ctas in (0, 1, 2, 5):
         out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
         assert err == 0 and torch.isnan(out).all() and torch.isnan(lse).all(), num_ctas
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n,num_ctas", [(9000, 4, 0), (300, 200, 0), (300, 200, 1)])
+def test_rows_made_anew_leave_out_scores_of_minus_infinity(T, n, num_ctas, dtype):
+    """Keys of -infinity, the first one's among them, weigh nothing, whether or not the rows are
+    made anew for a V that they do not see."""
+    kc, vc, table = ref.make_cache([T], 2, dtype, 65)
+    q = queries(n, 8, dtype, 66)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    for t in (0, 1, 70):
+        kc[table[0, t // 16].long(), :, t % 16, 3] = -math.inf
+    plain, lse0, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0
+    k64, v64 = (ref.cached(x, table, 0, T) for x in (kc, vc))
+    left = torch.tensor([t for t in range(T) if t not in (0, 1, 70)], device="cuda")
+    sees = torch.stack([(left < T - (n - 1 - i)).sum() for i in range(n)]).repeat_interleave(4)
+    vc[table[0, (T - 1) // 16].long(), :, (T - 1) % 16, 50] = math.nan
+    out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0 and torch.equal(lse, lse0)
+    for h in range(2):
+        rows = q[:, 4 * h:4 * h + 4].double().reshape(4 * n, ref.D)
+        want = ref.attend(rows, k64[h, left], v64[h, left], sees, 1 / math.sqrt(ref.D))
+        want = [x.view(n, 4, *x.shape[1:]) for x in want]
+        ref.check_attention(plain[:, 4 * h:4 * h + 4], lse0[:, 4 * h:4 * h + 4], want, T)
+        ref.check_attention(out[:-1, 4 * h:4 * h + 4], lse[:-1, 4 * h:4 * h + 4], [x[:-1] for x in want], T)
