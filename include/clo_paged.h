@@ -123,7 +123,9 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  * zeros and -inf for a row that sees no token.  Any mixture of prompts, chunks
  * of prompts and decoding requests is one call.  Nothing behind the last token a
  * row sees enters its result, whatever it holds; fp16 outputs beyond +-65504 are
- * +-65504.
+ * +-65504.  bf16 values may be as large as the type holds.  Rows whose first sums are not
+ * finite, by a value that they do not see or by values from 2^90 on, are made anew token by
+ * token: right, but slow.
  * q:           [N][Hq][d] of type `dtype`, rows q_stride elements apart (a
  *              multiple of 8, at least Hq * d).
  * kc, vc:      [num_blocks][Hkv][16][d] of type `dtype` with the strides
@@ -296,7 +298,8 @@ clo_status clo_paged_block_select(const clo_paged_block_select_args* args, cudaS
  *            lse: [B][Hq] fp32 or NULL.
  * workspace: >= clo_paged_chunk_workspace_size(Hq, Hkv, d, num_ctas) bytes,
  *            16-byte aligned.
- * Sums are in fp32; the weights are rounded to `dtype` for the product with V.
+ * Sums are in fp32; the weights are rounded to `dtype` for the product with V.  Large bf16
+ * values: as for clo_paged_chunk_attn.
  * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, B * Hq < 2^29,
  * num_blocks <= 2^26, max_blocks <= 2^20, B * Hkv * n_sel < 2^31, scale > 0.
  */

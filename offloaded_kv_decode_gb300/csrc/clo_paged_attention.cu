@@ -55,7 +55,11 @@
 // last token are zeroed as they are brought in; one between a row's last token and
 // the item's can only make the row's result not finite, so such results are looked at
 // again at the end and made anew by paged_row where a V that they do not see is
-// not finite (nothing of this runs on finite data).
+// not finite (nothing of this runs on results that are finite).
+//
+// Values near bf16's largest.  Weights of up to 2^14 times 2^24 values keep sums in fp32
+// finite below 2^90 alone.  So a bf16 result that is not finite is made anew too where a V
+// from 2^90 on is among what its item goes over.
 //
 // Every wait has a limit (about 2 s); one that runs out ends the CTA's work in order.
 #include <math.h>
@@ -302,6 +306,10 @@ __device__ __forceinline__ bool row_of(const PagedAttnArgs& a, int j, int tokens
     token = 2 * j * a.tt + i;
     return t < a.tt && i < tokens;
 }
+
+// Whether results that are not finite may be due to more than what their rows see; with fp16
+// values and the same tokens for all rows they are not.  (Sums of weights that are NaN always are.)
+__host__ __device__ constexpr bool ch_again(bool bf16, bool sparse) { return bf16 || !sparse; }
 
 // ---------------------------------------------------------------- small parts
 
@@ -775,7 +783,7 @@ struct RowSoftmax {
         if (!valid) return;
         if (whole) {
             if (a.lse != nullptr) a.lse[place] = none ? -INFINITY : (ref + log2f(sum)) * LN2;
-            if (!SPARSE && odd != 0.f) *reinterpret_cast<volatile int*>(&sm->again) = 1;
+            if (ch_again(BF16, SPARSE) && odd != 0.f && sum == sum) *reinterpret_cast<volatile int*>(&sm->again) = 1;
         } else {
             ws.ml[slot * CHUNK_ROWS + row] = make_float2(ref, bad ? -1.f : sum);
         }
@@ -1152,20 +1160,94 @@ __device__ bool hidden_odd(const PagedAttnArgs& a, int r, int h, int from, int t
     return __any_sync(FULL_MASK, odd);
 }
 
+// Whether a V from place `from` on among the first `sees` tokens (sparse: of the selected
+// places) is finite and 2^90 or larger (exponents 217 to 254); the block.
+template <bool BF16, bool SPARSE>
+__device__ __noinline__ bool large_values(const PagedAttnArgs& a, int r, int h, int from, int sees) {
+    const int lane = threadIdx.x & 31, places = paged_places<SPARSE>(a, sees);
+    bool large = false;
+#pragma unroll 1
+    for (int first = from + (threadIdx.x & ~31); first < places; first += MERGE_THREADS) {
+        const int mine = first + lane < places ? paged_place<SPARSE>(a, r, h, sees, first + lane) : 0;
+#pragma unroll 1
+        for (int p = 0; p < min(places - first, 32); ++p) {
+            const int at = __shfl_sync(FULL_MASK, mine, p);
+            if (at <= 0) continue;
+            const uint8_t* v = a.vc + static_cast<long long>(at / 32) * a.kv_block + h * a.kv_head + (lane & 15) * 16;
+            uint4 x[PG_BLOCK / 2];
+#pragma unroll
+            for (int i = 0; i < PG_BLOCK / 2; ++i) {
+                const int t = 2 * i + (lane >> 4);  // (a row behind the last token repeats the first)
+                x[i] = *reinterpret_cast<const uint4*>(v + (t < at % 32 ? t : 0) * a.kv_token);
+            }
+#pragma unroll
+            for (int i = 0; i < PG_BLOCK / 2; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) large |= ((w[c] & 0x7fffu) - 0x6c80u < 0x1300u) | ((w[c] >> 16 & 0x7fffu) - 0x6c80u < 0x1300u);
+            }
+        }
+    }
+    return __syncthreads_or(large) != 0;
+}
+
 // Makes a row whose result is not finite anew if that may come from what it does not
-// see.  `mine`: this lane's channels are written.
-template <bool BF16>
+// see, or from values so `large` that their sums were not finite.  `mine`: this lane's
+// channels are written.
+template <bool BF16, bool SPARSE>
 __device__ __noinline__ void look_again(const PagedAttnArgs& a, const PagedReq& q, int r, int h, int j, int token, int g, int lane,
-                                        bool mine) {
-    if (hidden_odd<BF16>(a, r, h, paged_sees<false>(q, token), item_sees<false>(a, q, j), lane))
-        paged_row<BF16, false>(a, r, q, token, h * a.G + g, lane, mine);
+                                        bool mine, bool large) {
+    if constexpr (!SPARSE) large = large || hidden_odd<BF16>(a, r, h, paged_sees<false>(q, token), item_sees<false>(a, q, j), lane);
+    if (large) paged_row<BF16, SPARSE>(a, r, q, token, h * a.G + g, lane, mine);
+}
+
+// Whole items of a CTA's share that have results that are not finite: the block's rows of each.
+// (Apart from the kernel, whose registers it would take.)
+template <bool BF16, bool SPARSE>
+__device__ __noinline__ void look_at_items(const PagedAttnArgs& a, const int4* desc) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 s = desc[DESC_START], e = desc[DESC_END];
+    Walk<SPARSE> walk(ChunkPos{s.x, s.y, s.z, s.w}, ChunkPos{e.x, e.y, e.z, e.w});
+    Piece p;
+    int r = -1, h = 0, looked = 0;  // places of request r and head h that were looked at
+    bool large = false;
+    while (walk.next(a, p)) {
+        if (!p.whole()) continue;
+        if (p.r != r || p.h != h) {
+            r = p.r;
+            h = p.h;
+            looked = 0;
+            large = false;
+        }
+        // (A warp has at most 8 rows: the grid has 4 blocks an item or more.)
+        const int row0 = blockIdx.y * (MERGE_THREADS / 32) + warp, step = gridDim.y * (MERGE_THREADS / 32);
+        unsigned odd = 0;
+        int token, g;
+#pragma unroll 1
+        for (int k = 0; row0 + k * step < CHUNK_ROWS; ++k) {
+            if (!row_of(a, p.j, p.tokens, row0 + k * step, token, g)) continue;
+            const size_t place = (static_cast<size_t>(p.q.row0) + token) * a.Hq + p.h * a.G + g;
+            const uint2 w = *reinterpret_cast<const uint2*>(a.out + place * PG_ROW + lane * 8);
+            const float2 x = pg_unpack<BF16>(w.x), y = pg_unpack<BF16>(w.y);
+            if (__any_sync(FULL_MASK, !(pg_finite(x.x) && pg_finite(x.y) && pg_finite(y.x) && pg_finite(y.y)))) odd |= 1u << k;
+        }
+        if (BF16 && __syncthreads_or(odd) && !large) {
+            // (A request's later items see the tokens of the earlier ones and more.)
+            large = large_values<BF16, SPARSE>(a, r, h, looked, SPARSE ? p.q.ctx : p.sees);
+            looked = p.sees / PG_BLOCK;
+        }
+        for (; odd != 0; odd &= odd - 1) {
+            row_of(a, p.j, p.tokens, row0 + (__ffs(odd) - 1) * step, token, g);
+            look_again<BF16, SPARSE>(a, p.q, p.r, p.h, p.j, token, g, lane, true, large);
+        }
+    }
 }
 
 // Block (c, y) joins the pieces of the item that starts in CTA c's share and ends in a
 // later one's, for ROWS of its rows and 4 * NI of the channels.  Lanes are rows, and with ROWS
 // = 8 four subsets of the pieces; a warp holds 4 channels of its rows, NI / 8 times.
 template <bool BF16, bool SPARSE, int ROWS, int NI>
-__global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedAttnArgs a, const ChunkWs ws, int ctas) {
+__global__ void __launch_bounds__(MERGE_THREADS, SPARSE ? 3 : 2) paged_merge_kernel(const PagedAttnArgs a, const ChunkWs ws, int ctas) {
     constexpr int SUBS = 32 / ROWS, K = NI / 8, AHEAD = 8 / K;
     __shared__ int odd_row[ROWS];
     __shared__ uint2 result[ROWS][NI + 1];
@@ -1251,7 +1333,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
                     odd += (y[0] + y[1] + y[2] + y[3]) * 0.f;
                     result[lane][warp + 8 * k] = make_uint2(pg_pack_out<BF16>(y[0], y[1]), pg_pack_out<BF16>(y[2], y[3]));
                 }
-                if (odd != 0.f && valid) odd_row[lane] = 1;
+                if (odd != 0.f && valid && l == l) odd_row[lane] = 1;
                 if (a.lse != nullptr && valid && warp == 0 && ib == 0)
                     a.lse[place_of(token, g)] = none ? -INFINITY : (m + log2f(l)) * LN2;
             }
@@ -1261,34 +1343,20 @@ __global__ void __launch_bounds__(MERGE_THREADS) paged_merge_kernel(const PagedA
                 if (row_of(a, e.z, tokens, row0 + x / NI, t, gg))
                     reinterpret_cast<uint2*>(a.out + place_of(t, gg) * PG_ROW)[ib * NI + x % NI] = result[x / NI][x % NI];
             }
-            if constexpr (!SPARSE) {
-                __syncthreads();  // (the rows made anew are written after these)
+            if constexpr (ch_again(BF16, SPARSE)) {
+                // (The rows made anew are written after these.)
+                const bool some = __syncthreads_or(threadIdx.x < ROWS && odd_row[threadIdx.x] != 0) != 0;
+                const bool large = BF16 && some && large_values<BF16, SPARSE>(a, e.x, e.y, 0, SPARSE ? q.ctx : item_sees<SPARSE>(a, q, e.z));
                 for (int x = warp; x < ROWS; x += MERGE_THREADS / 32) {
                     int t, gg;
                     if (odd_row[x] != 0 && row_of(a, e.z, tokens, row0 + x, t, gg))
-                        look_again<BF16>(a, q, e.x, e.y, e.z, t, gg, lane, lane / NI == ib);
+                        look_again<BF16, SPARSE>(a, q, e.x, e.y, e.z, t, gg, lane, lane / NI == ib, large);
                 }
             }
         }
     }
-    if (!SPARSE && flags.w != 0) {
-        // Whole items of CTA c with results that are not finite: this block's rows of each.
-        const int4 s = desc[DESC_START];
-        Walk<SPARSE> walk(ChunkPos{s.x, s.y, s.z, s.w}, ChunkPos{e.x, e.y, e.z, e.w});
-        Piece p;
-        while (walk.next(a, p)) {
-            if (!p.whole()) continue;
-            for (int row = blockIdx.y * (MERGE_THREADS / 32) + warp; row < CHUNK_ROWS; row += gridDim.y * (MERGE_THREADS / 32)) {
-                int token, g;
-                if (!row_of(a, p.j, p.tokens, row, token, g)) continue;
-                const size_t place = (static_cast<size_t>(p.q.row0) + token) * a.Hq + p.h * a.G + g;
-                const uint2 w = *reinterpret_cast<const uint2*>(a.out + place * PG_ROW + lane * 8);
-                const float2 x = pg_unpack<BF16>(w.x), y = pg_unpack<BF16>(w.y);
-                const bool fine = pg_finite(x.x) && pg_finite(x.y) && pg_finite(y.x) && pg_finite(y.y);
-                if (!__all_sync(FULL_MASK, fine)) look_again<BF16>(a, p.q, p.r, p.h, p.j, token, g, lane, true);
-            }
-        }
-    }
+    if constexpr (ch_again(BF16, SPARSE))
+        if (flags.w != 0) look_at_items<BF16, SPARSE>(a, desc);
 }
 
 // ---------------------------------------------------------------- host

@@ -6,7 +6,7 @@ import torch
 
 import offloaded_kv_decode_gb300 as clo
 import paged_ref as ref
-from test_paged16_attention_gpu import chunk, queries, sparse
+from test_paged16_attention_gpu import chunk, queries, sparse, sparse_ref
 from test_paged16_cache_gpu import rand, random_bounds, select
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +163,77 @@ def test_rows_made_anew_leave_out_scores_of_minus_infinity(T, n, num_ctas, dtype
         want = [x.view(n, 4, *x.shape[1:]) for x in want]
         ref.check_attention(plain[:, 4 * h:4 * h + 4], lse0[:, 4 * h:4 * h + 4], want, T)
         ref.check_attention(out[:-1, 4 * h:4 * h + 4], lse[:-1, 4 * h:4 * h + 4], [x[:-1] for x in want], T)
+
+
+def wide_values(vc, seed):
+    """Random values of one size in each quarter of the channels: 2^125 at most 2^127, 2^100, 1 and 2^-100."""
+    v = torch.randn(vc.shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+    size = torch.tensor([2.0 ** 125, 2.0 ** 100, 1.0, 2.0 ** -100], dtype=torch.float64).repeat_interleave(32)
+    top = torch.finfo(torch.bfloat16).max
+    vc.copy_((v * size).clamp(-top, top).to(torch.bfloat16))
+
+
+def check_wide(out, lse, want, tokens):
+    """As ref.check_attention (bf16), without a part that does not scale with the values: bf16
+    weights as small as 2^-126 count, and 2^-149 times 2^14 is far below 2^-100."""
+    o, e, mag, size = want
+    u = ref.half_step(out.dtype)
+    d = 2.0 ** -19 * size + 2.0 ** -20
+    tol = (2 * u + 2 * d[..., None] + tokens / 8 * 2.0 ** -23) * mag + u * o.abs()
+    assert torch.isfinite(out).all()
+    assert ((out.double() - o).abs() <= tol).all()
+    ref.check_attention(torch.zeros_like(out), lse, (torch.zeros_like(o), e, mag, size), tokens)
+
+
+@pytest.mark.parametrize("T,n,G,num_ctas", [(1, 1, 4, 0), (40, 40, 1, 0), (333, 50, 4, 0), (333, 50, 5, 1), (9000, 3, 4, 0), (9000, 3, 4, 1),
+                                            (3000, 100, 8, 0), (700, 700, 3, 3)])
+def test_large_bf16_values(T, n, G, num_ctas):
+    """bf16 values near its largest, where sums of weights times values pass fp32's: in whole
+    items and in ones that the joining kernel puts together."""
+    dtype = torch.bfloat16
+    kc, vc, table = ref.make_cache([T], 2, dtype, 71)
+    q = queries(n, 2 * G, dtype, 72)
+    top = torch.finfo(dtype).max
+    for values in ("wide", "top", "signs"):
+        if values == "wide":
+            wide_values(vc, T)
+        elif values == "top":
+            vc.fill_(top)
+        else:
+            vc[:, :, ::2] *= -1
+        out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+        assert err == 0
+        check_wide(out, lse, ref.chunk_attention(q, kc, vc, table, [T], [n]), T)
+        if values == "top":
+            assert torch.all(out == top)
+    # beside an infinity that is seen, and a NaN that is not
+    wide_values(vc, T)
+    want = ref.chunk_attention(q, kc, vc, table, [T], [n])
+    vc[table[0, 0].long(), :, 0, 5] = math.inf
+    if T > 1:
+        vc[table[0, (T - 1) // 16].long(), 0, (T - 1) % 16, 9] = math.nan
+    out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0 and not torch.isfinite(out[..., 5]).any()
+    rest = [c for c in range(ref.D) if c not in (5, 9)]
+    check_wide(out[..., rest], lse, (want[0][..., rest], want[1], want[2][..., rest], want[3]), T)
+    if T > 1 and n > 1:
+        assert torch.isnan(out[-1, :G, 9]).all()
+        check_wide(out[:-1, :, 9:10], None, (want[0][:-1, :, 9:10], None, want[2][:-1, :, 9:10], want[3][:-1]), T)
+
+
+@pytest.mark.parametrize("G,Hkv,n_sel,num_ctas", [(4, 2, 1, 0), (1, 3, 7, 0), (5, 2, 20, 1), (8, 1, 300, 0), (2, 2, 64, 3)])
+def test_large_bf16_values_of_selected_blocks(G, Hkv, n_sel, num_ctas):
+    dtype, lens = torch.bfloat16, [1, 900, 16 * n_sel, 16 * n_sel + 5, 33]
+    kc, vc, table = ref.make_cache(lens, Hkv, dtype, n_sel)
+    wide_values(vc, n_sel)
+    g = torch.Generator().manual_seed(n_sel)
+    sel = torch.full((5, Hkv, n_sel), -1, dtype=torch.int32)
+    for r, T in enumerate(lens):
+        for h in range(Hkv):
+            cols = torch.randperm(ref.blocks_of(T), generator=g)[:n_sel].to(torch.int32)
+            sel[r, h, :len(cols)] = cols
+    sel = sel.cuda()
+    q = queries(5, G * Hkv, dtype, n_sel + 1)
+    out, lse, err = sparse(q, kc, vc, table, lens, sel, num_ctas)
+    assert err == 0
+    check_wide(out, lse, sparse_ref(q, kc, vc, table, lens, sel), max(lens))
