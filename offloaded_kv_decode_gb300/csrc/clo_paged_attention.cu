@@ -1414,7 +1414,9 @@ static clo_status run_paged(PagedAttnArgs a, void* workspace, const clo_attn_opt
     // blocks and lanes.
     const long long rows = SPARSE ? a.G : static_cast<long long>(a.N) * a.G;
     const bool few = SPARSE || (rows <= 64 && a.N <= a.tt);
-    const auto merge = few ? paged_merge_kernel<BF16, SPARSE, 8, 8> : paged_merge_kernel<BF16, SPARSE, 32, 32>;
+    auto merge = paged_merge_kernel<BF16, SPARSE, 8, 8>;
+    if constexpr (!SPARSE)
+        if (!few) merge = paged_merge_kernel<BF16, false, 32, 32>;
     const unsigned y = few ? static_cast<unsigned>((rows + 7) / 8) * 4 : CHUNK_ROWS / 32;
     if (!prepare_kernel(reinterpret_cast<const void*>(main), CH_SMEM) ||
         !prepare_kernel(reinterpret_cast<const void*>(merge), 0))
