@@ -253,7 +253,8 @@ size_t clo_paged_select_workspace_size(int B, int Hkv, int max_blocks);
  * block_table, ctx_len: as for clo_paged_decode_attn.  A block out of range sets
  *              CLO_FLAG_BAD_INDEX and counts as one without a finite scale (what
  *              attends to it reports it); a bad length sets CLO_FLAG_BAD_CTX and
- *              selects nothing.
+ *              selects nothing.  A copy that does not end within about 2 s sets
+ *              CLO_FLAG_TIMEOUT; sel is then undefined.
  * sel:         [B][Hkv][n_sel] int32 output: columns of block_table, ascending,
  *              then -1.
  * workspace:   >= clo_paged_select_workspace_size(B, Hkv, max_blocks) bytes, 16-byte

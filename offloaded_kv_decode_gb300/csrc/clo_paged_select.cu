@@ -247,7 +247,10 @@ __global__ void __launch_bounds__(SCORE_THREADS, 3) block_score_kernel(const Sel
         codes[warp][1][lane] = neg;
     }
     __syncthreads();
-    if (!mbar_wait(b, 0) && lane == 0) report_error(a.err_flag, CLO_FLAG_TIMEOUT);
+    if (!mbar_wait(b, 0)) {  // once more, so that no copy comes after the CTA's end
+        if (lane == 0) report_error(a.err_flag, CLO_FLAG_TIMEOUT);
+        mbar_wait(b, 0);
+    }
     const int col = first + (threadIdx.x >> 3);
     const uint8_t* rec = records + (threadIdx.x >> 3) * bytes;
 #pragma unroll 2
