@@ -6,7 +6,7 @@ import torch
 
 import offloaded_kv_decode_gb300 as clo
 import paged_ref as ref
-from test_paged16_attention_gpu import chunk, queries, sparse, sparse_ref
+from test_paged16_attention_gpu import chunk, offsets_of, queries, sparse, sparse_ref
 from test_paged16_cache_gpu import rand, random_bounds, select
 
 pytestmark = pytest.mark.gpu
@@ -165,6 +165,25 @@ def test_rows_made_anew_leave_out_scores_of_minus_infinity(T, n, num_ctas, dtype
         ref.check_attention(out[:-1, 4 * h:4 * h + 4], lse[:-1, 4 * h:4 * h + 4], [x[:-1] for x in want], T)
 
 
+# ---------------------------------------------------------------- the largest values
+
+@pytest.mark.parametrize("T,n,num_ctas", [(333, 50, 0), (333, 50, 1), (9000, 3, 0), (9000, 3, 1), (5000, 130, 0), (100, 100, 0)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_values_of_65504_stay_finite(sign, T, n, num_ctas):
+    """In whole items and in ones that the joining kernel puts together."""
+    dtype = torch.float16
+    kc, vc, table = ref.make_cache([T], 1, dtype, 41)
+    vc.fill_(sign * 65504.0)
+    q = queries(n, 4, dtype, 42)
+    out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0 and torch.isfinite(out).all() and (out.abs() <= 65504).all()
+    ref.check_attention(out, lse, ref.chunk_attention(q, kc, vc, table, [T], [n]), T)
+    vc[..., ::2] *= -1
+    out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0 and torch.isfinite(out).all() and (out.abs() <= 65504).all()
+    ref.check_attention(out, lse, ref.chunk_attention(q, kc, vc, table, [T], [n]), T)
+
+
 def wide_values(vc, seed):
     """Random values of one size in each quarter of the channels: 2^125 at most 2^127, 2^100, 1 and 2^-100."""
     v = torch.randn(vc.shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
@@ -221,6 +240,53 @@ def test_large_bf16_values(T, n, G, num_ctas):
         check_wide(out[:-1, :, 9:10], None, (want[0][:-1, :, 9:10], None, want[2][:-1, :, 9:10], want[3][:-1]), T)
 
 
+@pytest.mark.parametrize("num_ctas", [0, 5])
+def test_large_bf16_values_of_some_requests(num_ctas):
+    """Among many requests, in a cache whose heads lie side by side, captured and replayed: the
+    others keep the bits that they have beside values of usual size."""
+    g = torch.Generator().manual_seed(75)
+    n_new = torch.randint(0, 5, (60,), generator=g).tolist()
+    n_new[7], n_new[31], n_new[32] = 300, 40, 1
+    lens = [n + int(torch.randint(0, 300, (1,), generator=g)) for n in n_new]
+    lens[32] = 6000
+    dtype, Hkv, Hq = torch.bfloat16, 2, 10
+    kc, vc, table = ref.make_cache(lens, Hkv, dtype, 76)
+    q = queries(sum(n_new), Hq, dtype, 77)
+    plain, lse0, err = chunk(q, kc, vc, table, lens, n_new, num_ctas)
+    assert err == 0
+    wide = vc.clone()
+    wide_values(wide, 78)
+    large = [r for r in range(60) if r % 3 == 1 or r == 32]
+    for r in large:
+        ids = table[r, :ref.blocks_of(lens[r])].long()
+        vc[ids] = wide[ids]
+    k2, v2 = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (kc, vc))
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(clo.clo_paged_chunk_workspace_size(Hq, Hkv, num_ctas=num_ctas), dtype=torch.uint8, device="cuda")
+    call = clo.prepare_paged_chunk_attn(q, k2, v2, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), offsets_of(n_new), out,
+                                        ws, lse=lse, err_flag=err, num_ctas=num_ctas)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    first = out.clone()
+    for _ in range(2):
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and torch.equal(out, first) and torch.equal(lse, lse0)
+    want = ref.chunk_attention(q, kc, vc, table, lens, n_new)
+    rows = offsets_of(n_new).tolist()
+    for r in range(60):
+        s = slice(rows[r], rows[r + 1])
+        if r not in large:
+            assert torch.equal(out[s], plain[s])
+        elif n_new[r]:
+            check_wide(out[s], lse[s], tuple(x[s] for x in want), max(lens))
+
+
 @pytest.mark.parametrize("G,Hkv,n_sel,num_ctas", [(4, 2, 1, 0), (1, 3, 7, 0), (5, 2, 20, 1), (8, 1, 300, 0), (2, 2, 64, 3)])
 def test_large_bf16_values_of_selected_blocks(G, Hkv, n_sel, num_ctas):
     dtype, lens = torch.bfloat16, [1, 900, 16 * n_sel, 16 * n_sel + 5, 33]
@@ -237,3 +303,26 @@ def test_large_bf16_values_of_selected_blocks(G, Hkv, n_sel, num_ctas):
     out, lse, err = sparse(q, kc, vc, table, lens, sel, num_ctas)
     assert err == 0
     check_wide(out, lse, sparse_ref(q, kc, vc, table, lens, sel), max(lens))
+    if n_sel > 1:
+        sel[1:3] = sel[1:3, :, :1]  # one column as often as there is room
+        out, lse, err = sparse(q, kc, vc, table, lens, sel, num_ctas)
+        assert err == 0
+        check_wide(out, lse, sparse_ref(q, kc, vc, table, lens, sel), max(lens))
+
+
+# ---------------------------------------------------------------- outputs at any 16-byte boundary
+
+@pytest.mark.parametrize("T,n,num_ctas", [(200, 150, 0), (3000, 2, 0), (700, 700, 0), (700, 700, 3)])
+def test_outputs_at_a_16_byte_boundary(T, n, num_ctas):
+    dtype = torch.bfloat16
+    kc, vc, table = ref.make_cache([T], 2, dtype, 43)
+    q = queries(n, 8, dtype, 44)
+    want, _, _ = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    room = torch.full((q.numel() + 16,), 5.0, dtype=dtype, device="cuda")
+    out = room[8:8 + q.numel()].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    ws = torch.empty(clo.clo_paged_chunk_workspace_size(8, 2, num_ctas=num_ctas), dtype=torch.uint8, device="cuda")
+    clo.clo_paged_chunk_attn(q, kc, vc, table, torch.tensor([T], dtype=torch.int32, device="cuda"), offsets_of([n]), out, ws,
+                             num_ctas=num_ctas)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.all(room[:8] == 5) and torch.all(room[-8:] == 5)
