@@ -499,6 +499,8 @@ size_t clo_paged_workspace_size(int B, int Hq, int Hkv, int d, int num_ctas);
  * block_table: [B][max_blocks] int32 entries in [0, num_blocks).
  * ctx_len:     [B] int32 in [0, max_blocks*block_size]; 0 gives zeros.
  * out, lse, workspace, err_flag, opts: as for clo_hybrid_decode_attn.
+ * (clo_paged_chunk_attn in clo_paged.h computes this too, in bf16 as well and
+ * for more tokens a request, and says which of the two is faster where.)
  * Requires block_size == 16, G <= 8, d == 128, B <= 4096,
  * B*Hkv*max_blocks < 2^31.
  */

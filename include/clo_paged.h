@@ -149,11 +149,17 @@ size_t clo_paged_chunk_workspace_size(int Hq, int Hkv, int d, int num_ctas);
  *              product that does not end within about 2 s, which says that the GPU
  *              is in trouble, sets CLO_FLAG_TIMEOUT; the outputs are then undefined.
  * opts:        optional: num_ctas, at most 4095; the events bracket the main kernel.
+ * One fp16 token a request over a contiguous cache is also what clo_paged_decode_attn
+ * computes.  With 4 query heads a KV head or more this call is the faster one (1.05 to 2.8
+ * times) up to B * Hkv of 2000, but for a few thousand cached tokens in all, and for contexts
+ * of several thousand tokens; with 1, or from there on where contexts are below 1000 tokens,
+ * that one is (up to 2.2 times).  With 2 or 3 they are about equal.
  * Scores and sums are in fp32; the weights are rounded to `dtype` for the product
- * with V, in fp16 after a factor that keeps what is 2^-31 of the largest; in tiles of
- * rows (a request's new tokens in groups of floor(128 Hkv / Hq)) whose last one sees at
- * most 128 tokens, to twice the bits.  The same call on the same kind of GPU gives the
- * same bits each time.
+ * with V (which may take a result off by half a step of `dtype` of the values' size,
+ * beside its own rounding), in fp16 after a factor that keeps what is 2^-31 of the
+ * largest; in tiles of rows (a request's new tokens in groups of floor(128 Hkv / Hq))
+ * whose last one sees at most 128 tokens, to twice the bits.  The same call on the same
+ * kind of GPU gives the same bits each time.
  * Requires d == 128, block_size == 16, Hq / Hkv <= 8, B <= 4096, N * Hq < 2^29,
  * max_blocks <= 2^20, num_blocks <= 2^26, scale > 0, strides of at most 2^38 (kv_token
  * 2^34) and a cache that spans less than 2^31 times the greatest common divisor of
@@ -209,8 +215,9 @@ size_t clo_paged_bounds_bytes(int block_size, int d);
  * kc:       [num_blocks][Hkv][16][d] of type `dtype`, contiguous.
  * slot_map: [N] int32.  A request's new tokens follow one another, as
  *           clo_paged_plan writes them: the last entry of a run of consecutive
- *           slots within one block names the block and the last of its tokens.
- *           Negative slots are skipped, any other outside [0, num_blocks * 16) too
+ *           slots within one block names the block and the last of its tokens (a
+ *           block's new tokens make one run; where two name a block its record is
+ *           undefined).  Negative slots are skipped, any other outside [0, num_blocks * 16) too
  *           (and CLO_FLAG_BAD_INDEX).
  * bounds:   [num_blocks][Hkv][272] uint8, 16-byte aligned; records of other blocks
  *           are left as they are.

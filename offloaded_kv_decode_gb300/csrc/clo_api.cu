@@ -14,7 +14,7 @@ extern "C" const char* clo_status_string(clo_status s) {
     return "CLO_ERR_UNKNOWN";
 }
 
-extern "C" int clo_version(void) { return 10500; }  // 1.5.0
+extern "C" int clo_version(void) { return 10501; }  // 1.5.1
 
 extern "C" clo_status clo_check_error_flag(int32_t host_err_flag) {
     if (host_err_flag == 0) return CLO_OK;

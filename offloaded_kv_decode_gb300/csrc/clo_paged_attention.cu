@@ -28,9 +28,9 @@
 // Q K^T reads both operands from shared memory) and its softmax (1130 clocks for 128 scores
 // a thread: exponentials, conversions and sums together), with about 700 clocks of
 // hand-overs between the two; 1.5 us a pair of tiles.  4096 tokens after 61440 with 32
-// query heads take 2.71 to 2.90 ms from idle (1.47 to 1.57 PFLOP/s, 0.78 to 0.83 of the measured
-// burst rate of bf16 products) and 3.1 to 3.2 ms back to back, under the power limit (1.35, 0.78
-// of the sustained rate).  Few rows: HBM; 64 requests of 8001 tokens and 8 KV heads, a token
+// query heads take 2.71 to 2.93 ms from idle (1.45 to 1.57 PFLOP/s, 0.77 to 0.83 of the measured
+// burst rate of bf16 products; the tensor pipe is busy 72% of the time) and 3.2 to 3.4 ms back to
+// back, under the power limit (1.25 to 1.33, 0.73 to 0.77 of the sustained rate).  Few rows: HBM; 64 requests of 8001 tokens and 8 KV heads, a token
 // each, take 308 us (6.8 TB/s), one of 128K 90 us (6.0).  Short calls: about 3 us until the
 // first copies, 2 a piece's end, 4 for the join.
 //   Tried and not kept: two warpgroups a stream, 64 scores a thread (+4%: the exponentials

@@ -424,8 +424,11 @@ extern "C" clo_status clo_paged_block_bounds(const clo_paged_block_bounds_args* 
     if (r.d != PG_D || r.block_size != PG_BLOCK || r.Hkv > 65535 || r.num_blocks > (1 << 26)) return CLO_ERR_UNSUPPORTED;
     if (r.N == 0) return CLO_OK;
     BoundsArgs a{static_cast<const uint8_t*>(r.kc), r.slot_map, r.bounds, r.err_flag, r.N, r.Hkv, r.num_blocks, 0};
-    // A warp looks at 16 tokens, about one block of a prompt; at one where that
-    // leaves few warps (a decode step: each token ends a block).
+    // A warp looks at 16 tokens, about one block of a prompt; at one where that leaves few
+    // warps, for the sake of a decode step, in which each token ends a block.  Us with 1 and
+    // with 16 tokens a warp, by tokens times heads (1, 8 or 32 heads, the same within 2%):
+    //   a token a block   2048: 3.3, 16.2   16384: 8.6, 19.1   32768: 16.6, 33   65536: 39, 51   131072: 74, 79
+    //   a prompt          2048: 2.2, 2.1    16384: 4.8, 2.6    32768: 9.1, 3.4   65536: 17, 4.3  131072: 34, 5.5
     a.tokens = static_cast<long long>(r.N) * r.Hkv <= 32768 ? 1 : 16;
     const long long warps = (static_cast<long long>(r.N) + a.tokens - 1) / a.tokens;
     const unsigned grid = static_cast<unsigned>((warps + BOUNDS_THREADS / 32 - 1) / (BOUNDS_THREADS / 32));
