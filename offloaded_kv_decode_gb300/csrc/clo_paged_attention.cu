@@ -30,9 +30,10 @@
 // hand-overs between the two; 1.5 us a pair of tiles.  4096 tokens after 61440 with 32
 // query heads take 2.71 to 2.93 ms from idle (1.45 to 1.57 PFLOP/s, 0.77 to 0.83 of the measured
 // burst rate of bf16 products; the tensor pipe is busy 72% of the time) and 3.2 to 3.4 ms back to
-// back, under the power limit (1.25 to 1.33, 0.73 to 0.77 of the sustained rate).  Few rows: HBM; 64 requests of 8001 tokens and 8 KV heads, a token
-// each, take 308 us (6.8 TB/s), one of 128K 90 us (6.0).  Short calls: about 3 us until the
-// first copies, 2 a piece's end, 4 for the join.
+// back, under the power limit (1.25 to 1.33, 0.73 to 0.77 of the sustained rate).  Few rows:
+// HBM; 64 requests of 8001 tokens and 8 KV heads, a token each, take 308 us (6.8 TB/s), one of
+// 128K 89 us (6.0).  Short calls: about 3 us until the first copies, 2 a piece's end, 4 for the
+// join.
 //   Tried and not kept: two warpgroups a stream, 64 scores a thread (+4%: the exponentials
 // take as long, and more warps wait); the maximum beside the weights instead of before them
 // (+4%); the first half of a tile's weights handed over early (+3%); one lane of a warp, or
@@ -1191,7 +1192,7 @@ __device__ __noinline__ bool large_values(const PagedAttnArgs& a, int r, int h, 
     return __syncthreads_or(large) != 0;
 }
 
-// Makes a row whose result is not finite anew if that may come from what it does not
+// Makes what is not finite of a row's result anew if that may come from what the row does not
 // see, or from values so `large` that their sums were not finite.  `mine`: this lane's
 // channels are written.
 template <bool BF16, bool SPARSE>

@@ -96,10 +96,11 @@ __device__ __forceinline__ uint32_t pg_pack_out(float lo, float hi) {
 
 // The attention of one query row by one warp, token after token in fp32: lane l
 // holds channels 4l .. 4l + 3.  Slow, and without any value of a token that the
-// row does not see.  `mine`: this lane's channels are written.  The row's lse is left:
-// values do not enter it, and blocks that make different channels anew share it.
-// bf16 values reach 2^128, and so would sums of a few: once one passes 2^100, a lane goes on
-// in units of 2^64, in which a sum of 2^24 values stays below 2^88.
+// row does not see.  `mine`: of this lane's channels those that are not finite so far are
+// written (what made one so stays in it, and leaves the others right).  The row's lse is
+// left: values do not enter it, and blocks that make different channels anew share it.
+// bf16 values reach 2^128, and so would sums of a few: a channel whose sum passes 2^100 goes
+// on in units of 2^64, in which a sum of 2^24 values stays below 2^88.
 template <bool BF16, bool SPARSE>
 __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const PagedReq& req, int i, int head, int lane, bool mine) {
     const int h = head / a.G;
@@ -107,7 +108,7 @@ __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const Page
     const uint2 qw = *reinterpret_cast<const uint2*>(a.q + static_cast<long long>(row) * a.q_stride + head * PG_ROW + lane * 8);
     const float2 q0 = pg_unpack<BF16>(qw.x), q1 = pg_unpack<BF16>(qw.y);
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    float unit = 1.f;  // of what is added to o, 1 or 2^-64
+    float unit[4] = {1.f, 1.f, 1.f, 1.f};  // of what is added to o, 1 or 2^-64
     const int sees = paged_sees<SPARSE>(req, i), places = paged_places<SPARSE>(a, sees);
     bool bad = false;
     for (int p = 0; p < places; ++p) {
@@ -129,15 +130,13 @@ __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const Page
             const uint2 vw = *reinterpret_cast<const uint2*>(a.vc + base + t * a.kv_token);
             const float2 v0 = pg_unpack<BF16>(vw.x), v1 = pg_unpack<BF16>(vw.y);
             l = l * old + w;
-            o[0] = o[0] * old + w * (v0.x * unit);
-            o[1] = o[1] * old + w * (v0.y * unit);
-            o[2] = o[2] * old + w * (v1.x * unit);
-            o[3] = o[3] * old + w * (v1.y * unit);
-            if constexpr (BF16) {
-                if (unit == 1.f && fmaxf(fmaxf(fabsf(o[0]), fabsf(o[1])), fmaxf(fabsf(o[2]), fabsf(o[3]))) > 0x1p100f) {
-                    unit = 0x1p-64f;
+            const float v[4] = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) o[c] *= unit;
+            for (int c = 0; c < 4; ++c) {
+                o[c] = o[c] * old + w * (v[c] * unit[c]);
+                if (BF16 && unit[c] == 1.f && fabsf(o[c]) > 0x1p100f) {
+                    unit[c] = 0x1p-64f;
+                    o[c] *= unit[c];
                 }
             }
             m = mn;
@@ -147,10 +146,13 @@ __device__ __noinline__ void paged_row(const PagedAttnArgs& a, int r, const Page
     const bool none = bad || l == 0.f;
     const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = none ? 0.f : o[c] * inv * (unit == 1.f ? 1.f : 0x1p64f);
-    const size_t place = row * a.Hq + head;
+    for (int c = 0; c < 4; ++c) o[c] = none ? 0.f : o[c] * inv * (unit[c] == 1.f ? 1.f : 0x1p64f);
     if (!mine) return;
-    *reinterpret_cast<uint2*>(a.out + place * PG_ROW + lane * 8) = make_uint2(pg_pack_out<BF16>(o[0], o[1]), pg_pack_out<BF16>(o[2], o[3]));
+    uint2* const out = reinterpret_cast<uint2*>(a.out + (row * a.Hq + head) * PG_ROW + lane * 8);
+    const uint2 first = *out;
+    const float2 f0 = pg_unpack<BF16>(first.x), f1 = pg_unpack<BF16>(first.y);
+    *out = make_uint2(pg_pack_out<BF16>(pg_finite(f0.x) ? f0.x : o[0], pg_finite(f0.y) ? f0.y : o[1]),
+                      pg_pack_out<BF16>(pg_finite(f1.x) ? f1.x : o[2], pg_finite(f1.y) ? f1.y : o[3]));
 }
 
 }  // namespace clo

@@ -240,6 +240,31 @@ def test_large_bf16_values(T, n, G, num_ctas):
         check_wide(out[:-1, :, 9:10], None, (want[0][:-1, :, 9:10], None, want[2][:-1, :, 9:10], want[3][:-1]), T)
 
 
+@pytest.mark.parametrize("T,n,G,num_ctas", [(40, 40, 1, 0), (333, 50, 4, 1), (9000, 3, 4, 0), (3000, 100, 8, 0)])
+def test_large_bf16_values_beside_small_ones(T, n, G, num_ctas):
+    """Channels of 2^-100 between channels of 2^125: those keep the bits that they have beside
+    values of usual size, also where the rows are made anew."""
+    dtype = torch.bfloat16
+    kc, vc, table = ref.make_cache([T], 2, dtype, 73)
+    q = queries(n, 2 * G, dtype, 74)
+    small = [c for c in range(ref.D) if c % 4 != 1]
+    vc[..., small] *= 2.0 ** -100
+    plain, lse0, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0
+    vc[..., 1::4] *= 2.0 ** 125
+    out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+    assert err == 0 and torch.equal(out[..., small], plain[..., small]) and torch.equal(lse, lse0)
+    want = ref.chunk_attention(q, kc, vc, table, [T], [n])
+    check_wide(out[..., 1::4], lse, (want[0][..., 1::4], want[1], want[2][..., 1::4], want[3]), T)
+    if T > 1:  # a V that most rows do not see, in a small channel
+        vc[table[0, (T - 1) // 16].long(), :, (T - 1) % 16, 2] = math.nan
+        out, lse, err = chunk(q, kc, vc, table, [T], [n], num_ctas)
+        assert err == 0 and torch.isnan(out[-1, :, 2]).all()
+        others = [c for c in small if c != 2]
+        assert torch.equal(out[..., others], plain[..., others]) and torch.equal(lse, lse0)
+        check_wide(out[:-1], lse[:-1], tuple(x[:-1] for x in want), T)
+
+
 @pytest.mark.parametrize("num_ctas", [0, 5])
 def test_large_bf16_values_of_some_requests(num_ctas):
     """Among many requests, in a cache whose heads lie side by side, captured and replayed: the
