@@ -7,7 +7,7 @@ import torch
 import offloaded_kv_decode_gb300 as clo
 import paged_ref as ref
 from test_paged16_attention_gpu import chunk, offsets_of, queries, sparse, sparse_ref
-from test_paged16_cache_gpu import rand, random_bounds, select
+from test_paged16_cache_gpu import check_select, rand, random_bounds, select
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float16, torch.bfloat16]
@@ -39,6 +39,12 @@ def test_first_and_last_blocks_come_before_those_without_a_score(n_first, n_last
     for h in range(Hkv):
         assert sel[0, h].tolist() == want
         assert sel[1, h].tolist() == ([0, 1] + [-1] * n_sel)[:n_sel] if n_sel > 1 else [1]
+
+
+@pytest.mark.parametrize("Hkv", [1, 8, 9, 32])
+def test_select_for_any_number_of_heads(Hkv):
+    """Up to eight heads share a CTA's records, and more take several; after calls with fewer."""
+    check_select([500, 30, 0, 777], 2, Hkv, 12, 1, 2, torch.bfloat16, Hkv)
 
 
 # ---------------------------------------------------------------- short contexts
